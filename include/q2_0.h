@@ -48,7 +48,7 @@ typedef enum {
     Q2_0_OK = 0,
     Q2_0_ERR_NULL = 1,        /* a required pointer is NULL */
     Q2_0_ERR_SHAPE = 2,       /* K <= 0, K % 64 != 0, a negative size, or a size beyond the limits */
-    Q2_0_ERR_LAYOUT = 3,      /* ldx < K, ldy < M or ld_out < K */
+    Q2_0_ERR_LAYOUT = 3,      /* ldx < K, ldy < M or ld_out < K, or a stride a call does not take */
     Q2_0_ERR_ALIGN = 4,       /* w not 2-byte aligned, or x / y / out / ids not aligned to their element size */
     Q2_0_ERR_UNSUPPORTED = 5, /* N > 8 for the mat-vec, or an unknown precision or activation type */
     Q2_0_ERR_WORKSPACE = 6,   /* workspace smaller than q2_0_mul_mat_workspace_bytes(), or not 16-byte aligned */
@@ -357,6 +357,148 @@ int q2_0_quantize(const float *src, int64_t M, int64_t K, int64_t ld_src, void *
  * Errors: SHAPE (also K % 128 != 0), the M == 0 no-op, NULL, ALIGN.
  */
 int q2_0_repack_g128(const void *w128, int64_t M, int64_t K, void *w, void *stream);
+
+/*
+ * ---- Decoder-step operators around the products: position rotation and paged cache
+ * append, shared-prefix attention, expert choice and the expert layer.
+ *
+ * A paged key/value cache.  Keys and values live in two pools of n_pages pages; a page
+ * holds page_size token rows of head_dim elements for each of n_kv key heads, row
+ * (page, head, token) at element page*page_stride + head*head_stride +
+ * token*token_stride of its pool (so [page][head][token][dim] and
+ * [page][token][head][dim] are both strides of one layout).
+ *   k, v   : device pools, 16-byte aligned, of element type `type` (Q2_0_ACT_F16 or
+ *            Q2_0_ACT_BF16); strides are in elements, positive multiples of 8, and
+ *            rows must not overlap; token_stride <= 2^24.
+ *   head_dim: 64, 128 or 256 (UNSUPPORTED otherwise); page_size >= 1, any.
+ * A page table is n_seqs rows of table_len int32 page numbers, row s at table + s*ld_table:
+ * token i of sequence s is row i % page_size of page table[s][i / page_size].
+ */
+typedef struct {
+    void *k, *v;
+    int type;
+    int64_t n_pages, page_size, n_kv, head_dim;
+    int64_t page_stride, head_stride, token_stride;
+} q2_0_kv_cache;
+
+/* Which elements of a head turn together (see q2_0_kv_append). */
+typedef enum {
+    Q2_0_ROPE_HALF = 0,    /* element i with element i + rot_dim/2 */
+    Q2_0_ROPE_PAIRS = 1    /* element 2i with element 2i + 1 */
+} q2_0_rope_style;
+
+/*
+ * kv_append: rotate q and k by their positions and store k and v in the cache, one
+ * launch.  Token t belongs to sequence seq[t] and has position pos[t], which is both
+ * its row of the rotation table and its place in the sequence's pages.
+ *   table  : DEVICE page table (above), 4-byte aligned, ld_table >= table_len.
+ *   seq, pos : DEVICE int32 [n_tokens], 4-byte aligned.
+ *   q      : n_tokens rows of n_q*head_dim elements of x_type at q + t*ldq (NULL with
+ *            n_q = 0: only k and v); k, v: n_tokens rows of n_kv*head_dim elements --
+ *            the rows the q, k and v products write.
+ *   rope   : f32 [n_pos][rot_dim]: cos of the rot_dim/2 angles of a position, then their
+ *            sin (so any frequency scaling is the caller's); rot_dim is even and at most
+ *            head_dim; elements rot_dim.. of a head pass unrotated.  rot_dim = 0 (rope
+ *            may be NULL): no rotation.
+ *   q_out  : n_tokens rows of n_q*head_dim elements of the cache's type at
+ *            q_out + t*ldqo; must not overlap an input.
+ * A turned pair (a, b) becomes (a cos - b sin, b cos + a sin) in f32, rounded once to the
+ * cache's type.  A position outside [0, n_pos) turns its pairs into NaN.  A token whose
+ * seq is outside [0, n_seqs), whose position is negative or beyond its table row, or whose
+ * page is outside [0, n_pages) is not stored (its q row is still written): mark padding
+ * with seq = -1.  Two tokens of one call must not share a cache row.
+ * Errors: SHAPE (also n_pos beyond 2^31 - 1 and rot_dim odd, negative or > head_dim), the
+ * n_tokens == 0 no-op, NULL, LAYOUT, UNSUPPORTED (x_type, cache type, head_dim, style),
+ * ALIGN.
+ */
+int q2_0_kv_append(const q2_0_kv_cache *cache, const int32_t *table, int64_t n_seqs, int64_t table_len,
+                   int64_t ld_table, const int32_t *seq, const int32_t *pos, int64_t n_tokens, const void *q,
+                   int64_t ldq, int64_t n_q, const void *k, int64_t ldk, const void *v, int64_t ldv, int x_type,
+                   const float *rope, int64_t n_pos, int64_t rot_dim, int style, void *q_out, int64_t ldqo,
+                   void *stream);
+
+/*
+ * attn_shared: attention of n_qt query tokens of each of n_seqs sequences over the paged
+ * cache; the sequences share their first prefix_len tokens, which are read once for the
+ * whole batch (prefix_len = 0: nothing is shared).
+ *   q      : row s*n_qt + j (query token j of sequence s) of n_q*head_dim elements of the
+ *            cache's type at q + row*ldq; n_q is a multiple of n_kv, head h reads key
+ *            head h / (n_q/n_kv).  1 <= n_qt <= Q2_0_ATTN_MAX_QT.
+ *   table  : DEVICE page table.  Keys below prefix_len are read through row 0, the others
+ *            through their sequence's row.
+ *   lens   : DEVICE int32 [n_seqs]: tokens of each sequence, the prefix and its own query
+ *            tokens included, so query j of sequence s sees keys i < lens[s] - n_qt + 1 + j.
+ *   max_len: bound on lens (host), prefix_len <= max_len <= table_len*page_size; it only
+ *            sets how the work is split.
+ *   scale  : finite and positive; scores are scale * (q . k).
+ *   out    : rows as q's, element type of the cache, at out + row*ldo.
+ * The result is sum_i softmax_i(score) v_i, softmax statistics and sums in f32; the softmax
+ * weights are rounded to the cache's type for the matrix cores (relative 2^-8 for BF16 at most,
+ * 2^-11 for F16, each key by itself), the result once more.  A query that sees no key (or only
+ * scores of -inf) gives zeros.  Keys and values that a query does not see are never part
+ * of its result, whatever they hold (NaN and inf included).  lens[s] outside
+ * [0, max_len], or a page outside [0, n_pages) among the keys a query sees, gives NaN
+ * and reads nothing out of bounds.  Results are deterministic run to run.
+ *   workspace / ws_bytes: at least q2_0_attn_shared_workspace_bytes() bytes, 16-byte aligned
+ *            (may be 0): partial results of the splits of the key axis.  Overwritten.
+ * Errors: SHAPE (also n_q not a multiple of n_kv, n_qt outside [1, 16], a bad max_len or
+ * prefix_len, scale), the no-op for n_seqs == 0 or n_q == 0, NULL, LAYOUT, UNSUPPORTED,
+ * ALIGN (q, out and the cache 16-byte aligned, strides multiples of 8: LAYOUT),
+ * WORKSPACE.
+ */
+#define Q2_0_ATTN_MAX_QT 16
+int q2_0_attn_shared(const q2_0_kv_cache *cache, const int32_t *table, int64_t n_seqs, int64_t table_len,
+                     int64_t ld_table, const int32_t *lens, int64_t prefix_len, int64_t max_len, const void *q,
+                     int64_t ldq, int64_t n_q, int64_t n_qt, float scale, void *out, int64_t ldo, void *workspace,
+                     size_t ws_bytes, void *stream);
+
+/* Workspace bytes q2_0_attn_shared needs (0 when none, and for invalid sizes). */
+size_t q2_0_attn_shared_workspace_bytes(int64_t n_seqs, int64_t n_q, int64_t n_kv, int64_t head_dim, int64_t n_qt,
+                                        int64_t prefix_len, int64_t max_len);
+
+/*
+ * moe_route: choose experts from router logits.
+ *   logits : n_tokens rows of n_expert values of element type x_type at logits + t*ld.
+ *   ids    : int32 [n_tokens][n_used]: the n_used largest logits of a token, largest first,
+ *            the lower index first among equals (-0 equals +0; NaN comes after -inf).
+ *   weights: f32 [n_tokens][n_used]: exp(logit - max) over its sum, the sum taken over the
+ *            chosen (normalise != 0) or over all experts (0); f32 throughout.  A token whose
+ *            logits are all -inf gets weights 0.
+ * 1 <= n_used <= min(n_expert, 64), n_expert <= 8192: SHAPE otherwise.  Errors: SHAPE, the
+ * n_tokens == 0 no-op, NULL, LAYOUT (ld < n_expert), UNSUPPORTED (x_type), ALIGN.
+ */
+int q2_0_moe_route(const void *logits, int x_type, int64_t ld, int64_t n_tokens, int64_t n_expert, int64_t n_used,
+                   int normalise, int32_t *ids, float *weights, void *stream);
+
+/*
+ * moe_layer: a whole expert layer for few tokens,
+ *     y[t] = sum_u weights[t][u] * W_down,e ( silu(W_gate,e x[t]) * (W_up,e x[t]) ),  e = ids[t][u],
+ * with silu(a) = a / (1 + exp(-a)).
+ *   w_gate, w_up : n_expert n_ff x K matrices back to back, w_down: n_expert K x n_ff
+ *             matrices (K and n_ff positive multiples of 64), 2-byte aligned.
+ *   x       : n_tokens rows of K elements of x_type at x + t*ldx.
+ *   ids, weights : DEVICE [n_tokens][n_used], as q2_0_moe_route writes them; ids may repeat.
+ *             An id outside [0, n_expert) makes its token's y NaN and reads nothing.
+ *   y       : f32 row t of K elements at y + t*ldy, overwritten.
+ * n_tokens <= Q2_0_MOE_LAYER_MAX_TOKENS and n_used <= 32, UNSUPPORTED otherwise (use
+ * q2_0_mul_mat_id).
+ * Accuracy: all three products are fp32-grade, as q2_0_mul_mat_vec's (x and the
+ * hidden activation enter the matrix cores as fp16 hi/lo pairs under its range
+ * condition); sums over the experts are f32.  Deterministic run to run.
+ *   workspace / ws_bytes: at least q2_0_moe_layer_workspace_bytes() bytes, 16-byte
+ *             aligned: the hidden activations and the experts' partial results.
+ * Errors: SHAPE (also n_expert < 1 or > 8192), the no-op for n_tokens == 0, NULL, LAYOUT,
+ * UNSUPPORTED, ALIGN, WORKSPACE.  n_used == 0 writes zeros.
+ */
+#define Q2_0_MOE_LAYER_MAX_TOKENS 64
+#define Q2_0_MOE_LAYER_MAX_USED 32
+int q2_0_moe_layer(const void *w_gate, const void *w_up, const void *w_down, int64_t n_expert, int64_t n_ff,
+                   int64_t K, const void *x, int x_type, int64_t ldx, const int32_t *ids, const float *weights,
+                   int64_t n_used, int64_t n_tokens, float *y, int64_t ldy, void *workspace, size_t ws_bytes,
+                   void *stream);
+
+/* Workspace bytes q2_0_moe_layer needs (0 for invalid sizes). */
+size_t q2_0_moe_layer_workspace_bytes(int64_t n_ff, int64_t K, int64_t n_used, int64_t n_tokens);
 
 /* A static, human-readable name for a status code. */
 const char *q2_0_status_string(int status);

@@ -1,0 +1,499 @@
+// Attention of a batch over a paged cache, the prefix that the sequences share read once.
+//
+//   o[r] = sum_i p_ri v_i / sum_i p_ri,   p_ri = 2^(c q_r.k_i - m_r),   c = scale log2 e
+//
+// The softmax is one pass: a wave keeps a reference exponent m_r, the sum l_r and the
+// unnormalised O_r (f32) of its rows; two results over different keys join as
+// l = l1 2^(m1-m) + l2 2^(m2-m), O likewise, with m = max(m1, m2).
+//
+// Rows.  A key head's rows are (query token, query head of its group).  In the prefix part
+// the rows of all sequences stand together (the keys are read once for all of them), in the
+// own part those of one sequence.  A wave carries RT tiles of 16 rows.
+//
+// Keys.  A wave takes 32 keys at a time straight from the cache into the matrix cores'
+// operands, without LDS:
+//  * S^T = K Q^T (v_mfma 16x16x32): A = 16 keys x 32 dims, 16 bytes a lane, as they lie in
+//    the cache; B = Q^T, loaded once.  D: lane (row j = lane%16, g = lane/16) holds the
+//    scores of keys 4g..4g+3 of each 16-key half for row j.
+//  * O^T += V^T P^T: B = P^T needs, in lane (j, g), 8 keys of row j: exactly the two
+//    halves' scores of that lane, rounded.  A = V^T takes the same 8 keys {4g+i, 16+4g+i} of
+//    dims d = DPL*c + e (c = lane%16, one MFMA per e): a lane loads DPL consecutive dims
+//    of those 8 value rows (full rows across the 16 lanes) and pairs keys up with one
+//    v_perm_b32 a dword.
+// So a score never leaves its lane: no lane exchange per step.  The reference m_r is only
+// raised when some score passes it by 2^8 (a ballot decides), and the sum of a row stays
+// spread over its four lanes until the end; f32 has room for terms up to 2^8 and the 16-bit
+// P for them too.
+//
+// Masks.  A row sees keys below its limit.  Scores past it become -inf before the maximum;
+// keys some row of the wave does not see are multiplied once per distinct limit, with
+// the value rows past that limit zeroed, so that what lies in unseen places (NaN, inf)
+// reaches no row that does not see it.  Addresses are clamped to seen keys.
+//
+// Split.  The 4 waves of a workgroup interleave the key tiles of one split; their results
+// join in LDS, the splits' in attn_join.
+#include <type_traits>
+
+#include "layer_common.h"
+
+namespace q2_0 {
+
+typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
+
+template <typename CT>
+struct Mma;
+template <>
+struct Mma<_Float16> {
+    static __device__ __forceinline__ float4_t mul(u32x4_t a, u32x4_t b, float4_t c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c,
+                                                      0, 0, 0);
+    }
+};
+template <>
+struct Mma<bf16_t> {
+    static __device__ __forceinline__ float4_t mul(u32x4_t a, u32x4_t b, float4_t c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8_t, a), __builtin_bit_cast(bf8_t, b), c, 0,
+                                                       0, 0);
+    }
+};
+
+constexpr int kAttnWaves = 4;
+constexpr int kAttnTile = 32;    // keys per step
+
+// N dwords from 4-byte aligned memory (8 or 16 bytes aligned as N goes)
+template <int N>
+__device__ __forceinline__ void load_dwords(const uint8_t *p, uint32_t *v) {
+    if constexpr (N == 2) {
+        const u32x2_t t = *reinterpret_cast<const u32x2_t *>(p);
+        v[0] = t.x, v[1] = t.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const u32x4_t t = *reinterpret_cast<const u32x4_t *>(p + 4 * i);
+            v[i] = t.x, v[i + 1] = t.y, v[i + 2] = t.z, v[i + 3] = t.w;
+        }
+    }
+}
+
+// P16: page_size % 16 == 0, so that the 16 keys of a half tile lie in one page and its page
+// number is read once for the wave; otherwise 32 lanes look up a key each and pass the rows
+// round through LDS.
+template <typename CT, int D, int RT, bool P16>
+__global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_rows(AttnShared a) {
+    constexpr int KS = D / 32;       // 32-dim steps of a score
+    constexpr int DPL = D / 16;      // dims per lane of a value row
+    constexpr int VD = DPL / 2;      // dwords of those
+    constexpr int OS = D + 4;        // LDS floats per row
+
+    __shared__ __attribute__((aligned(16))) float lds_o[kAttnWaves][RT * 16][OS];
+    __shared__ float lds_m[kAttnWaves][RT * 16], lds_l[kAttnWaves][RT * 16];
+    __shared__ int64_t lds_row[P16 ? 1 : kAttnWaves][P16 ? 1 : kAttnTile];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int j = lane & 15, g = lane >> 4;
+
+    // this workgroup's part: prefix (all sequences' rows) or one sequence's own keys
+    const bool pre = (int)blockIdx.x < a.wgs_p;
+    int u = pre ? (int)blockIdx.x : (int)blockIdx.x - a.wgs_p;
+    const int groups = pre ? a.groups_p : a.groups_o, splits = pre ? a.splits_p : a.splits_o;
+    const int nrows = pre ? a.rows_p : a.rows_o;
+    const int rg = u % groups;
+    u /= groups;
+    const int kvh = u % a.n_kv;
+    u /= a.n_kv;
+    const int split = u % splits;
+    const int seq = pre ? 0 : u / splits;
+    const int r0 = rg * RT * 16;
+    const int nrt = min(RT, (nrows - r0 + 15) / 16);
+    const int tok0 = seq * a.n_qt;
+
+    // a row's query (token, head) and the keys it sees
+    const int grp = (int)a.group.d;
+    const auto row_token = [&](int r) { return tok0 + a.group.div((uint32_t)r); };
+    const auto row_limit = [&](int r) {
+        if (r >= nrows) return 0;
+        const int t = row_token(r);
+        const int s = t / a.n_qt;
+        const int len = a.lens[s];
+        if (len < 0 || len > a.max_len) return 0;
+        const int lim = len - a.n_qt + 1 + (t - s * a.n_qt);
+        return max(0, pre ? min(lim, a.prefix_len) : lim);
+    };
+    int lim[RT];
+    int lim_lo = 0x7fffffff, lim_hi = 0;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int r = r0 + 16 * t + j;
+        lim[t] = t < nrt ? row_limit(r) : 0;
+        if (t < nrt && r < nrows) {
+            lim_lo = min(lim_lo, lim[t]);
+            lim_hi = max(lim_hi, lim[t]);
+        }
+    }
+#pragma unroll
+    for (int off = 1; off < 16; off <<= 1) {
+        lim_lo = min(lim_lo, __shfl_xor(lim_lo, off));
+        lim_hi = max(lim_hi, __shfl_xor(lim_hi, off));
+    }
+    lim_lo = __builtin_amdgcn_readfirstlane(lim_lo);
+    lim_hi = __builtin_amdgcn_readfirstlane(lim_hi);
+
+    // key tiles of this split: tiles [ta, tb) of the part's keys [k_lo, lim_hi)
+    const int k_lo = pre ? 0 : a.prefix_len;
+    const int t_first = k_lo / kAttnTile;
+    const int t_end = lim_hi > k_lo ? (lim_hi + kAttnTile - 1) / kAttnTile : t_first;
+    const int ntile = t_end - t_first;
+    const int per = (ntile + splits - 1) / splits;
+    const int ta = t_first + min(ntile, per * split), tb = t_first + min(ntile, per * (split + 1));
+
+    // queries as the scores' B operand
+    u32x4_t qv[RT][KS];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int r = r0 + 16 * t + j;
+        const bool in = t < nrt && r < nrows;
+        const int tok = in ? row_token(r) : 0;
+        const int head = kvh * grp + (in ? r - (tok - tok0) * grp : 0);
+        const uint8_t *qp = static_cast<const uint8_t *>(a.q) + 2 * ((int64_t)tok * a.ldq + (int64_t)head * D + 8 * g);
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+            qv[t][k] = in ? *reinterpret_cast<const u32x4_t *>(qp + 64 * k) : u32x4_t{0u, 0u, 0u, 0u};
+    }
+
+    float4_t o[RT][DPL];
+    float m[RT], ms[RT], l[RT];   // reference (-inf: none yet), the same as a number, sum of this lane
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        m[t] = -__builtin_inff();
+        ms[t] = 0.f;
+        l[t] = 0.f;
+#pragma unroll
+        for (int e = 0; e < DPL; ++e) o[t][e] = float4_t{0.f, 0.f, 0.f, 0.f};
+    }
+
+    const int32_t *trow = a.table + (pre ? 0 : (int64_t)seq * a.ld_table);
+    const uint8_t *kbase = static_cast<const uint8_t *>(a.kc) + 2 * (int64_t)kvh * a.head_stride;
+    const uint8_t *vbase = static_cast<const uint8_t *>(a.vc) + 2 * (int64_t)kvh * a.head_stride;
+    const int ts = (int)a.token_stride;
+    const int psz = (int)a.page.d;
+
+    u32x4_t kv[2][KS];
+    uint32_t vv[8][VD];
+    uint32_t bad = 0;        // keys of the loaded tile whose page does not exist
+
+    // element offset of key's row, and whether its page exists
+    const auto key_row = [&](int key, bool &ok) {
+        const int pi = a.page.div((uint32_t)key);
+        const int page = trow[pi];
+        ok = page >= 0 && page < a.n_pages;
+        return (int64_t)(ok ? page : 0) * a.page_stride + (int64_t)(key - pi * psz) * a.token_stride;
+    };
+    const auto load_tile = [&](int tile) {
+        const int key0 = tile * kAttnTile;
+        if constexpr (P16) {
+            bad = 0;
+            int64_t base[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                // a half past the last seen key reads the first half again (it is masked)
+                const int kk = key0 + 16 * h < lim_hi ? key0 + 16 * h : key0;
+                bool ok;
+                base[h] = 2 * key_row(kk, ok);
+                if (!ok) bad |= 0xffffu << (16 * h);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+                    kv[h][k] = *reinterpret_cast<const u32x4_t *>(kbase + base[h] + (2 * (j * ts + 8 * g) + 64 * k));
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                load_dwords<VD>(vbase + base[i / 4] + 2 * ((4 * g + i % 4) * ts + DPL * j), vv[i]);
+        } else {
+            const int key = min(max(key0 + (lane & 31), k_lo), lim_hi - 1);
+            bool ok;
+            const int64_t row = 2 * key_row(key, ok);
+            bad = (uint32_t)__ballot(!ok);
+            if (lane < kAttnTile) lds_row[wave][lane] = row;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t b = lds_row[wave][16 * h + j];
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+                    kv[h][k] = *reinterpret_cast<const u32x4_t *>(kbase + b + (16 * g + 64 * k));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                load_dwords<VD>(vbase + lds_row[wave][16 * (i / 4) + 4 * g + i % 4] + 2 * DPL * j, vv[i]);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+    };
+    // the value tile's operand of dim e: its 8 keys' halves
+    const auto v_operand = [&](int e) {
+        const uint32_t sel = (e & 1) ? 0x07060302u : 0x05040100u;
+        u32x4_t r;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) r[p] = __builtin_amdgcn_perm(vv[2 * p + 1][e / 2], vv[2 * p][e / 2], sel);
+        return r;
+    };
+
+    for (int tile = ta + wave; tile < tb; tile += kAttnWaves) {
+        load_tile(tile);
+        const int key0 = tile * kAttnTile;
+        const bool edge = key0 < k_lo || key0 + kAttnTile > lim_lo || bad != 0;   // some score needs a mask
+        u32x4_t p[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            if (t >= nrt) break;
+            float4_t s[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                s[h] = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < KS; ++k) s[h] = Mma<CT>::mul(kv[h][k], qv[t][k], s[h]);
+            }
+            if (edge) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int kk = 16 * h + 4 * g + i;
+                        if ((bad >> kk) & 1u) s[h][i] = __builtin_nanf("");
+                        if (key0 + kk >= lim[t] || key0 + kk < k_lo) s[h][i] = -__builtin_inff();
+                    }
+            }
+            const float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                                    fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3]))) *
+                              a.scale2;
+            if (__ballot(top > m[t] + 8.f)) {
+                // raise the rows' references to their maxima so far and rescale what they hold
+                float mx = fmaxf(m[t], top);
+                mx = fmaxf(mx, __shfl_xor(mx, 16));
+                mx = fmaxf(mx, __shfl_xor(mx, 32));
+                const float mn = mx == -__builtin_inff() ? 0.f : mx;
+                const float f = m[t] == mx ? 1.f : __builtin_amdgcn_exp2f(m[t] - mn);
+                m[t] = mx;
+                ms[t] = mn;
+                l[t] *= f;
+#pragma unroll
+                for (int e = 0; e < DPL; ++e)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[t][e][i] *= f;
+            }
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 4][i % 4], a.scale2, -ms[t]));
+                l[t] += w[i];
+            }
+            p[t] = u32x4_t{pack2<CT>(w[0], w[1]), pack2<CT>(w[2], w[3]), pack2<CT>(w[4], w[5]), pack2<CT>(w[6], w[7])};
+        }
+        if (!edge) {
+#pragma unroll
+            for (int e = 0; e < DPL; ++e) {
+                const u32x4_t va = v_operand(e);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    if (t >= nrt) break;
+                    o[t][e] = Mma<CT>::mul(va, p[t], o[t][e]);
+                }
+            }
+        } else {
+            // once per distinct limit, lowest first, with value rows at or past it zeroed; only
+            // rows of that limit take the result
+            int done = -1;
+            while (true) {
+                int cur = 0x7fffffff;
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+                    if (t < nrt && lim[t] > done) cur = min(cur, lim[t]);
+#pragma unroll
+                for (int off = 1; off < 16; off <<= 1) cur = min(cur, __shfl_xor(cur, off));
+                cur = __builtin_amdgcn_readfirstlane(cur);
+                if (cur == 0x7fffffff) break;
+                done = cur;
+                if (cur <= key0) continue;      // these rows see nothing here
+                uint32_t keep[4];               // per pair of keys: which halves stay
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int k0 = key0 + 16 * (q / 2) + 4 * g + 2 * (q % 2);
+                    keep[q] = (k0 < cur && k0 >= k_lo ? 0xffffu : 0u) | (k0 + 1 < cur && k0 + 1 >= k_lo ? 0xffff0000u : 0u);
+                }
+#pragma unroll
+                for (int e = 0; e < DPL; ++e) {
+                    u32x4_t va = v_operand(e);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) va[q] &= keep[q];
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) {
+                        if (t >= nrt) break;
+                        // (a selected result, not a zeroed P: 0 * NaN would reach the other rows)
+                        const float4_t r = Mma<CT>::mul(va, p[t], o[t][e]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[t][e][i] = lim[t] == cur ? r[i] : o[t][e][i];
+                    }
+                }
+            }
+        }
+    }
+
+    // join the four waves' results
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        if (t >= nrt) break;
+        float lt = l[t];
+        lt += __shfl_xor(lt, 16);
+        lt += __shfl_xor(lt, 32);
+        if (g == 0) {
+            lds_m[wave][16 * t + j] = m[t];
+            lds_l[wave][16 * t + j] = lt;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < DPL; ++e) lds_o[wave][16 * t + j][DPL * (4 * g + i) + e] = o[t][e][i];
+    }
+    __syncthreads();
+    const int rows_here = min(nrows - r0, RT * 16);
+    const int nsplit = a.splits_p + a.splits_o;
+    const int sidx = pre ? split : a.splits_p + split;
+    const int64_t n_out = (int64_t)a.n_seqs * a.n_qt * a.n_q;
+    for (int x = tid; x < rows_here * (D / 4); x += 256) {
+        const int r = x / (D / 4), d = 4 * (x % (D / 4));
+        float mm = -__builtin_inff();
+#pragma unroll
+        for (int w = 0; w < kAttnWaves; ++w) mm = fmaxf(mm, lds_m[w][r]);
+        const float mb = mm == -__builtin_inff() ? 0.f : mm;
+        float ll = 0.f;
+        float4_t oo = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kAttnWaves; ++w) {
+            const float f = __builtin_amdgcn_exp2f(lds_m[w][r] - mb);
+            ll += f * lds_l[w][r];
+            const float4_t v = *reinterpret_cast<const float4_t *>(&lds_o[w][r][d]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) oo[i] += f * v[i];
+        }
+        const int tok = row_token(r0 + r);
+        const int head = kvh * grp + (r0 + r - (tok - tok0) * grp);
+        if (nsplit == 1) {
+            const int len = a.lens[tok / a.n_qt];
+            const float nv = len < 0 || len > a.max_len ? __builtin_nanf("") : 0.f;
+            const float inv = 1.f / ll;
+            float4_t res;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) res[i] = ll == 0.f ? nv : oo[i] * inv;
+            CT *op = static_cast<CT *>(a.out) + (int64_t)tok * a.ldo + (int64_t)head * D + d;
+            *reinterpret_cast<u32x2_t *>(op) = u32x2_t{pack2<CT>(res[0], res[1]), pack2<CT>(res[2], res[3])};
+        } else {
+            const int64_t row = sidx * n_out + (int64_t)tok * a.n_q + head;
+            *reinterpret_cast<float4_t *>(a.part_o + row * D + d) = oo;
+            if (d == 0) *reinterpret_cast<float2_t *>(a.part_ml + 2 * row) = float2_t{mm, ll};
+        }
+    }
+}
+
+// Joins the splits of a row: a wave per row.
+template <typename CT, int D>
+__global__ __launch_bounds__(256) void attn_join(AttnShared a) {
+    constexpr int PER = D / 64;
+    const int lane = threadIdx.x & 63;
+    const int64_t n_out = (int64_t)a.n_seqs * a.n_qt * a.n_q;
+    const int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (row >= n_out) return;
+    const int nsplit = a.splits_p + a.splits_o;
+    float mm = -__builtin_inff();
+    for (int s = 0; s < nsplit; ++s) mm = fmaxf(mm, a.part_ml[2 * (s * n_out + row)]);
+    const float mb = mm == -__builtin_inff() ? 0.f : mm;
+    float ll = 0.f, oo[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) oo[i] = 0.f;
+    for (int s = 0; s < nsplit; ++s) {
+        const int64_t at = s * n_out + row;
+        const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - mb);
+        ll += f * a.part_ml[2 * at + 1];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) oo[i] += f * a.part_o[at * D + lane * PER + i];
+    }
+    const int64_t tok = row / a.n_q;
+    const int head = (int)(row - tok * a.n_q);
+    const int len = a.lens[tok / a.n_qt];
+    const float nv = len < 0 || len > a.max_len ? __builtin_nanf("") : 0.f;
+    const float inv = 1.f / ll;
+    CT *op = static_cast<CT *>(a.out) + tok * a.ldo + (int64_t)head * D + lane * PER;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) op[i] = to_elem<CT>(ll == 0.f ? nv : oo[i] * inv);
+}
+
+AttnPlan attn_plan(int64_t n_seqs, int64_t n_q, int64_t n_kv, int64_t dim, int64_t n_qt, int64_t prefix_len,
+                   int64_t max_len) {
+    AttnPlan p;
+    const int64_t rows_o = n_qt * (n_q / n_kv), rows_p = n_seqs * rows_o;
+    const int64_t most = prefix_len > 0 ? rows_p : rows_o;
+    p.row_tiles = most <= 16 || dim == 256 ? 1 : (dim == 128 ? 2 : 4);
+    const int64_t rpg = 16 * p.row_tiles;
+    const auto splits = [](int64_t units, int64_t tiles) {
+        // enough workgroups for the chip, but at least a tile for each of a workgroup's waves
+        int64_t s = (512 + units - 1) / units;
+        if (s > (tiles + kAttnWaves - 1) / kAttnWaves) s = (tiles + kAttnWaves - 1) / kAttnWaves;
+        if (s > 128) s = 128;
+        return s < 1 ? (int64_t)1 : s;
+    };
+    p.groups_p = (int)((rows_p + rpg - 1) / rpg);
+    p.groups_o = (int)((rows_o + rpg - 1) / rpg);
+    p.splits_p = p.splits_o = 0;
+    if (prefix_len > 0) p.splits_p = (int)splits(p.groups_p * n_kv, (prefix_len + kAttnTile - 1) / kAttnTile);
+    if (max_len > prefix_len)
+        p.splits_o = (int)splits(n_seqs * p.groups_o * n_kv, (max_len + kAttnTile - 1) / kAttnTile - prefix_len / kAttnTile);
+    const int64_t n = p.splits_p + p.splits_o;
+    p.ws_bytes = n <= 1 ? 0 : (size_t)(n * n_seqs * n_qt * n_q) * (size_t)(dim + 2) * 4;
+    return p;
+}
+
+hipError_t launch_attn_shared(AttnShared a, const AttnPlan &p, Act ct, int dim, hipStream_t s) {
+    a.groups_p = p.groups_p;
+    a.groups_o = p.groups_o;
+    a.splits_p = p.splits_p;
+    a.splits_o = p.splits_o;
+    a.rows_o = a.n_qt * (int)a.group.d;
+    a.rows_p = a.n_seqs * a.rows_o;
+    const int64_t wgs_p = (int64_t)a.groups_p * a.n_kv * a.splits_p;
+    const int64_t wgs_o = (int64_t)a.groups_o * a.n_kv * a.splits_o * a.n_seqs;
+    a.wgs_p = (int)wgs_p;
+    const int64_t n_out = (int64_t)a.n_seqs * a.n_qt * a.n_q;
+    const int nsplit = a.splits_p + a.splits_o;
+    a.part_ml = a.part_o + nsplit * n_out * dim;
+    const dim3 grid((unsigned)(wgs_p + wgs_o));
+    const bool p16 = a.page.d % 16 == 0;
+    auto run = [&](auto ctag, auto d, auto rt) -> hipError_t {
+        using CT = decltype(ctag);
+        constexpr int D = decltype(d)::value, RT = decltype(rt)::value;
+        if (grid.x) {
+            if (p16) attn_rows<CT, D, RT, true><<<grid, 256, 0, s>>>(a);
+            else attn_rows<CT, D, RT, false><<<grid, 256, 0, s>>>(a);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        if (nsplit != 1) {
+            attn_join<CT, D><<<dim3((unsigned)((n_out + 3) / 4)), 256, 0, s>>>(a);
+            return hipGetLastError();
+        }
+        return hipSuccess;
+    };
+    auto by_rt = [&](auto ctag, auto d) -> hipError_t {
+        constexpr int big = decltype(d)::value == 256 ? 1 : decltype(d)::value == 128 ? 2 : 4;
+        if (p.row_tiles == 1) return run(ctag, d, std::integral_constant<int, 1>{});
+        return run(ctag, d, std::integral_constant<int, big>{});
+    };
+    auto by_dim = [&](auto ctag) -> hipError_t {
+        if (dim == 64) return by_rt(ctag, std::integral_constant<int, 64>{});
+        if (dim == 128) return by_rt(ctag, std::integral_constant<int, 128>{});
+        return by_rt(ctag, std::integral_constant<int, 256>{});
+    };
+    return ct == Act::F16 ? by_dim(_Float16{}) : by_dim(bf16_t{});
+}
+
+}  // namespace q2_0

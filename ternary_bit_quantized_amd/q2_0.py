@@ -31,16 +31,23 @@ Q2_0_PREC_F32_MFMA = 2
 Q2_0_ACT_F32 = 0
 Q2_0_ACT_F16 = 1
 Q2_0_ACT_BF16 = 2
+Q2_0_ROPE_HALF = 0
+Q2_0_ROPE_PAIRS = 1
 BLOCK_WEIGHTS = 64
 BLOCK_BYTES = 18
 MAT_VEC_MAX_N = 8
 NOALLOC_SCRATCH_BYTES = 64 << 20
+ATTN_MAX_QT = 16
+MOE_LAYER_MAX_TOKENS = 64
+MOE_LAYER_MAX_USED = 32
 
 EXPORTS = ("q2_0_get_rows", "q2_0_mul_mat_vec", "q2_0_mul_mat_vec_group", "q2_0_mul_mat",
            "q2_0_mul_mat_workspace_bytes", "q2_0_mul_mat_group", "q2_0_mul_mat_group_workspace_bytes",
            "q2_0_mul_mat_vec_act", "q2_0_mul_mat_vec_group_act", "q2_0_mul_mat_act", "q2_0_mul_mat_group_act",
            "q2_0_quantize", "q2_0_repack_g128", "q2_0_mul_mat_id", "q2_0_mul_mat_id_workspace_bytes",
-           "q2_0_mul_mat_noalloc", "q2_0_mul_mat_vec_batch", "q2_0_status_string", "q2_0_last_hip_error", "q2_0_version")
+           "q2_0_mul_mat_noalloc", "q2_0_mul_mat_vec_batch", "q2_0_kv_append", "q2_0_attn_shared",
+           "q2_0_attn_shared_workspace_bytes", "q2_0_moe_route", "q2_0_moe_layer", "q2_0_moe_layer_workspace_bytes",
+           "q2_0_status_string", "q2_0_last_hip_error", "q2_0_version")
 
 
 class MatVecItem(ctypes.Structure):
@@ -53,6 +60,13 @@ class MatVecBatchItem(ctypes.Structure):
     """q2_0_mat_vec_batch_item: one product of a batched mat-vec (its own K and x)."""
     _fields_ = [("w", ctypes.c_void_p), ("M", ctypes.c_int64), ("K", ctypes.c_int64), ("x", ctypes.c_void_p),
                 ("ldx", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64)]
+
+
+class KvCache(ctypes.Structure):
+    """q2_0_kv_cache: the two pools of a paged key/value cache; strides in elements."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("type", ctypes.c_int), ("n_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("n_kv", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
 
 
 def make_batch_items(entries):
@@ -119,6 +133,20 @@ def lib() -> ctypes.CDLL:
         L.q2_0_mul_mat_vec_batch.restype = ctypes.c_int
         L.q2_0_mul_mat_noalloc.argtypes = [P, I64, I64, P, I64, I64, P, I64, ctypes.c_int, P]
         L.q2_0_mul_mat_noalloc.restype = ctypes.c_int
+        L.q2_0_kv_append.argtypes = [P, P, I64, I64, I64, P, P, I64, P, I64, I64, P, I64, P, I64, C, P, I64, I64, C, P,
+                                     I64, P]
+        L.q2_0_kv_append.restype = C
+        L.q2_0_attn_shared.argtypes = [P, P, I64, I64, I64, P, I64, I64, P, I64, I64, I64, ctypes.c_float, P, I64, P,
+                                       ctypes.c_size_t, P]
+        L.q2_0_attn_shared.restype = C
+        L.q2_0_attn_shared_workspace_bytes.argtypes = [I64] * 7
+        L.q2_0_attn_shared_workspace_bytes.restype = ctypes.c_size_t
+        L.q2_0_moe_route.argtypes = [P, C, I64, I64, I64, I64, C, P, P, P]
+        L.q2_0_moe_route.restype = C
+        L.q2_0_moe_layer.argtypes = [P, P, P, I64, I64, I64, P, C, I64, P, P, I64, I64, P, I64, P, ctypes.c_size_t, P]
+        L.q2_0_moe_layer.restype = C
+        L.q2_0_moe_layer_workspace_bytes.argtypes = [I64] * 4
+        L.q2_0_moe_layer_workspace_bytes.restype = ctypes.c_size_t
         for f in (L.q2_0_mul_mat_vec_act, L.q2_0_mul_mat_vec_group_act, L.q2_0_mul_mat_act,
                   L.q2_0_mul_mat_group_act, L.q2_0_quantize, L.q2_0_repack_g128, L.q2_0_mul_mat_id):
             f.restype = ctypes.c_int
@@ -227,6 +255,43 @@ def quantize_raw(src: int, M: int, K: int, ld_src: int, w: int, stream: int = 0)
 
 def repack_g128_raw(w128: int, M: int, K: int, w: int, stream: int = 0) -> int:
     return lib().q2_0_repack_g128(w128, M, K, w, stream)
+
+
+def kv_append_raw(cache: KvCache, table: int, n_seqs: int, table_len: int, ld_table: int, seq: int, pos: int,
+                  n_tokens: int, q: int, ldq: int, n_q: int, k: int, ldk: int, v: int, ldv: int, x_type: int, rope: int,
+                  n_pos: int, rot_dim: int, style: int, q_out: int, ldqo: int, stream: int = 0) -> int:
+    return lib().q2_0_kv_append(ctypes.byref(cache) if cache is not None else None, table, n_seqs, table_len, ld_table,
+                                seq, pos, n_tokens, q, ldq, n_q, k, ldk, v, ldv, x_type, rope, n_pos, rot_dim, style,
+                                q_out, ldqo, stream)
+
+
+def attn_shared_raw(cache: KvCache, table: int, n_seqs: int, table_len: int, ld_table: int, lens: int, prefix_len: int,
+                    max_len: int, q: int, ldq: int, n_q: int, n_qt: int, scale: float, out: int, ldo: int,
+                    workspace: int, ws_bytes: int, stream: int = 0) -> int:
+    return lib().q2_0_attn_shared(ctypes.byref(cache) if cache is not None else None, table, n_seqs, table_len, ld_table,
+                                  lens, prefix_len, max_len, q, ldq, n_q, n_qt, scale, out, ldo, workspace, ws_bytes,
+                                  stream)
+
+
+def attn_shared_workspace_bytes(n_seqs: int, n_q: int, n_kv: int, head_dim: int, n_qt: int, prefix_len: int,
+                                max_len: int) -> int:
+    return lib().q2_0_attn_shared_workspace_bytes(n_seqs, n_q, n_kv, head_dim, n_qt, prefix_len, max_len)
+
+
+def moe_route_raw(logits: int, x_type: int, ld: int, n_tokens: int, n_expert: int, n_used: int, normalise: int, ids: int,
+                  weights: int, stream: int = 0) -> int:
+    return lib().q2_0_moe_route(logits, x_type, ld, n_tokens, n_expert, n_used, normalise, ids, weights, stream)
+
+
+def moe_layer_raw(w_gate: int, w_up: int, w_down: int, n_expert: int, n_ff: int, K: int, x: int, x_type: int, ldx: int,
+                  ids: int, weights: int, n_used: int, n_tokens: int, y: int, ldy: int, workspace: int, ws_bytes: int,
+                  stream: int = 0) -> int:
+    return lib().q2_0_moe_layer(w_gate, w_up, w_down, n_expert, n_ff, K, x, x_type, ldx, ids, weights, n_used, n_tokens,
+                                y, ldy, workspace, ws_bytes, stream)
+
+
+def moe_layer_workspace_bytes(n_ff: int, K: int, n_used: int, n_tokens: int) -> int:
+    return lib().q2_0_moe_layer_workspace_bytes(n_ff, K, n_used, n_tokens)
 
 
 def version() -> str:
@@ -415,3 +480,170 @@ def q2_0_mul_mat_group(mats, K: int, x, precision: int = Q2_0_PREC_F16_MFMA, ys=
     _check(mul_mat_group_act_raw(items, len(entries), K, xp, xt, ldx, N, precision, wsp, wsb, _stream(stream)),
            "q2_0_mul_mat_group_act")
     return ys
+
+
+# ------------------------------------------------------------- decoder-step operators (torch)
+
+def _act_types():
+    import torch
+    return {torch.float32: Q2_0_ACT_F32, torch.float16: Q2_0_ACT_F16, torch.bfloat16: Q2_0_ACT_BF16}
+
+
+def _rows(t, rows, cols, name):
+    """A 2-D CUDA tensor of `rows` rows of at least `cols` elements, unit inner stride -> row stride."""
+    if not t.is_cuda or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < cols or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError("%s must be a 2-D CUDA tensor of %d rows of at least %d elements with unit inner stride"
+                         % (name, rows, cols))
+    return t.stride(0) if rows > 1 else max(t.stride(0), t.shape[1])
+
+
+def _int32(t, shape, name):
+    import torch
+    if t.dtype != torch.int32 or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 CUDA tensor of shape %s" % (name, tuple(shape)))
+    return t.data_ptr()
+
+
+def _table(t):
+    import torch
+    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError("table must be a 2-D int32 CUDA tensor with unit inner stride")
+    n, cols = t.shape
+    return t.data_ptr(), n, cols, t.stride(0) if n > 1 else max(t.stride(0), cols)
+
+
+def _cache(k_cache, v_cache):
+    """Pools (n_pages, n_kv, page_size, head_dim) with unit inner stride and equal strides -> KvCache."""
+    st = k_cache.stride()
+    if k_cache.dim() != 4 or not k_cache.is_cuda or not v_cache.is_cuda or st[3] != 1 or \
+            v_cache.shape != k_cache.shape or v_cache.stride() != st or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must be CUDA tensors (n_pages, n_kv, page_size, head_dim) of one dtype "
+                         "and equal strides, unit inner stride")
+    dtype = _act_types().get(k_cache.dtype)
+    if dtype is None or dtype == Q2_0_ACT_F32:
+        raise ValueError("the cache must be float16 or bfloat16")
+    n_pages, n_kv, page, dim = k_cache.shape
+    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), dtype, n_pages, page, n_kv, dim, st[0], st[1], st[2])
+
+
+def q2_0_kv_append(k_cache, v_cache, table, seq, pos, k, v, rope=None, style: int = Q2_0_ROPE_HALF, q=None, q_out=None,
+                   stream=None):
+    """Rotate q and k by their positions and store k and v in the paged cache.
+
+    k_cache, v_cache (n_pages, n_kv, page_size, head_dim) float16 or bfloat16, any strides with unit inner
+    stride; table (n_seqs, pages) int32 page numbers; seq, pos (n_tokens) int32; k, v (n_tokens, n_kv*head_dim)
+    and q (n_tokens, n_q*head_dim) float32, float16 or bfloat16, all of one dtype; rope (n_pos, rot_dim) float32, cos then
+    sin of a position's angles (None: no rotation).  Returns the rotated q in the cache's dtype (None without q)."""
+    import torch
+    c = _cache(k_cache, v_cache)
+    n = k.shape[0]
+    xt = _act_types().get(k.dtype)
+    if xt is None or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise ValueError("q, k and v must be float32, float16 or bfloat16, all of one dtype")
+    tp, n_seqs, cols, ldt = _table(table)
+    kv = c.n_kv * c.head_dim
+    ldk, ldv = _rows(k, n, kv, "k"), _rows(v, n, kv, "v")
+    qp, ldq, n_q, op, ldo = 0, 0, 0, 0, 0
+    if q is not None:
+        n_q = q.shape[1] // c.head_dim
+        if q.shape[1] != n_q * c.head_dim:
+            raise ValueError("q must have whole heads of %d elements" % c.head_dim)
+        ldq, qp = _rows(q, n, q.shape[1], "q"), q.data_ptr()
+        if q_out is None:
+            q_out = torch.empty((n, q.shape[1]), dtype=k_cache.dtype, device=q.device)
+        elif q_out.dtype != k_cache.dtype:
+            raise ValueError("q_out must have the cache's dtype")
+        ldo, op = _rows(q_out, n, q.shape[1], "q_out"), q_out.data_ptr()
+    rp, n_pos, rot = 0, 0, 0
+    if rope is not None:
+        if rope.dtype != torch.float32 or not rope.is_cuda or rope.dim() != 2 or not rope.is_contiguous():
+            raise ValueError("rope must be a contiguous 2-D float32 CUDA tensor")
+        n_pos, rot = rope.shape
+        rp = rope.data_ptr()
+    _check(kv_append_raw(c, tp, n_seqs, cols, ldt, _int32(seq, (n,), "seq"), _int32(pos, (n,), "pos"), n, qp, ldq, n_q,
+                         k.data_ptr(), ldk, v.data_ptr(), ldv, xt, rp, n_pos, rot, style, op, ldo, _stream(stream)),
+           "q2_0_kv_append")
+    return q_out
+
+
+def q2_0_attn_shared(q, k_cache, v_cache, table, lens, scale: float, prefix_len: int = 0, max_len=None, n_qt: int = 1,
+                     out=None, workspace=None, stream=None):
+    """Attention of n_qt query tokens per sequence over the paged cache, the first prefix_len tokens shared.
+
+    q (n_seqs*n_qt, n_q*head_dim) of the cache's dtype; table (n_seqs, pages) int32; lens (n_seqs) int32: tokens of
+    each sequence with the prefix and its query tokens; max_len bounds lens (default: what the table holds).  Returns
+    out like q."""
+    import torch
+    c = _cache(k_cache, v_cache)
+    tp, n_seqs, cols, ldt = _table(table)
+    width = q.shape[1]
+    n_q = width // c.head_dim
+    if q.dtype != k_cache.dtype or width != n_q * c.head_dim:
+        raise ValueError("q must have the cache's dtype and whole heads of %d elements" % c.head_dim)
+    ldq = _rows(q, n_seqs * n_qt, width, "q")
+    if out is None:
+        out = torch.empty((n_seqs * n_qt, width), dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype:
+        raise ValueError("out must have the cache's dtype")
+    ldo = _rows(out, n_seqs * n_qt, width, "out")
+    if max_len is None:
+        max_len = cols * c.page_size
+    need = attn_shared_workspace_bytes(n_seqs, n_q, c.n_kv, c.head_dim, n_qt, prefix_len, max_len)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    wsp = workspace.data_ptr() if workspace is not None else 0
+    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(attn_shared_raw(c, tp, n_seqs, cols, ldt, _int32(lens, (n_seqs,), "lens"), prefix_len, max_len, q.data_ptr(),
+                           ldq, n_q, n_qt, scale, out.data_ptr(), ldo, wsp, wsb, _stream(stream)), "q2_0_attn_shared")
+    return out
+
+
+def q2_0_moe_route(logits, n_used: int, normalise: bool = True, ids=None, weights=None, stream=None):
+    """(ids, weights), each (n_tokens, n_used): the n_used largest router logits of each row of logits
+    (n_tokens, n_expert) float32, float16 or bfloat16, largest first and the lower index first among equals, and their
+    softmax weights over the chosen (normalise) or over all experts."""
+    import torch
+    n, n_expert = logits.shape
+    xt = _act_types().get(logits.dtype)
+    if xt is None:
+        raise ValueError("logits must be float32, float16 or bfloat16")
+    ld = _rows(logits, n, n_expert, "logits")
+    if ids is None:
+        ids = torch.empty((n, n_used), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((n, n_used), dtype=torch.float32, device=logits.device)
+    if weights.dtype != torch.float32 or weights.shape != (n, n_used) or not weights.is_contiguous():
+        raise ValueError("weights must be a contiguous float32 tensor (n_tokens, n_used)")
+    _check(moe_route_raw(logits.data_ptr(), xt, ld, n, n_expert, n_used, int(bool(normalise)),
+                         _int32(ids, (n, n_used), "ids"), weights.data_ptr(), _stream(stream)), "q2_0_moe_route")
+    return ids, weights
+
+
+def q2_0_moe_layer(w_gate, w_up, w_down, n_expert: int, n_ff: int, K: int, x, ids, weights, y=None, workspace=None,
+                   stream=None):
+    """y (n_tokens, K) float32 = sum over u of weights[t, u] * W_down (silu(W_gate x) * (W_up x)) of expert ids[t, u].
+
+    w_gate and w_up hold n_expert (n_ff, K) Q2_0 matrices back to back, w_down n_expert (K, n_ff) ones; x (n_tokens, >=K)
+    float32, float16 or bfloat16, at most MOE_LAYER_MAX_TOKENS rows; ids int32 and weights float32 (n_tokens, n_used)."""
+    import torch
+    xp, n, ldx, xt = _xcols(x, K, "x")
+    n_used = ids.shape[1]
+    if weights.dtype != torch.float32 or weights.shape != (n, n_used) or not weights.is_contiguous():
+        raise ValueError("weights must be a contiguous float32 tensor (n_tokens, n_used)")
+    for w, name in ((w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down")):
+        if not w.is_contiguous() or w.numel() * w.element_size() < n_expert * n_ff * K // BLOCK_WEIGHTS * BLOCK_BYTES:
+            raise ValueError("%s must be contiguous and hold n_expert matrices" % name)
+    if y is None:
+        y = torch.empty((n, K), dtype=torch.float32, device=x.device)
+    yp, yn, ldy = _cols(y, K, "y")
+    if yn != n:
+        raise ValueError("y must have n_tokens rows")
+    need = moe_layer_workspace_bytes(n_ff, K, n_used, n)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    wsp = workspace.data_ptr() if workspace is not None else 0
+    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(moe_layer_raw(w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), n_expert, n_ff, K, xp, xt, ldx,
+                         _int32(ids, (n, n_used), "ids"), weights.data_ptr(), n_used, n, yp, ldy, wsp, wsb,
+                         _stream(stream)), "q2_0_moe_layer")
+    return y
