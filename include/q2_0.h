@@ -482,11 +482,14 @@ int q2_0_moe_route(const void *logits, int x_type, int64_t ld, int64_t n_tokens,
  *   y       : f32 row t of K elements at y + t*ldy, overwritten.
  * n_tokens <= Q2_0_MOE_LAYER_MAX_TOKENS and n_used <= 32, UNSUPPORTED otherwise (use
  * q2_0_mul_mat_id).
- * Accuracy: all three products are fp32-grade, as q2_0_mul_mat_vec's (x and the
- * hidden activation enter the matrix cores as fp16 hi/lo pairs under its range
- * condition); sums over the experts are f32.  Deterministic run to run.
+ * Accuracy.  x and the hidden activation enter the matrix cores as fixed point: an element errs
+ * by at most 2^-30 of the largest |x| among the 128 of its block pair (and elements below
+ * 2^-127 count as zero); integer block sums are exact, sums over blocks and experts f32.  So
+ * each product meets |y - y_exact| <= 1e-5 * A, A = sum_k |W x|, whenever
+ *     max_k |x| * sum_k |W| <= 2^12 * A    (taken over block pairs),
+ * and a block pair holding inf or NaN gives NaN.  Deterministic run to run.
  *   workspace / ws_bytes: at least q2_0_moe_layer_workspace_bytes() bytes, 16-byte
- *             aligned: the hidden activations and the experts' partial results.
+ *             aligned: the hidden activations, x and the experts' results.  Overwritten.
  * Errors: SHAPE (also n_expert < 1 or > 8192), the no-op for n_tokens == 0, NULL, LAYOUT,
  * UNSUPPORTED, ALIGN, WORKSPACE.  n_used == 0 writes zeros.
  */

@@ -34,6 +34,7 @@
 
 #include "q2_0_internal.h"
 #include "mat_vec_common.h"
+#include "lds_dma.h"
 #include "x_to_f16.h"
 
 namespace q2_0 {
@@ -126,32 +127,6 @@ __device__ __forceinline__ int find_gemm_item(const GemmGroup &grp, int tmg) {
 // group, and the 8 even or odd ones differ in c >> 1); a load lane picks the global chunk
 // that belongs at its LDS position.  (With ch ^ (c & 7) the groups of 16 met in pairs:
 // ~7x the bank-conflict cycles, measured.)
-// One 16-byte LDS-DMA load per lane: lane i's 16 bytes at src land at LDS byte address
-// lds + 16 i.  Issued as inline assembly so that the compiler does not track it: its
-// own wait insertion would otherwise make every later LDS read wait for all of these
-// loads (it cannot tell that they fill a different buffer).  The caller orders them
-// with wait_vmcnt before the barrier that publishes the tile.
-// M0 (the LDS address) is saved and restored around the load, so the compiler's view of
-// it does not change.
-__device__ __forceinline__ void lds_dma16(const void *src, uint32_t lds) {
-    uint32_t saved;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %2\n\t"
-        "global_load_lds_dwordx4 %1, off\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
-        : "v"(src), "s"(lds)
-        : "memory");
-}
-
-// s_waitcnt with only the vector-memory count set (expcnt and lgkmcnt at their maxima).
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
-}
-
 template <int RF, int NJ, int NXB, bool kAligned, int OCC, bool HL>
 __global__ __launch_bounds__(256, OCC) void gemm_f16_mfma(GemmGroup grp, int nb, const _Float16 *__restrict__ x16,
                                                           const int *__restrict__ xe, int N, int tiles_n,

@@ -42,6 +42,23 @@ __device__ __forceinline__ uint32_t pack2<bf16_t>(float a, float b) {
     return __builtin_bit_cast(uint32_t, bf2{(__bf16)a, (__bf16)b});
 }
 
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
+    return v > o ? v : o;
+}
+
+// Maximum over the wave, uniform: row shifts by 1, 2, 4, 8, then the row broadcasts.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+    v = dpp_max<0x111>(v);
+    v = dpp_max<0x112>(v);
+    v = dpp_max<0x114>(v);
+    v = dpp_max<0x118>(v);
+    v = dpp_max<0x142>(v);
+    v = dpp_max<0x143>(v);
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
 struct KvAppend {
     const void *q, *k, *v;
     int64_t ldq, ldk, ldv;

@@ -10,7 +10,7 @@
 // What bounds it: a launch for few tokens; its bytes are 4*n_expert + 8*n_used a token.
 #include <type_traits>
 
-#include "q2_0_internal.h"
+#include "layer_common.h"
 
 namespace q2_0 {
 
@@ -18,23 +18,6 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     if (v != v) return 1u;
     const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);   // -0 + 0 = +0
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);           // -inf: 0x007fffff
-}
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
-    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
-    return v > o ? v : o;
-}
-
-// Maximum over the wave, uniform (row shifts by 1, 2, 4, 8, then the row broadcasts).
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-    v = dpp_max<0x111>(v);
-    v = dpp_max<0x112>(v);
-    v = dpp_max<0x114>(v);
-    v = dpp_max<0x118>(v);
-    v = dpp_max<0x142>(v);
-    v = dpp_max<0x143>(v);
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
 template <int PL, typename XT>
