@@ -30,8 +30,9 @@
 // the value rows past that limit zeroed, so that what lies in unseen places (NaN, inf)
 // reaches no row that does not see it.  Addresses are clamped to seen keys.
 //
-// Split.  The 4 waves of a workgroup interleave the key tiles of one split; their results
-// join in LDS, the splits' in attn_join.
+// Split.  The waves of a workgroup interleave the key tiles of one split; their results join in
+// LDS, the splits' in attn_join.  Workgroups that read the same prefix keys for other rows get
+// launch numbers 8 apart: the same XCD, whose L2 then serves all but one of them.
 #include <type_traits>
 
 #include "layer_common.h"
@@ -57,8 +58,21 @@ struct Mma<bf16_t> {
     }
 };
 
-constexpr int kAttnWaves = 4;
 constexpr int kAttnTile = 32;    // keys per step
+constexpr int kAttnMaxSplits = 32;
+
+template <int CTRL>
+__device__ __forceinline__ int dpp_int(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, false);
+}
+
+// Over the 16 lanes of a DPP row (row_ror 8, 4, 2, 1).
+__device__ __forceinline__ int row_min(int v) {
+    v = min(v, dpp_int<0x128>(v));
+    v = min(v, dpp_int<0x124>(v));
+    v = min(v, dpp_int<0x122>(v));
+    return min(v, dpp_int<0x121>(v));
+}
 
 // N dwords from 4-byte aligned memory (8 or 16 bytes aligned as N goes)
 template <int N>
@@ -75,75 +89,75 @@ __device__ __forceinline__ void load_dwords(const uint8_t *p, uint32_t *v) {
     }
 }
 
-// P16: page_size % 16 == 0, so that the 16 keys of a half tile lie in one page and its page
-// number is read once for the wave; otherwise 32 lanes look up a key each and pass the rows
-// round through LDS.
-template <typename CT, int D, int RT, bool P16>
-__global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_rows(AttnShared a) {
+// W: waves.  P16: page_size % 16 == 0 (and the keys start at a multiple of 16, or are all of one page
+// table row), so that the 16 keys of a half tile lie in one page and its page number is read
+// once for the wave; otherwise 32 lanes look up a key each and pass the rows round through LDS.
+template <typename CT, int D, int RT, int W, bool P16>
+__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows(AttnShared a) {
     constexpr int KS = D / 32;       // 32-dim steps of a score
     constexpr int DPL = D / 16;      // dims per lane of a value row
     constexpr int VD = DPL / 2;      // dwords of those
     constexpr int OS = D + 4;        // LDS floats per row
 
-    __shared__ __attribute__((aligned(16))) float lds_o[kAttnWaves][RT * 16][OS];
-    __shared__ float lds_m[kAttnWaves][RT * 16], lds_l[kAttnWaves][RT * 16];
-    __shared__ int64_t lds_row[P16 ? 1 : kAttnWaves][P16 ? 1 : kAttnTile];
+    __shared__ __attribute__((aligned(16))) float lds_o[W][RT * 16][OS];
+    __shared__ float lds_m[W][RT * 16], lds_l[W][RT * 16];
+    __shared__ int64_t lds_row[P16 ? 1 : W][P16 ? 1 : kAttnTile];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15, g = lane >> 4;
 
     // this workgroup's part: prefix (all sequences' rows) or one sequence's own keys
     const bool pre = (int)blockIdx.x < a.wgs_p;
-    int u = pre ? (int)blockIdx.x : (int)blockIdx.x - a.wgs_p;
-    const int groups = pre ? a.groups_p : a.groups_o, splits = pre ? a.splits_p : a.splits_o;
     const int nrows = pre ? a.rows_p : a.rows_o;
-    const int rg = u % groups;
-    u /= groups;
-    const int kvh = u % a.n_kv;
-    u /= a.n_kv;
-    const int split = u % splits;
-    const int seq = pre ? 0 : u / splits;
+    int rg, kvh, split, seq = 0;
+    if (pre) {
+        const int id = blockIdx.x, x = a.xcd_p ? id & 7 : 0, y = a.xcd_p ? id >> 3 : id;
+        int u = a.groups_p.div((uint32_t)y);
+        rg = y - u * (int)a.groups_p.d;
+        if (a.xcd_p) u = u * 8 + x;
+        split = a.heads.div((uint32_t)u);
+        kvh = u - split * a.n_kv;
+    } else {
+        const int id = (int)blockIdx.x - a.wgs_p;
+        int u = a.groups_o.div((uint32_t)id);
+        rg = id - u * (int)a.groups_o.d;
+        int v = a.heads.div((uint32_t)u);
+        kvh = u - v * a.n_kv;
+        seq = a.splits_o.div((uint32_t)v);
+        split = v - seq * (int)a.splits_o.d;
+    }
+    const int splits = pre ? a.splits_p : (int)a.splits_o.d;
     const int r0 = rg * RT * 16;
-    const int nrt = min(RT, (nrows - r0 + 15) / 16);
+    const int nrt = RT == 1 ? 1 : min(RT, (nrows - r0 + 15) / 16);
     const int tok0 = seq * a.n_qt;
 
     // a row's query (token, head) and the keys it sees
     const int grp = (int)a.group.d;
     const auto row_token = [&](int r) { return tok0 + a.group.div((uint32_t)r); };
-    const auto row_limit = [&](int r) {
-        if (r >= nrows) return 0;
-        const int t = row_token(r);
-        const int s = t / a.n_qt;
-        const int len = a.lens[s];
-        if (len < 0 || len > a.max_len) return 0;
-        const int lim = len - a.n_qt + 1 + (t - s * a.n_qt);
-        return max(0, pre ? min(lim, a.prefix_len) : lim);
-    };
     int lim[RT];
     int lim_lo = 0x7fffffff, lim_hi = 0;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         const int r = r0 + 16 * t + j;
-        lim[t] = t < nrt ? row_limit(r) : 0;
-        if (t < nrt && r < nrows) {
+        lim[t] = 0;
+        if (r < nrows) {
+            const int tok = row_token(r), s = a.queries.div((uint32_t)tok);
+            const int len = a.lens[s];
+            const int n = len - a.n_qt + 1 + (tok - s * a.n_qt);
+            lim[t] = len < 0 || len > a.max_len ? 0 : max(0, pre ? min(n, a.prefix_len) : n);
             lim_lo = min(lim_lo, lim[t]);
             lim_hi = max(lim_hi, lim[t]);
         }
     }
-#pragma unroll
-    for (int off = 1; off < 16; off <<= 1) {
-        lim_lo = min(lim_lo, __shfl_xor(lim_lo, off));
-        lim_hi = max(lim_hi, __shfl_xor(lim_hi, off));
-    }
-    lim_lo = __builtin_amdgcn_readfirstlane(lim_lo);
-    lim_hi = __builtin_amdgcn_readfirstlane(lim_hi);
+    lim_lo = __builtin_amdgcn_readfirstlane(row_min(lim_lo));
+    lim_hi = __builtin_amdgcn_readfirstlane(-row_min(-lim_hi));
 
     // key tiles of this split: tiles [ta, tb) of the part's keys [k_lo, lim_hi)
-    const int k_lo = pre ? 0 : a.prefix_len;
+    const int k_lo = pre ? 0 : a.own_from;
     const int t_first = k_lo / kAttnTile;
     const int t_end = lim_hi > k_lo ? (lim_hi + kAttnTile - 1) / kAttnTile : t_first;
     const int ntile = t_end - t_first;
-    const int per = (ntile + splits - 1) / splits;
+    const int per = splits == 1 ? ntile : (pre ? a.div_p : a.splits_o).div((uint32_t)(ntile + splits - 1));
     const int ta = t_first + min(ntile, per * split), tb = t_first + min(ntile, per * (split + 1));
 
     // queries as the scores' B operand
@@ -151,7 +165,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_rows(AttnShared a) 
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         const int r = r0 + 16 * t + j;
-        const bool in = t < nrt && r < nrows;
+        const bool in = r < nrows;
         const int tok = in ? row_token(r) : 0;
         const int head = kvh * grp + (in ? r - (tok - tok0) * grp : 0);
         const uint8_t *qp = static_cast<const uint8_t *>(a.q) + 2 * ((int64_t)tok * a.ldq + (int64_t)head * D + 8 * g);
@@ -171,7 +185,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_rows(AttnShared a) 
         for (int e = 0; e < DPL; ++e) o[t][e] = float4_t{0.f, 0.f, 0.f, 0.f};
     }
 
-    const int32_t *trow = a.table + (pre ? 0 : (int64_t)seq * a.ld_table);
+    const int32_t *trow = a.table + (int64_t)seq * a.ld_table;
     const uint8_t *kbase = static_cast<const uint8_t *>(a.kc) + 2 * (int64_t)kvh * a.head_stride;
     const uint8_t *vbase = static_cast<const uint8_t *>(a.vc) + 2 * (int64_t)kvh * a.head_stride;
     const int ts = (int)a.token_stride;
@@ -184,7 +198,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_rows(AttnShared a) 
     // element offset of key's row, and whether its page exists
     const auto key_row = [&](int key, bool &ok) {
         const int pi = a.page.div((uint32_t)key);
-        const int page = trow[pi];
+        const int page = (key < a.joint_len ? a.table : trow)[pi];
         ok = page >= 0 && page < a.n_pages;
         return (int64_t)(ok ? page : 0) * a.page_stride + (int64_t)(key - pi * psz) * a.token_stride;
     };
@@ -240,14 +254,16 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_rows(AttnShared a) 
         return r;
     };
 
-    for (int tile = ta + wave; tile < tb; tile += kAttnWaves) {
+    for (int tile = ta + wave; tile < tb; tile += W) {
         load_tile(tile);
         const int key0 = tile * kAttnTile;
         const bool edge = key0 < k_lo || key0 + kAttnTile > lim_lo || bad != 0;   // some score needs a mask
         u32x4_t p[RT];
 #pragma unroll
+        for (int t = 0; t < RT; ++t) p[t] = u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
         for (int t = 0; t < RT; ++t) {
-            if (t >= nrt) break;
+            if (RT > 1 && t >= nrt) break;
             float4_t s[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -297,7 +313,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_rows(AttnShared a) 
                 const u32x4_t va = v_operand(e);
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
-                    if (t >= nrt) break;
+                    if (RT > 1 && t >= nrt) break;
                     o[t][e] = Mma<CT>::mul(va, p[t], o[t][e]);
                 }
             }
@@ -309,10 +325,8 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_rows(AttnShared a) 
                 int cur = 0x7fffffff;
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
-                    if (t < nrt && lim[t] > done) cur = min(cur, lim[t]);
-#pragma unroll
-                for (int off = 1; off < 16; off <<= 1) cur = min(cur, __shfl_xor(cur, off));
-                cur = __builtin_amdgcn_readfirstlane(cur);
+                    if ((RT == 1 || t < nrt) && lim[t] > done) cur = min(cur, lim[t]);
+                cur = __builtin_amdgcn_readfirstlane(row_min(cur));
                 if (cur == 0x7fffffff) break;
                 done = cur;
                 if (cur <= key0) continue;      // these rows see nothing here
@@ -329,8 +343,9 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_rows(AttnShared a) 
                     for (int q = 0; q < 4; ++q) va[q] &= keep[q];
 #pragma unroll
                     for (int t = 0; t < RT; ++t) {
-                        if (t >= nrt) break;
-                        // (a selected result, not a zeroed P: 0 * NaN would reach the other rows)
+                        // (a selected result, not a zeroed P: 0 * NaN would reach the other rows; and no
+                        // branch on t between: the compiler leaves out the wait states from a matrix
+                        // instruction to a read of its result at a branch's target)
                         const float4_t r = Mma<CT>::mul(va, p[t], o[t][e]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) o[t][e][i] = lim[t] == cur ? r[i] : o[t][e][i];
@@ -340,10 +355,10 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_rows(AttnShared a) 
         }
     }
 
-    // join the four waves' results
+    // join the waves' results
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-        if (t >= nrt) break;
+        if (RT > 1 && t >= nrt) break;
         float lt = l[t];
         lt += __shfl_xor(lt, 16);
         lt += __shfl_xor(lt, 32);
@@ -354,33 +369,35 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_rows(AttnShared a) 
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < DPL; ++e) lds_o[wave][16 * t + j][DPL * (4 * g + i) + e] = o[t][e][i];
+            for (int e = 0; e < DPL; e += 4)
+                *reinterpret_cast<float4_t *>(&lds_o[wave][16 * t + j][DPL * (4 * g + i) + e]) =
+                    float4_t{o[t][e][i], o[t][e + 1][i], o[t][e + 2][i], o[t][e + 3][i]};
     }
     __syncthreads();
     const int rows_here = min(nrows - r0, RT * 16);
-    const int nsplit = a.splits_p + a.splits_o;
+    const int nsplit = a.splits_p + (a.wgs_o ? (int)a.splits_o.d : 0);
     const int sidx = pre ? split : a.splits_p + split;
-    const int64_t n_out = (int64_t)a.n_seqs * a.n_qt * a.n_q;
-    for (int x = tid; x < rows_here * (D / 4); x += 256) {
+#pragma unroll 1
+    for (int x = tid; x < rows_here * (D / 4); x += 64 * W) {
         const int r = x / (D / 4), d = 4 * (x % (D / 4));
         float mm = -__builtin_inff();
 #pragma unroll
-        for (int w = 0; w < kAttnWaves; ++w) mm = fmaxf(mm, lds_m[w][r]);
+        for (int w = 0; w < W; ++w) mm = fmaxf(mm, lds_m[w][r]);
         const float mb = mm == -__builtin_inff() ? 0.f : mm;
         float ll = 0.f;
         float4_t oo = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < kAttnWaves; ++w) {
+#pragma unroll 1
+        for (int w = 0; w < W; ++w) {
             const float f = __builtin_amdgcn_exp2f(lds_m[w][r] - mb);
-            ll += f * lds_l[w][r];
+            ll = __builtin_fmaf(f, lds_l[w][r], ll);
             const float4_t v = *reinterpret_cast<const float4_t *>(&lds_o[w][r][d]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) oo[i] += f * v[i];
+            for (int i = 0; i < 4; ++i) oo[i] = __builtin_fmaf(f, v[i], oo[i]);
         }
         const int tok = row_token(r0 + r);
         const int head = kvh * grp + (r0 + r - (tok - tok0) * grp);
         if (nsplit == 1) {
-            const int len = a.lens[tok / a.n_qt];
+            const int len = a.lens[a.queries.div((uint32_t)tok)];
             const float nv = len < 0 || len > a.max_len ? __builtin_nanf("") : 0.f;
             const float inv = 1.f / ll;
             float4_t res;
@@ -389,102 +406,135 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_rows(AttnShared a) 
             CT *op = static_cast<CT *>(a.out) + (int64_t)tok * a.ldo + (int64_t)head * D + d;
             *reinterpret_cast<u32x2_t *>(op) = u32x2_t{pack2<CT>(res[0], res[1]), pack2<CT>(res[2], res[3])};
         } else {
-            const int64_t row = sidx * n_out + (int64_t)tok * a.n_q + head;
+            const int64_t row = ((int64_t)tok * a.n_q + head) * nsplit + sidx;
             *reinterpret_cast<float4_t *>(a.part_o + row * D + d) = oo;
             if (d == 0) *reinterpret_cast<float2_t *>(a.part_ml + 2 * row) = float2_t{mm, ll};
         }
     }
 }
 
-// Joins the splits of a row: a wave per row.
+// Joins the splits (at most 64) of a row: a workgroup per row, D/4 lanes for a split's O.
 template <typename CT, int D>
-__global__ __launch_bounds__(256) void attn_join(AttnShared a) {
-    constexpr int PER = D / 64;
-    const int lane = threadIdx.x & 63;
-    const int64_t n_out = (int64_t)a.n_seqs * a.n_qt * a.n_q;
-    const int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (row >= n_out) return;
-    const int nsplit = a.splits_p + a.splits_o;
-    float mm = -__builtin_inff();
-    for (int s = 0; s < nsplit; ++s) mm = fmaxf(mm, a.part_ml[2 * (s * n_out + row)]);
-    const float mb = mm == -__builtin_inff() ? 0.f : mm;
-    float ll = 0.f, oo[PER];
+__global__ __launch_bounds__(256) void attn_join(AttnShared a, int nsplit) {
+    constexpr int L = D / 4, G = 256 / L;
+    __shared__ float4_t lds[256];
+    __shared__ float lds_f[64];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int64_t row = blockIdx.x;
+    // every wave: the splits' weights, one a lane
+    float2_t ml = {-__builtin_inff(), 0.f};
+    if (lane < nsplit) ml = *reinterpret_cast<const float2_t *>(a.part_ml + 2 * (row * nsplit + lane));
+    float mm = ml.x;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) oo[i] = 0.f;
-    for (int s = 0; s < nsplit; ++s) {
-        const int64_t at = s * n_out + row;
-        const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - mb);
-        ll += f * a.part_ml[2 * at + 1];
+    for (int off = 32; off >= 1; off >>= 1) mm = fmaxf(mm, __shfl_xor(mm, off));
+    const float f = __builtin_amdgcn_exp2f(ml.x - (mm == -__builtin_inff() ? 0.f : mm));
+    float ll = f * ml.y;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) oo[i] += f * a.part_o[at * D + lane * PER + i];
+    for (int off = 32; off >= 1; off >>= 1) ll += __shfl_xor(ll, off);
+    if (tid < 64) lds_f[lane] = f;
+    __syncthreads();
+    const int d = 4 * (tid % L);
+    float4_t oo = {0.f, 0.f, 0.f, 0.f};
+    const float *po = a.part_o + row * nsplit * D + d;
+#pragma unroll 4
+    for (int s = tid / L; s < nsplit; s += G) {
+        const float w = lds_f[s];
+        const float4_t v = *reinterpret_cast<const float4_t *>(po + s * D);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) oo[i] = __builtin_fmaf(w, v[i], oo[i]);
     }
-    const int64_t tok = row / a.n_q;
-    const int head = (int)(row - tok * a.n_q);
-    const int len = a.lens[tok / a.n_qt];
-    const float nv = len < 0 || len > a.max_len ? __builtin_nanf("") : 0.f;
-    const float inv = 1.f / ll;
-    CT *op = static_cast<CT *>(a.out) + tok * a.ldo + (int64_t)head * D + lane * PER;
+    lds[tid] = oo;
+    __syncthreads();
+    if (tid < L) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) op[i] = to_elem<CT>(ll == 0.f ? nv : oo[i] * inv);
+        for (int k = 1; k < G; ++k) {
+            const float4_t v = lds[k * L + tid];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) oo[i] += v[i];
+        }
+        const int tok = (int)(row / a.n_q), head = (int)(row - (int64_t)tok * a.n_q);
+        const int len = a.lens[a.queries.div((uint32_t)tok)];
+        const float nv = len < 0 || len > a.max_len ? __builtin_nanf("") : 0.f;
+        const float inv = 1.f / ll;
+        float4_t res;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) res[i] = ll == 0.f ? nv : oo[i] * inv;
+        CT *op = static_cast<CT *>(a.out) + (int64_t)tok * a.ldo + (int64_t)head * D + d;
+        *reinterpret_cast<u32x2_t *>(op) = u32x2_t{pack2<CT>(res[0], res[1]), pack2<CT>(res[2], res[3])};
+    }
 }
+
+// 8 waves where two of them fit a SIMD's registers with one row tile each
+constexpr int attn_waves(int64_t dim, int row_tiles) { return row_tiles == 1 && dim < 256 ? 8 : 4; }
 
 AttnPlan attn_plan(int64_t n_seqs, int64_t n_q, int64_t n_kv, int64_t dim, int64_t n_qt, int64_t prefix_len,
                    int64_t max_len) {
-    AttnPlan p;
+    AttnPlan p{};
     const int64_t rows_o = n_qt * (n_q / n_kv), rows_p = n_seqs * rows_o;
-    const int64_t most = prefix_len > 0 ? rows_p : rows_o;
-    p.row_tiles = most <= 16 || dim == 256 ? 1 : (dim == 128 ? 2 : 4);
-    const int64_t rpg = 16 * p.row_tiles;
-    const auto splits = [](int64_t units, int64_t tiles) {
-        // enough workgroups for the chip, but at least a tile for each of a workgroup's waves
+    const auto tiles = [](int64_t keys) { return (keys + kAttnTile - 1) / kAttnTile; };
+    const auto groups = [&](int64_t rows) { return (rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles); };
+    // enough workgroups for the chip, but two tiles for each of a workgroup's waves
+    const auto splits = [&](int64_t units, int64_t t) {
         int64_t s = (512 + units - 1) / units;
-        if (s > (tiles + kAttnWaves - 1) / kAttnWaves) s = (tiles + kAttnWaves - 1) / kAttnWaves;
-        if (s > 128) s = 128;
+        if (s > t / (2 * p.waves)) s = t / (2 * p.waves);
+        if (s > kAttnMaxSplits) s = kAttnMaxSplits;
         return s < 1 ? (int64_t)1 : s;
     };
-    p.groups_p = (int)((rows_p + rpg - 1) / rpg);
-    p.groups_o = (int)((rows_o + rpg - 1) / rpg);
-    p.splits_p = p.splits_o = 0;
-    if (prefix_len > 0) p.splits_p = (int)splits(p.groups_p * n_kv, (prefix_len + kAttnTile - 1) / kAttnTile);
-    if (max_len > prefix_len)
-        p.splits_o = (int)splits(n_seqs * p.groups_o * n_kv, (max_len + kAttnTile - 1) / kAttnTile - prefix_len / kAttnTile);
+    // Short and few: one workgroup per sequence and key head takes all keys, prefix included
+    // (read once per sequence, from the L2), and writes the result itself: no join.
+    const int big = dim == 64 ? 4 : dim == 128 ? 2 : 1;
+    p.row_tiles = rows_o <= 16 ? 1 : big;
+    p.waves = attn_waves(dim, p.row_tiles);
+    p.joint = prefix_len > 0 && tiles(max_len) <= 5 * p.waves && n_seqs * n_kv * groups(rows_o) <= 256;
+    const bool shared = prefix_len > 0 && !p.joint;
+    if (shared) {
+        p.row_tiles = rows_p <= 16 ? 1 : big;
+        p.waves = attn_waves(dim, p.row_tiles);
+    }
+    p.groups_p = groups(rows_p);
+    p.groups_o = groups(rows_o);
+    p.splits_p = shared ? splits(p.groups_p * n_kv, tiles(prefix_len)) : 0;
+    const int64_t own = shared ? tiles(max_len) - prefix_len / kAttnTile : tiles(max_len);
+    p.splits_o = !shared || max_len > prefix_len ? (own <= 5 * p.waves ? 1 : splits(n_seqs * p.groups_o * n_kv, own)) : 0;
     const int64_t n = p.splits_p + p.splits_o;
-    p.ws_bytes = n <= 1 ? 0 : (size_t)(n * n_seqs * n_qt * n_q) * (size_t)(dim + 2) * 4;
+    p.ws_bytes = n <= 1 ? 0 : (size_t)(n * rows_p * n_kv) * (size_t)(dim + 2) * 4;
     return p;
 }
 
 hipError_t launch_attn_shared(AttnShared a, const AttnPlan &p, Act ct, int dim, hipStream_t s) {
-    a.groups_p = p.groups_p;
-    a.groups_o = p.groups_o;
-    a.splits_p = p.splits_p;
-    a.splits_o = p.splits_o;
+    const auto div = [](int64_t d) { return FastDiv::make((uint32_t)(d > 0 ? d : 1)); };
+    a.groups_p = div(p.groups_p);
+    a.groups_o = div(p.groups_o);
+    a.heads = div(a.n_kv);
+    a.queries = div(a.n_qt);
+    a.div_p = div(p.splits_p);
+    a.splits_o = div(p.splits_o);
+    a.splits_p = (int)p.splits_p;
     a.rows_o = a.n_qt * (int)a.group.d;
     a.rows_p = a.n_seqs * a.rows_o;
-    const int64_t wgs_p = (int64_t)a.groups_p * a.n_kv * a.splits_p;
-    const int64_t wgs_o = (int64_t)a.groups_o * a.n_kv * a.splits_o * a.n_seqs;
-    a.wgs_p = (int)wgs_p;
-    const int64_t n_out = (int64_t)a.n_seqs * a.n_qt * a.n_q;
-    const int nsplit = a.splits_p + a.splits_o;
+    a.own_from = p.joint ? 0 : a.prefix_len;
+    a.joint_len = p.joint ? a.prefix_len : 0;
+    const int64_t units_p = a.n_kv * p.splits_p;
+    a.xcd_p = p.groups_p > 1 && units_p % 8 == 0;
+    a.wgs_p = (int)(p.groups_p * units_p);
+    a.wgs_o = (int)(p.groups_o * a.n_kv * p.splits_o * a.n_seqs);
+    const int64_t n_out = (int64_t)a.rows_p * a.n_kv;
+    const int nsplit = (int)(p.splits_p + p.splits_o);
     a.part_ml = a.part_o + nsplit * n_out * dim;
-    const dim3 grid((unsigned)(wgs_p + wgs_o));
-    const bool p16 = a.page.d % 16 == 0;
+    const dim3 grid((unsigned)(a.wgs_p + a.wgs_o));
+    const bool p16 = a.page.d % 16 == 0 && (!p.joint || a.prefix_len % 16 == 0);
     auto run = [&](auto ctag, auto d, auto rt) -> hipError_t {
         using CT = decltype(ctag);
-        constexpr int D = decltype(d)::value, RT = decltype(rt)::value;
-        if (grid.x) {
-            if (p16) attn_rows<CT, D, RT, true><<<grid, 256, 0, s>>>(a);
-            else attn_rows<CT, D, RT, false><<<grid, 256, 0, s>>>(a);
-            const hipError_t e = hipGetLastError();
-            if (e != hipSuccess) return e;
-        }
-        if (nsplit != 1) {
-            attn_join<CT, D><<<dim3((unsigned)((n_out + 3) / 4)), 256, 0, s>>>(a);
-            return hipGetLastError();
-        }
-        return hipSuccess;
+        constexpr int D = decltype(d)::value, RT = decltype(rt)::value, W = attn_waves(D, RT);
+        if (p16) attn_rows<CT, D, RT, W, true><<<grid, 64 * W, 0, s>>>(a);
+        else attn_rows<CT, D, RT, W, false><<<grid, 64 * W, 0, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || nsplit == 1) return e;
+        attn_join<CT, D><<<dim3((unsigned)n_out), 256, 0, s>>>(a, nsplit);
+        return hipGetLastError();
     };
     auto by_rt = [&](auto ctag, auto d) -> hipError_t {
-        constexpr int big = decltype(d)::value == 256 ? 1 : decltype(d)::value == 128 ? 2 : 4;
+        constexpr int dm = decltype(d)::value, big = dm == 64 ? 4 : dm == 128 ? 2 : 1;
         if (p.row_tiles == 1) return run(ctag, d, std::integral_constant<int, 1>{});
         return run(ctag, d, std::integral_constant<int, big>{});
     };

@@ -91,20 +91,23 @@ struct AttnShared {
     const int32_t *lens;
     void *out;
     int64_t ldo;
-    float *part_o;        // [split][row][dim], row = query row * n_q + head
-    float *part_ml;       // [split][row][2]: reference exponent, sum
-    FastDiv page, group;  // tokens per page, query heads per key head
+    float *part_o;        // [row][split][dim], row = query row * n_q + head
+    float *part_ml;       // [row][split][2]: reference exponent, sum
+    FastDiv page, group, heads, queries;   // tokens per page, query heads per key head, key heads, query tokens
     float scale2;         // scale * log2(e)
     int n_seqs, n_qt, n_q, n_kv;
     int prefix_len, max_len;
     // the launch: prefix workgroups first, then own ones
-    int rows_p, groups_p, splits_p;     // rows of a key head, row groups, splits of the prefix
-    int rows_o, groups_o, splits_o;     // the same for one sequence's own keys
-    int wgs_p;
+    int rows_p, splits_p, wgs_p;           // rows of a key head, splits and workgroups of the prefix
+    int rows_o, wgs_o;                     // the same for one sequence's own keys
+    FastDiv groups_p, groups_o, splits_o, div_p;   // row groups; splits
+    int own_from, joint_len;               // first key of the own part; its keys below this are the prefix's (row 0)
+    int xcd_p;                             // row groups of the same prefix keys 8 workgroups apart
 };
 struct AttnPlan {
-    int row_tiles;                      // 16-row tiles a wave carries
-    int groups_p, splits_p, groups_o, splits_o;
+    int row_tiles, waves;                  // 16-row tiles a wave carries, waves of a workgroup
+    bool joint;                            // the own part takes the prefix too
+    int64_t groups_p, splits_p, groups_o, splits_o;
     size_t ws_bytes;
 };
 AttnPlan attn_plan(int64_t n_seqs, int64_t n_q, int64_t n_kv, int64_t dim, int64_t n_qt, int64_t prefix_len,
