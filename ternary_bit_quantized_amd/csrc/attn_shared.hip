@@ -25,10 +25,10 @@
 // spread over its four lanes until the end; f32 has room for terms up to 2^8 and the 16-bit
 // P for them too.
 //
-// Masks.  A row sees keys below its limit.  Scores past it become -inf before the maximum;
-// keys some row of the wave does not see are multiplied once per distinct limit, with
-// the value rows past that limit zeroed, so that what lies in unseen places (NaN, inf)
-// reaches no row that does not see it.  Addresses are clamped to seen keys.
+// Masks.  A row sees keys below its limit.  Scores past it become -inf before the maximum, value
+// rows nobody sees are zeroed, and tiles whose keys only some of the wave's rows see (draft tokens,
+// sequences shorter than the prefix) go through a loop of their own, so that what lies in
+// unseen places (NaN, inf) reaches no row that does not see it.  Addresses are clamped to seen keys.
 //
 // Split.  The waves of a workgroup interleave the key tiles of one split; their results join in
 // LDS, the splits' in attn_join.  Workgroups that read the same prefix keys for other rows get
@@ -57,6 +57,15 @@ struct Mma<bf16_t> {
                                                        0, 0);
     }
 };
+
+// Past every wait state of the matrix instructions before it.  The compiler inserts those that a read
+// of their results needs within a block, but was seen to leave them out at a branch's target
+// (results then came out wrong now and then); so one stands before such branches.
+__device__ __forceinline__ void settle() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15");
+    __builtin_amdgcn_sched_barrier(0);
+}
 
 constexpr int kAttnTile = 32;    // keys per step
 constexpr int kAttnMaxSplits = 32;
@@ -128,7 +137,6 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows(AttnShared
     }
     const int splits = pre ? a.splits_p : (int)a.splits_o.d;
     const int r0 = rg * RT * 16;
-    const int nrt = RT == 1 ? 1 : min(RT, (nrows - r0 + 15) / 16);
     const int tok0 = seq * a.n_qt;
 
     // a row's query (token, head) and the keys it sees
@@ -145,7 +153,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows(AttnShared
             const int len = a.lens[s];
             const int n = len - a.n_qt + 1 + (tok - s * a.n_qt);
             lim[t] = len < 0 || len > a.max_len ? 0 : max(0, pre ? min(n, a.prefix_len) : n);
-            lim_lo = min(lim_lo, lim[t]);
+            if (lim[t] > (pre ? 0 : a.own_from)) lim_lo = min(lim_lo, lim[t]);   // (of rows that see some key here)
             lim_hi = max(lim_hi, lim[t]);
         }
     }
@@ -193,7 +201,6 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows(AttnShared
 
     u32x4_t kv[2][KS];
     uint32_t vv[8][VD];
-    uint32_t bad = 0;        // keys of the loaded tile whose page does not exist
 
     // element offset of key's row, and whether its page exists
     const auto key_row = [&](int key, bool &ok) {
@@ -202,11 +209,13 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows(AttnShared
         ok = page >= 0 && page < a.n_pages;
         return (int64_t)(ok ? page : 0) * a.page_stride + (int64_t)(key - pi * psz) * a.token_stride;
     };
-    const auto load_tile = [&](int tile) {
+    // Where a tile's rows are: byte offsets of its halves (P16), or of every key in the wave's
+    // lds_row.  Returns the keys whose page does not exist.
+    int64_t base[2];
+    const auto find_tile = [&](int tile) {
         const int key0 = tile * kAttnTile;
+        uint32_t bad = 0;
         if constexpr (P16) {
-            bad = 0;
-            int64_t base[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 // a half past the last seen key reads the first half again (it is masked)
@@ -215,34 +224,33 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows(AttnShared
                 base[h] = 2 * key_row(kk, ok);
                 if (!ok) bad |= 0xffffu << (16 * h);
             }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    kv[h][k] = *reinterpret_cast<const u32x4_t *>(kbase + base[h] + (2 * (j * ts + 8 * g) + 64 * k));
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                load_dwords<VD>(vbase + base[i / 4] + 2 * ((4 * g + i % 4) * ts + DPL * j), vv[i]);
         } else {
             const int key = min(max(key0 + (lane & 31), k_lo), lim_hi - 1);
             bool ok;
             const int64_t row = 2 * key_row(key, ok);
             bad = (uint32_t)__ballot(!ok);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
             if (lane < kAttnTile) lds_row[wave][lane] = row;
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
+        }
+        return bad;
+    };
+    const auto load_k = [&]() {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t b = lds_row[wave][16 * h + j];
+        for (int h = 0; h < 2; ++h) {
+            const uint8_t *kp = P16 ? kbase + base[h] + 2 * (j * ts + 8 * g) : kbase + lds_row[P16 ? 0 : wave][P16 ? 0 : 16 * h + j] + 16 * g;
 #pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    kv[h][k] = *reinterpret_cast<const u32x4_t *>(kbase + b + (16 * g + 64 * k));
-            }
+            for (int k = 0; k < KS; ++k) kv[h][k] = *reinterpret_cast<const u32x4_t *>(kp + 64 * k);
+        }
+    };
+    const auto load_v = [&]() {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                load_dwords<VD>(vbase + lds_row[wave][16 * (i / 4) + 4 * g + i % 4] + 2 * DPL * j, vv[i]);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+        for (int i = 0; i < 8; ++i) {
+            const uint8_t *vp = P16 ? vbase + base[i / 4] + 2 * ((4 * g + i % 4) * ts + DPL * j)
+                                    : vbase + lds_row[P16 ? 0 : wave][P16 ? 0 : 16 * (i / 4) + 4 * g + i % 4] + 2 * DPL * j;
+            load_dwords<VD>(vp, vv[i]);
         }
     };
     // the value tile's operand of dim e: its 8 keys' halves
@@ -254,23 +262,41 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows(AttnShared
         return r;
     };
 
-    for (int tile = ta + wave; tile < tb; tile += W) {
-        load_tile(tile);
-        const int key0 = tile * kAttnTile;
-        const bool edge = key0 < k_lo || key0 + kAttnTile > lim_lo || bad != 0;   // some score needs a mask
-        u32x4_t p[RT];
+    // This lane's part of a row tile's O in the wave's part of lds_o.
+    const auto o_to_lds = [&](int t) {
 #pragma unroll
-        for (int t = 0; t < RT; ++t) p[t] = u32x4_t{0u, 0u, 0u, 0u};
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            if (RT > 1 && t >= nrt) break;
-            float4_t s[2];
+            for (int e = 0; e < DPL; e += 4)
+                *reinterpret_cast<float4_t *>(&lds_o[wave][16 * t + j][DPL * (4 * g + i) + e]) =
+                    float4_t{o[t][e][i], o[t][e + 1][i], o[t][e + 2][i], o[t][e + 3][i]};
+    };
+    const auto o_from_lds = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < DPL; e += 4) {
+                const float4_t v = *reinterpret_cast<const float4_t *>(&lds_o[wave][16 * t + j][DPL * (4 * g + i) + e]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) o[t][e + q][i] = v[q];
+            }
+    };
+
+    const auto scores = [&](float4_t (&sc)[RT][2]) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                s[h] = float4_t{0.f, 0.f, 0.f, 0.f};
+                sc[t][h] = float4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < KS; ++k) s[h] = Mma<CT>::mul(kv[h][k], qv[t][k], s[h]);
+                for (int k = 0; k < KS; ++k) sc[t][h] = Mma<CT>::mul(kv[h][k], qv[t][k], sc[t][h]);
             }
+    };
+    // Scores to weights: masks, the running reference and sum, and P rounded.
+    const auto softmax = [&](float4_t (&sc)[RT][2], u32x4_t (&p)[RT], int key0, bool edge, uint32_t bad) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            float4_t(&s)[2] = sc[t];
             if (edge) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -307,58 +333,100 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows(AttnShared
             }
             p[t] = u32x4_t{pack2<CT>(w[0], w[1]), pack2<CT>(w[2], w[3]), pack2<CT>(w[4], w[5]), pack2<CT>(w[6], w[7])};
         }
-        if (!edge) {
+    };
+
+    // Tiles from t_split on hold keys that only some of the rows see.
+    const int t_split = lim_lo < lim_hi ? max(ta, min(tb, lim_lo / kAttnTile)) : tb;
+    int tile = ta + wave;
+    // The keys of the next tile are on their way while this one's softmax and values are worked
+    // on, its values during the next scores: one set of registers each.
+    uint32_t bad = 0, next_bad = 0;
+    if (tile < t_split) {
+        next_bad = find_tile(tile);
+        load_k();
+        load_v();
+    }
+    for (; tile < t_split; tile += W) {
+        bad = next_bad;
+        const bool more = tile + W < t_split;
+        if (more) next_bad = find_tile(tile + W);
+        const int key0 = tile * kAttnTile;
+        const bool edge = key0 < k_lo || key0 + kAttnTile > lim_hi || bad != 0;   // some key needs a mask
+        float4_t sc[RT][2];
+        u32x4_t p[RT];
+        scores(sc);
+        if (more) load_k();
+        softmax(sc, p, key0, edge, bad);
+        if (edge) {     // what nobody sees may be NaN: its value rows go
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int kk = key0 + 16 * (i / 4) + 4 * g + i % 4;
+                const bool seen = kk < lim_hi && kk >= k_lo;
+#pragma unroll
+                for (int q = 0; q < VD; ++q) vv[i][q] = seen ? vv[i][q] : 0u;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < DPL; ++e) {
+            const u32x4_t va = v_operand(e);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) o[t][e] = Mma<CT>::mul(va, p[t], o[t][e]);
+        }
+        if (more) load_v();
+    }
+    // The others, without overlap: a tile's values are multiplied once per distinct limit, lowest
+    // first, with value rows at or past it zeroed; the rows of other limits take back what they had
+    // (a zeroed P would not do: 0 * NaN reaches them).  The wave's part of lds_o holds it meanwhile.
+    for (; tile < tb; tile += W) {
+        bad = find_tile(tile);
+        const int key0 = tile * kAttnTile;
+        float4_t sc[RT][2];
+        u32x4_t p[RT];
+        load_k();
+        scores(sc);
+        softmax(sc, p, key0, true, bad);
+        load_v();
+        int done = max(key0, k_lo);             // (rows of limits up to here see nothing in this tile)
+        while (true) {
+            int cur = 0x7fffffff;
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+                if (lim[t] > done) cur = min(cur, lim[t]);
+            cur = __builtin_amdgcn_readfirstlane(row_min(cur));
+            if (cur == 0x7fffffff) break;
+            done = cur;
+            uint32_t keep[4];                   // per pair of keys: which halves stay
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int k0 = key0 + 16 * (q / 2) + 4 * g + 2 * (q % 2);
+                keep[q] = (k0 < cur && k0 >= k_lo ? 0xffffu : 0u) | (k0 + 1 < cur && k0 + 1 >= k_lo ? 0xffff0000u : 0u);
+            }
+#pragma unroll
+            for (int t = 0; t < RT; ++t) o_to_lds(t);
 #pragma unroll
             for (int e = 0; e < DPL; ++e) {
-                const u32x4_t va = v_operand(e);
+                u32x4_t va = v_operand(e);
 #pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    if (RT > 1 && t >= nrt) break;
-                    o[t][e] = Mma<CT>::mul(va, p[t], o[t][e]);
-                }
+                for (int q = 0; q < 4; ++q) va[q] &= keep[q];
+#pragma unroll
+                for (int t = 0; t < RT; ++t) o[t][e] = Mma<CT>::mul(va, p[t], o[t][e]);
             }
-        } else {
-            // once per distinct limit, lowest first, with value rows at or past it zeroed; only
-            // rows of that limit take the result
-            int done = -1;
-            while (true) {
-                int cur = 0x7fffffff;
+            settle();
 #pragma unroll
-                for (int t = 0; t < RT; ++t)
-                    if ((RT == 1 || t < nrt) && lim[t] > done) cur = min(cur, lim[t]);
-                cur = __builtin_amdgcn_readfirstlane(row_min(cur));
-                if (cur == 0x7fffffff) break;
-                done = cur;
-                if (cur <= key0) continue;      // these rows see nothing here
-                uint32_t keep[4];               // per pair of keys: which halves stay
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int k0 = key0 + 16 * (q / 2) + 4 * g + 2 * (q % 2);
-                    keep[q] = (k0 < cur && k0 >= k_lo ? 0xffffu : 0u) | (k0 + 1 < cur && k0 + 1 >= k_lo ? 0xffff0000u : 0u);
-                }
-#pragma unroll
-                for (int e = 0; e < DPL; ++e) {
-                    u32x4_t va = v_operand(e);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) va[q] &= keep[q];
-#pragma unroll
-                    for (int t = 0; t < RT; ++t) {
-                        // (a selected result, not a zeroed P: 0 * NaN would reach the other rows; and no
-                        // branch on t between: the compiler leaves out the wait states from a matrix
-                        // instruction to a read of its result at a branch's target)
-                        const float4_t r = Mma<CT>::mul(va, p[t], o[t][e]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[t][e][i] = lim[t] == cur ? r[i] : o[t][e][i];
-                    }
-                }
-            }
+            for (int t = 0; t < RT; ++t)
+                if (lim[t] != cur) o_from_lds(t);
         }
     }
 
     // join the waves' results
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-        if (RT > 1 && t >= nrt) break;
+        if (lim[t] <= k_lo || m[t] == -__builtin_inff()) {   // no key seen: what was added up is not data
+            m[t] = -__builtin_inff();
+            l[t] = 0.f;
+#pragma unroll
+            for (int e = 0; e < DPL; ++e) o[t][e] = float4_t{0.f, 0.f, 0.f, 0.f};
+        }
         float lt = l[t];
         lt += __shfl_xor(lt, 16);
         lt += __shfl_xor(lt, 32);
@@ -366,12 +434,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows(AttnShared
             lds_m[wave][16 * t + j] = m[t];
             lds_l[wave][16 * t + j] = lt;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < DPL; e += 4)
-                *reinterpret_cast<float4_t *>(&lds_o[wave][16 * t + j][DPL * (4 * g + i) + e]) =
-                    float4_t{o[t][e][i], o[t][e + 1][i], o[t][e + 2][i], o[t][e + 3][i]};
+        o_to_lds(t);
     }
     __syncthreads();
     const int rows_here = min(nrows - r0, RT * 16);
@@ -482,7 +545,7 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t n_q, int64_t n_kv, int64_t dim, int64
     };
     // Short and few: one workgroup per sequence and key head takes all keys, prefix included
     // (read once per sequence, from the L2), and writes the result itself: no join.
-    const int big = dim == 64 ? 4 : dim == 128 ? 2 : 1;
+    const int big = dim == 256 ? 1 : 2;
     p.row_tiles = rows_o <= 16 ? 1 : big;
     p.waves = attn_waves(dim, p.row_tiles);
     p.joint = prefix_len > 0 && tiles(max_len) <= 5 * p.waves && n_seqs * n_kv * groups(rows_o) <= 256;
@@ -534,7 +597,7 @@ hipError_t launch_attn_shared(AttnShared a, const AttnPlan &p, Act ct, int dim, 
         return hipGetLastError();
     };
     auto by_rt = [&](auto ctag, auto d) -> hipError_t {
-        constexpr int dm = decltype(d)::value, big = dm == 64 ? 4 : dm == 128 ? 2 : 1;
+        constexpr int big = decltype(d)::value == 256 ? 1 : 2;
         if (p.row_tiles == 1) return run(ctag, d, std::integral_constant<int, 1>{});
         return run(ctag, d, std::integral_constant<int, big>{});
     };
