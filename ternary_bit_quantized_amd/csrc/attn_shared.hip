@@ -6,36 +6,43 @@
 // unnormalised O_r (f32) of its rows; two results over different keys join as
 // l = l1 2^(m1-m) + l2 2^(m2-m), O likewise, with m = max(m1, m2).
 //
-// Rows.  A key head's rows are (query token, query head of its group).  In the prefix part
-// the rows of all sequences stand together (the keys are read once for all of them), in the
-// own part those of one sequence.  A wave carries RT tiles of 16 rows.
-//
-// Keys.  A wave takes 32 keys at a time straight from the cache into the matrix cores'
-// operands, without LDS:
+// Operands.  32 keys at a time:
 //  * S^T = K Q^T (v_mfma 16x16x32): A = 16 keys x 32 dims, 16 bytes a lane, as they lie in
 //    the cache; B = Q^T, loaded once.  D: lane (row j = lane%16, g = lane/16) holds the
 //    scores of keys 4g..4g+3 of each 16-key half for row j.
 //  * O^T += V^T P^T: B = P^T needs, in lane (j, g), 8 keys of row j: exactly the two
 //    halves' scores of that lane, rounded.  A = V^T takes the same 8 keys {4g+i, 16+4g+i} of
-//    dims d = DPL*c + e (c = lane%16, one MFMA per e): a lane loads DPL consecutive dims
-//    of those 8 value rows (full rows across the 16 lanes) and pairs keys up with one
-//    v_perm_b32 a dword.
+//    dims d = DPL*c + e (c = lane%16, one MFMA per e): a lane holds DPL consecutive dims
+//    of those 8 value rows and pairs keys up with one v_perm_b32 a dword.
 // So a score never leaves its lane: no lane exchange per step.  The reference m_r is only
 // raised when some score passes it by 2^8 (a ballot decides), and the sum of a row stays
 // spread over its four lanes until the end; f32 has room for terms up to 2^8 and the 16-bit
 // P for them too.
 //
+// A key head's rows are (query token, query head of its group).  Two parts, one launch:
+//  * own keys (own_part): a workgroup takes up to 16 rows of one sequence; its waves take
+//    different key tiles, straight from the cache into operand registers (full 256-byte value
+//    rows, 64-byte pieces of key rows), the next tile's keys on their way during the softmax and
+//    its values during the next scores.  HBM-bound with enough sequences.
+//  * the prefix (prefix_part), where the rows of all sequences stand together: the waves take
+//    different rows (16 RTP each) of the same key tiles, which go to LDS once per workgroup by
+//    16-byte LDS-DMA loads, two tiles ahead, one barrier a tile.  A key row's 16-byte pieces
+//    sit XOR-swizzled by its number, so that the 16 rows of an operand read meet 16 different
+//    bank groups.  (Key operands straight from the cache touch 64 lines an instruction, 16 rows
+//    x 4 pieces: with every wave reading them so, the L1's tag rate held 64 sequences over
+//    32768 keys at 123 us.)  Issue-bound: ~150 VALU instructions per 32 keys x 32 rows.
+//    Few rows, or a short prefix of few sequences, go the own part's way instead.
+// Workgroups that read the same prefix keys for other rows get launch numbers 8 apart: the same XCD,
+// whose L2 then serves all but one of them.  Splits of the key axis join in attn_join.
+//
 // Masks.  A row sees keys below its limit.  Scores past it become -inf before the maximum, value
-// rows nobody sees are zeroed, and tiles whose keys only some of the wave's rows see (draft tokens,
+// rows nobody sees are zeroed, and tiles whose keys only some of a wave's rows see (draft tokens,
 // sequences shorter than the prefix) go through a loop of their own, so that what lies in
 // unseen places (NaN, inf) reaches no row that does not see it.  Addresses are clamped to seen keys.
-//
-// Split.  The waves of a workgroup interleave the key tiles of one split; their results join in
-// LDS, the splits' in attn_join.  Workgroups that read the same prefix keys for other rows get
-// launch numbers 8 apart: the same XCD, whose L2 then serves all but one of them.
 #include <type_traits>
 
 #include "layer_common.h"
+#include "lds_dma.h"
 
 namespace q2_0 {
 
@@ -98,382 +105,595 @@ __device__ __forceinline__ void load_dwords(const uint8_t *p, uint32_t *v) {
     }
 }
 
-// W: waves.  P16: page_size % 16 == 0 (and the keys start at a multiple of 16, or are all of one page
-// table row), so that the 16 keys of a half tile lie in one page and its page number is read
-// once for the wave; otherwise 32 lanes look up a key each and pass the rows round through LDS.
-template <typename CT, int D, int RT, int W, bool P16>
-__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows(AttnShared a) {
-    constexpr int KS = D / 32;       // 32-dim steps of a score
-    constexpr int DPL = D / 16;      // dims per lane of a value row
-    constexpr int VD = DPL / 2;      // dwords of those
-    constexpr int OS = D + 4;        // LDS floats per row
+// Waves of a workgroup.  With a prefix part 4, so that two workgroups share a CU and are not in step: one's
+// softmax then runs beside the other's matrix instructions.  Without, 8 (one sequence's keys are read
+// by more waves), or 4 where a wave needs more than half a SIMD's registers.
+constexpr int attn_waves(int dim, bool prefix) { return dim < 256 && !prefix ? 8 : 4; }
 
-    __shared__ __attribute__((aligned(16))) float lds_o[W][RT * 16][OS];
-    __shared__ float lds_m[W][RT * 16], lds_l[W][RT * 16];
-    __shared__ int64_t lds_row[P16 ? 1 : W][P16 ? 1 : kAttnTile];
+// The page table through the scalar cache (uniform index).
+__device__ __forceinline__ int table_at(const int32_t *t, int i) {
+    typedef const __attribute__((address_space(4))) int32_t *ConstPtr;
+    return ((ConstPtr)(uintptr_t)t)[i];
+}
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int j = lane & 15, g = lane >> 4;
+// What a wave knows of its rows, RT tiles of 16, and holds of their results.
+template <typename CT, int D, int RT>
+struct Rows {
+    static constexpr int KS = D / 32;       // 32-dim steps of a score
+    static constexpr int DPL = D / 16;      // dims per lane of a value row
+    static constexpr int VD = DPL / 2;      // dwords of those
+    static constexpr int OS = D + 4;        // LDS floats per row
 
-    // this workgroup's part: prefix (all sequences' rows) or one sequence's own keys
-    const bool pre = (int)blockIdx.x < a.wgs_p;
-    const int nrows = pre ? a.rows_p : a.rows_o;
-    int rg, kvh, split, seq = 0;
-    if (pre) {
-        const int id = blockIdx.x, x = a.xcd_p ? id & 7 : 0, y = a.xcd_p ? id >> 3 : id;
-        int u = a.groups_p.div((uint32_t)y);
-        rg = y - u * (int)a.groups_p.d;
-        if (a.xcd_p) u = u * 8 + x;
-        split = a.heads.div((uint32_t)u);
-        kvh = u - split * a.n_kv;
-    } else {
-        const int id = (int)blockIdx.x - a.wgs_p;
-        int u = a.groups_o.div((uint32_t)id);
-        rg = id - u * (int)a.groups_o.d;
-        int v = a.heads.div((uint32_t)u);
-        kvh = u - v * a.n_kv;
-        seq = a.splits_o.div((uint32_t)v);
-        split = v - seq * (int)a.splits_o.d;
-    }
-    const int splits = pre ? a.splits_p : (int)a.splits_o.d;
-    const int r0 = rg * RT * 16;
-    const int tok0 = seq * a.n_qt;
-
-    // a row's query (token, head) and the keys it sees
-    const int grp = (int)a.group.d;
-    const auto row_token = [&](int r) { return tok0 + a.group.div((uint32_t)r); };
-    int lim[RT];
-    int lim_lo = 0x7fffffff, lim_hi = 0;
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        const int r = r0 + 16 * t + j;
-        lim[t] = 0;
-        if (r < nrows) {
-            const int tok = row_token(r), s = a.queries.div((uint32_t)tok);
-            const int len = a.lens[s];
-            const int n = len - a.n_qt + 1 + (tok - s * a.n_qt);
-            lim[t] = len < 0 || len > a.max_len ? 0 : max(0, pre ? min(n, a.prefix_len) : n);
-            if (lim[t] > (pre ? 0 : a.own_from)) lim_lo = min(lim_lo, lim[t]);   // (of rows that see some key here)
-            lim_hi = max(lim_hi, lim[t]);
-        }
-    }
-    lim_lo = __builtin_amdgcn_readfirstlane(row_min(lim_lo));
-    lim_hi = __builtin_amdgcn_readfirstlane(-row_min(-lim_hi));
-
-    // key tiles of this split: tiles [ta, tb) of the part's keys [k_lo, lim_hi)
-    const int k_lo = pre ? 0 : a.own_from;
-    const int t_first = k_lo / kAttnTile;
-    const int t_end = lim_hi > k_lo ? (lim_hi + kAttnTile - 1) / kAttnTile : t_first;
-    const int ntile = t_end - t_first;
-    const int per = splits == 1 ? ntile : (pre ? a.div_p : a.splits_o).div((uint32_t)(ntile + splits - 1));
-    const int ta = t_first + min(ntile, per * split), tb = t_first + min(ntile, per * (split + 1));
-
-    // queries as the scores' B operand
-    u32x4_t qv[RT][KS];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        const int r = r0 + 16 * t + j;
-        const bool in = r < nrows;
-        const int tok = in ? row_token(r) : 0;
-        const int head = kvh * grp + (in ? r - (tok - tok0) * grp : 0);
-        const uint8_t *qp = static_cast<const uint8_t *>(a.q) + 2 * ((int64_t)tok * a.ldq + (int64_t)head * D + 8 * g);
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-            qv[t][k] = in ? *reinterpret_cast<const u32x4_t *>(qp + 64 * k) : u32x4_t{0u, 0u, 0u, 0u};
-    }
-
+    u32x4_t q[RT][KS];       // queries as the scores' B operand
     float4_t o[RT][DPL];
     float m[RT], ms[RT], l[RT];   // reference (-inf: none yet), the same as a number, sum of this lane
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        m[t] = -__builtin_inff();
-        ms[t] = 0.f;
-        l[t] = 0.f;
-#pragma unroll
-        for (int e = 0; e < DPL; ++e) o[t][e] = float4_t{0.f, 0.f, 0.f, 0.f};
-    }
+    int lim[RT];             // keys row j sees
+    int lim_lo, lim_hi;      // the least (of rows that see some key past k_lo) and most of the wave's rows
+    u32x4_t k[2][KS];        // a key tile's operands
+    uint32_t v[8][VD];       // and its value rows
 
-    const int32_t *trow = a.table + (int64_t)seq * a.ld_table;
-    const uint8_t *kbase = static_cast<const uint8_t *>(a.kc) + 2 * (int64_t)kvh * a.head_stride;
-    const uint8_t *vbase = static_cast<const uint8_t *>(a.vc) + 2 * (int64_t)kvh * a.head_stride;
-    const int ts = (int)a.token_stride;
-    const int psz = (int)a.page.d;
-
-    u32x4_t kv[2][KS];
-    uint32_t vv[8][VD];
-
-    // element offset of key's row, and whether its page exists
-    const auto key_row = [&](int key, bool &ok) {
-        const int pi = a.page.div((uint32_t)key);
-        const int page = (key < a.joint_len ? a.table : trow)[pi];
-        ok = page >= 0 && page < a.n_pages;
-        return (int64_t)(ok ? page : 0) * a.page_stride + (int64_t)(key - pi * psz) * a.token_stride;
-    };
-    // Where a tile's rows are: byte offsets of its halves (P16), or of every key in the wave's
-    // lds_row.  Returns the keys whose page does not exist.
-    int64_t base[2];
-    const auto find_tile = [&](int tile) {
-        const int key0 = tile * kAttnTile;
-        uint32_t bad = 0;
-        if constexpr (P16) {
+    // Rows r0 .. of nrows; tok0: the first row's query row; key head kvh.
+    __device__ __forceinline__ void init(const AttnShared &a, int r0, int nrows, int tok0, int kvh, int k_lo, int k_hi, int j, int g) {
+        const int grp = (int)a.group.d;
+        lim_lo = 0x7fffffff, lim_hi = 0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                // a half past the last seen key reads the first half again (it is masked)
-                const int kk = key0 + 16 * h < lim_hi ? key0 + 16 * h : key0;
-                bool ok;
-                base[h] = 2 * key_row(kk, ok);
-                if (!ok) bad |= 0xffffu << (16 * h);
+        for (int t = 0; t < RT; ++t) {
+            const int r = r0 + 16 * t + j;
+            lim[t] = 0, m[t] = -__builtin_inff(), ms[t] = 0.f, l[t] = 0.f;
+#pragma unroll
+            for (int e = 0; e < DPL; ++e) o[t][e] = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) q[t][s] = u32x4_t{0u, 0u, 0u, 0u};
+            if (r < nrows) {
+                const int tr = a.group.div((uint32_t)r), tok = tok0 + tr, s = a.queries.div((uint32_t)tok);
+                const int len = a.lens[s];
+                const int n = min(k_hi, len - a.n_qt + 1 + (tok - s * a.n_qt));
+                lim[t] = len < 0 || len > a.max_len ? 0 : max(0, n);
+                if (lim[t] > k_lo) lim_lo = min(lim_lo, lim[t]);
+                lim_hi = max(lim_hi, lim[t]);
+                const uint8_t *qp = static_cast<const uint8_t *>(a.q) +
+                                    2 * ((int64_t)tok * a.ldq + (int64_t)(kvh * grp + r - tr * grp) * D + 8 * g);
+#pragma unroll
+                for (int st = 0; st < KS; ++st) q[t][st] = *reinterpret_cast<const u32x4_t *>(qp + 64 * st);
             }
-        } else {
-            const int key = min(max(key0 + (lane & 31), k_lo), lim_hi - 1);
-            bool ok;
-            const int64_t row = 2 * key_row(key, ok);
-            bad = (uint32_t)__ballot(!ok);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            if (lane < kAttnTile) lds_row[wave][lane] = row;
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
         }
-        return bad;
-    };
-    const auto load_k = [&]() {
+        lim_lo = __builtin_amdgcn_readfirstlane(row_min(lim_lo));
+        lim_hi = __builtin_amdgcn_readfirstlane(-row_min(-lim_hi));
+    }
+    __device__ __forceinline__ void scores(float4_t (&s)[2], int t) const {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint8_t *kp = P16 ? kbase + base[h] + 2 * (j * ts + 8 * g) : kbase + lds_row[P16 ? 0 : wave][P16 ? 0 : 16 * h + j] + 16 * g;
+            s[h] = float4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < KS; ++k) kv[h][k] = *reinterpret_cast<const u32x4_t *>(kp + 64 * k);
+            for (int i = 0; i < KS; ++i) s[h] = Mma<CT>::mul(k[h][i], q[t][i], s[h]);
         }
-    };
-    const auto load_v = [&]() {
+    }
+    // What row j does not see, and NaN for keys whose page does not exist (bad)
+    __device__ __forceinline__ void mask(float4_t (&s)[2], int t, int key0, int k_lo, uint32_t bad, int g) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int kk = 16 * h + 4 * g + i;
+                if ((bad >> kk) & 1u) s[h][i] = __builtin_nanf("");
+                if (key0 + kk >= lim[t] || key0 + kk < k_lo) s[h][i] = -__builtin_inff();
+            }
+    }
+    // Where a score passes its row's reference by 2^8: raises the rows' references to their maxima so far
+    // and rescales what they hold.
+    __device__ __forceinline__ void raise(const float4_t (&s)[2], int t, float scale2) {
+        const float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                                fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3]))) *
+                          scale2;
+        if (__ballot(top > m[t] + 8.f)) {
+            float mx = fmaxf(m[t], top);
+            mx = fmaxf(mx, __shfl_xor(mx, 16));
+            mx = fmaxf(mx, __shfl_xor(mx, 32));
+            const float mn = mx == -__builtin_inff() ? 0.f : mx;
+            const float f = m[t] == mx ? 1.f : __builtin_amdgcn_exp2f(m[t] - mn);
+            m[t] = mx;
+            ms[t] = mn;
+            l[t] *= f;
+#pragma unroll
+            for (int e = 0; e < DPL; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[t][e][i] *= f;
+        }
+    }
+    // Scores to weights: the running sum, and P rounded to the cache's type (the matrix cores' operand).
+    __device__ __forceinline__ u32x4_t weights(const float4_t (&s)[2], int t, float scale2) {
+        float w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint8_t *vp = P16 ? vbase + base[i / 4] + 2 * ((4 * g + i % 4) * ts + DPL * j)
-                                    : vbase + lds_row[P16 ? 0 : wave][P16 ? 0 : 16 * (i / 4) + 4 * g + i % 4] + 2 * DPL * j;
-            load_dwords<VD>(vp, vv[i]);
+            w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 4][i % 4], scale2, -ms[t]));
+            l[t] += w[i];
         }
-    };
+        return u32x4_t{pack2<CT>(w[0], w[1]), pack2<CT>(w[2], w[3]), pack2<CT>(w[4], w[5]), pack2<CT>(w[6], w[7])};
+    }
     // the value tile's operand of dim e: its 8 keys' halves
-    const auto v_operand = [&](int e) {
+    __device__ __forceinline__ u32x4_t v_operand(int e) const {
         const uint32_t sel = (e & 1) ? 0x07060302u : 0x05040100u;
         u32x4_t r;
 #pragma unroll
-        for (int p = 0; p < 4; ++p) r[p] = __builtin_amdgcn_perm(vv[2 * p + 1][e / 2], vv[2 * p][e / 2], sel);
+        for (int i = 0; i < 4; ++i) r[i] = __builtin_amdgcn_perm(v[2 * i + 1][e / 2], v[2 * i][e / 2], sel);
         return r;
-    };
-
-    // This lane's part of a row tile's O in the wave's part of lds_o.
-    const auto o_to_lds = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < DPL; e += 4)
-                *reinterpret_cast<float4_t *>(&lds_o[wave][16 * t + j][DPL * (4 * g + i) + e]) =
-                    float4_t{o[t][e][i], o[t][e + 1][i], o[t][e + 2][i], o[t][e + 3][i]};
-    };
-    const auto o_from_lds = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < DPL; e += 4) {
-                const float4_t v = *reinterpret_cast<const float4_t *>(&lds_o[wave][16 * t + j][DPL * (4 * g + i) + e]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) o[t][e + q][i] = v[q];
-            }
-    };
-
-    const auto scores = [&](float4_t (&sc)[RT][2]) {
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                sc[t][h] = float4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int k = 0; k < KS; ++k) sc[t][h] = Mma<CT>::mul(kv[h][k], qv[t][k], sc[t][h]);
-            }
-    };
-    // Scores to weights: masks, the running reference and sum, and P rounded.
-    const auto softmax = [&](float4_t (&sc)[RT][2], u32x4_t (&p)[RT], int key0, bool edge, uint32_t bad) {
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            float4_t(&s)[2] = sc[t];
-            if (edge) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int kk = 16 * h + 4 * g + i;
-                        if ((bad >> kk) & 1u) s[h][i] = __builtin_nanf("");
-                        if (key0 + kk >= lim[t] || key0 + kk < k_lo) s[h][i] = -__builtin_inff();
-                    }
-            }
-            const float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                                    fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3]))) *
-                              a.scale2;
-            if (__ballot(top > m[t] + 8.f)) {
-                // raise the rows' references to their maxima so far and rescale what they hold
-                float mx = fmaxf(m[t], top);
-                mx = fmaxf(mx, __shfl_xor(mx, 16));
-                mx = fmaxf(mx, __shfl_xor(mx, 32));
-                const float mn = mx == -__builtin_inff() ? 0.f : mx;
-                const float f = m[t] == mx ? 1.f : __builtin_amdgcn_exp2f(m[t] - mn);
-                m[t] = mx;
-                ms[t] = mn;
-                l[t] *= f;
-#pragma unroll
-                for (int e = 0; e < DPL; ++e)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[t][e][i] *= f;
-            }
-            float w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 4][i % 4], a.scale2, -ms[t]));
-                l[t] += w[i];
-            }
-            p[t] = u32x4_t{pack2<CT>(w[0], w[1]), pack2<CT>(w[2], w[3]), pack2<CT>(w[4], w[5]), pack2<CT>(w[6], w[7])};
-        }
-    };
-
-    // Tiles from t_split on hold keys that only some of the rows see.
-    const int t_split = lim_lo < lim_hi ? max(ta, min(tb, lim_lo / kAttnTile)) : tb;
-    int tile = ta + wave;
-    // The keys of the next tile are on their way while this one's softmax and values are worked
-    // on, its values during the next scores: one set of registers each.
-    uint32_t bad = 0, next_bad = 0;
-    if (tile < t_split) {
-        next_bad = find_tile(tile);
-        load_k();
-        load_v();
     }
-    for (; tile < t_split; tile += W) {
-        bad = next_bad;
-        const bool more = tile + W < t_split;
-        if (more) next_bad = find_tile(tile + W);
-        const int key0 = tile * kAttnTile;
-        const bool edge = key0 < k_lo || key0 + kAttnTile > lim_hi || bad != 0;   // some key needs a mask
-        float4_t sc[RT][2];
-        u32x4_t p[RT];
-        scores(sc);
-        if (more) load_k();
-        softmax(sc, p, key0, edge, bad);
-        if (edge) {     // what nobody sees may be NaN: its value rows go
+    // Value rows that nobody sees may hold NaN: zeroed.
+    __device__ __forceinline__ void clear_unseen(int key0, int k_lo, int g) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int kk = key0 + 16 * (i / 4) + 4 * g + i % 4;
-                const bool seen = kk < lim_hi && kk >= k_lo;
+        for (int i = 0; i < 8; ++i) {
+            const int kk = key0 + 16 * (i / 4) + 4 * g + i % 4;
+            const bool seen = kk < lim_hi && kk >= k_lo;
 #pragma unroll
-                for (int q = 0; q < VD; ++q) vv[i][q] = seen ? vv[i][q] : 0u;
-            }
+            for (int d = 0; d < VD; ++d) v[i][d] = seen ? v[i][d] : 0u;
         }
+    }
+    // O += P V
+    __device__ __forceinline__ void values(const u32x4_t (&p)[RT]) {
 #pragma unroll
         for (int e = 0; e < DPL; ++e) {
             const u32x4_t va = v_operand(e);
 #pragma unroll
             for (int t = 0; t < RT; ++t) o[t][e] = Mma<CT>::mul(va, p[t], o[t][e]);
         }
-        if (more) load_v();
     }
-    // The others, without overlap: a tile's values are multiplied once per distinct limit, lowest
-    // first, with value rows at or past it zeroed; the rows of other limits take back what they had
-    // (a zeroed P would not do: 0 * NaN reaches them).  The wave's part of lds_o holds it meanwhile.
-    for (; tile < tb; tile += W) {
-        bad = find_tile(tile);
-        const int key0 = tile * kAttnTile;
-        float4_t sc[RT][2];
-        u32x4_t p[RT];
-        load_k();
-        scores(sc);
-        softmax(sc, p, key0, true, bad);
-        load_v();
+    // Row tile t's O in a wave's LDS area of 16 rows.
+    __device__ __forceinline__ void o_to_lds(float *area, int t, int j, int g) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < DPL; e += 4)
+                *reinterpret_cast<float4_t *>(area + j * OS + DPL * (4 * g + i) + e) =
+                    float4_t{o[t][e][i], o[t][e + 1][i], o[t][e + 2][i], o[t][e + 3][i]};
+    }
+    __device__ __forceinline__ void o_from_lds(const float *area, int t, int j, int g) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < DPL; e += 4) {
+                const float4_t w = *reinterpret_cast<const float4_t *>(area + j * OS + DPL * (4 * g + i) + e);
+#pragma unroll
+                for (int d = 0; d < 4; ++d) o[t][e + d][i] = w[d];
+            }
+    }
+    // A tile whose keys only some rows see: its values are multiplied once per distinct limit, lowest
+    // first, with value rows at or past it zeroed; the rows of other limits take back what they
+    // had (a zeroed P would not do: 0 * NaN reaches them).
+    template <typename Tile>
+    __device__ __forceinline__ void mixed_tile(const Tile &tile, int t, float scale2, int key0, int k_lo, uint32_t bad, float *area,
+                                               int j, int g) {
+        float4_t s[2];
+        tile.load_k(*this, j, g);
+        scores(s, t);
+        settle();
+        mask(s, t, key0, k_lo, bad, g);
+        raise(s, t, scale2);
+        const u32x4_t p = weights(s, t, scale2);
+        tile.load_v(*this, j, g);
         int done = max(key0, k_lo);             // (rows of limits up to here see nothing in this tile)
         while (true) {
-            int cur = 0x7fffffff;
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-                if (lim[t] > done) cur = min(cur, lim[t]);
-            cur = __builtin_amdgcn_readfirstlane(row_min(cur));
+            const int cur = __builtin_amdgcn_readfirstlane(row_min(lim[t] > done ? lim[t] : 0x7fffffff));
             if (cur == 0x7fffffff) break;
             done = cur;
             uint32_t keep[4];                   // per pair of keys: which halves stay
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int k0 = key0 + 16 * (q / 2) + 4 * g + 2 * (q % 2);
-                keep[q] = (k0 < cur && k0 >= k_lo ? 0xffffu : 0u) | (k0 + 1 < cur && k0 + 1 >= k_lo ? 0xffff0000u : 0u);
+            for (int i = 0; i < 4; ++i) {
+                const int k0 = key0 + 16 * (i / 2) + 4 * g + 2 * (i % 2);
+                keep[i] = (k0 < cur && k0 >= k_lo ? 0xffffu : 0u) | (k0 + 1 < cur && k0 + 1 >= k_lo ? 0xffff0000u : 0u);
             }
-#pragma unroll
-            for (int t = 0; t < RT; ++t) o_to_lds(t);
+            o_to_lds(area, t, j, g);
 #pragma unroll
             for (int e = 0; e < DPL; ++e) {
                 u32x4_t va = v_operand(e);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) va[q] &= keep[q];
-#pragma unroll
-                for (int t = 0; t < RT; ++t) o[t][e] = Mma<CT>::mul(va, p[t], o[t][e]);
+                for (int i = 0; i < 4; ++i) va[i] &= keep[i];
+                o[t][e] = Mma<CT>::mul(va, p, o[t][e]);
             }
             settle();
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-                if (lim[t] != cur) o_from_lds(t);
+            if (lim[t] != cur) o_from_lds(area, t, j, g);
         }
     }
+    // Row j's final reference and sum; rows that saw nothing hold nothing.
+    __device__ __forceinline__ void finish(int k_lo) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            if (lim[t] <= k_lo || m[t] == -__builtin_inff()) {
+                m[t] = -__builtin_inff();
+                l[t] = 0.f;
+#pragma unroll
+                for (int e = 0; e < DPL; ++e) o[t][e] = float4_t{0.f, 0.f, 0.f, 0.f};
+            }
+            l[t] += __shfl_xor(l[t], 16);
+            l[t] += __shfl_xor(l[t], 32);
+        }
+    }
+};
 
-    // join the waves' results
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        if (lim[t] <= k_lo || m[t] == -__builtin_inff()) {   // no key seen: what was added up is not data
-            m[t] = -__builtin_inff();
-            l[t] = 0.f;
-#pragma unroll
-            for (int e = 0; e < DPL; ++e) o[t][e] = float4_t{0.f, 0.f, 0.f, 0.f};
-        }
-        float lt = l[t];
-        lt += __shfl_xor(lt, 16);
-        lt += __shfl_xor(lt, 32);
-        if (g == 0) {
-            lds_m[wave][16 * t + j] = m[t];
-            lds_l[wave][16 * t + j] = lt;
-        }
-        o_to_lds(t);
+// Stands for rows of pages that do not exist: NaN in either type.
+__device__ const uint32_t kNanRow[4] = {0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu};
+
+// Where a key tile's rows are.  P16: the 16 keys of a half tile lie in one page (page_size % 16 == 0, and
+// the keys of a half are all of one table row), whose number is read once for the wave: byte
+// offsets of the halves.  Otherwise 32 lanes look up a key each and pass the rows round through
+// the wave's lds_row.
+template <typename CT, int D, bool P16>
+struct KeyTile {
+    const AttnShared &a;
+    const int32_t *trow;        // the sequence's table row; keys below a.joint_len are in row 0
+    const uint8_t *kbase, *vbase;
+    int64_t *lds_row;
+    int64_t base[2];
+
+    __device__ __forceinline__ int64_t row_of(int key, int page, int pi, bool &ok) const {
+        ok = page >= 0 && page < a.n_pages;
+        return 2 * ((int64_t)(ok ? page : 0) * a.page_stride + (int64_t)(key - pi * (int)a.page.d) * a.token_stride);
     }
+    __device__ __forceinline__ const int32_t *table_of(int key) const { return key < a.joint_len ? a.table : trow; }
+
+    // keys key0 .. key0 + 31 (those outside [k_lo, k_hi) are not looked up); returns the keys whose page
+    // does not exist
+    __device__ __forceinline__ uint32_t find(int key0, int k_lo, int k_hi, int lane) {
+        uint32_t bad = 0;
+        if constexpr (P16) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                // a half past the last seen key reads the first half again (it is masked)
+                const int kk = key0 + 16 * h < k_hi ? key0 + 16 * h : key0;
+                const int pi = a.page.div((uint32_t)kk);
+                bool ok;
+                base[h] = row_of(kk, table_at(table_of(kk), pi), pi, ok);
+                if (!ok) bad |= 0xffffu << (16 * h);
+            }
+        } else {
+            const int key = min(max(key0 + (lane & 31), k_lo), k_hi - 1);
+            const int pi = a.page.div((uint32_t)key);
+            bool ok;
+            const int64_t row = row_of(key, table_of(key)[pi], pi, ok);
+            bad = (uint32_t)__ballot(!ok);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            if (lane < kAttnTile) lds_row[lane] = row;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+        return bad;
+    }
+    // byte offset of row r of the tile
+    __device__ __forceinline__ int64_t row(int r) const {
+        if constexpr (P16) return (r < 16 ? base[0] : base[1]) + 2 * (r & 15) * (int)a.token_stride;
+        else return lds_row[r];
+    }
+    template <int RT>
+    __device__ __forceinline__ void load_k(Rows<CT, D, RT> &w, int j, int g) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint8_t *p = P16 ? kbase + base[h] + 2 * (j * (int)a.token_stride + 8 * g) : kbase + lds_row[16 * h + j] + 16 * g;
+#pragma unroll
+            for (int s = 0; s < D / 32; ++s) w.k[h][s] = *reinterpret_cast<const u32x4_t *>(p + 64 * s);
+        }
+    }
+    template <int RT>
+    __device__ __forceinline__ void load_v(Rows<CT, D, RT> &w, int j, int g) const {
+        constexpr int DPL = D / 16;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint8_t *p = P16 ? vbase + base[i / 4] + 2 * ((4 * g + i % 4) * (int)a.token_stride + DPL * j)
+                                   : vbase + lds_row[16 * (i / 4) + 4 * g + i % 4] + 2 * DPL * j;
+            load_dwords<DPL / 2>(p, w.v[i]);
+        }
+    }
+};
+
+// Result or partial of a row (output row tok, head): dims d .. d + 3 of split sidx.
+template <typename CT, int D>
+__device__ __forceinline__ void store_row(const AttnShared &a, int nsplit, int sidx, int tok, int head, int d, float4_t o, float m, float l) {
+    if (nsplit == 1) {
+        const int len = a.lens[a.queries.div((uint32_t)tok)];
+        const float nv = len < 0 || len > a.max_len ? __builtin_nanf("") : 0.f;
+        const float inv = 1.f / l;
+        float4_t r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = l == 0.f ? nv : o[i] * inv;
+        CT *op = static_cast<CT *>(a.out) + (int64_t)tok * a.ldo + (int64_t)head * D + d;
+        *reinterpret_cast<u32x2_t *>(op) = u32x2_t{pack2<CT>(r[0], r[1]), pack2<CT>(r[2], r[3])};
+    } else {
+        const int64_t row = ((int64_t)tok * a.n_q + head) * nsplit + sidx;
+        *reinterpret_cast<float4_t *>(a.part_o + row * D + d) = o;
+        if (d == 0) *reinterpret_cast<float2_t *>(a.part_ml + 2 * row) = float2_t{m, l};
+    }
+}
+
+// LDS of attn_rows: the waves' O areas and joint references of the own part, or the prefix part's tile
+// buffers (then its O areas); and the row tables.
+template <int D, bool PRE>
+struct AttnLds {
+    static constexpr int W = attn_waves(D, PRE), OS = D + 4;
+    static constexpr int kTileBytes = kAttnTile * D * 2;                   // keys, or values, of a tile
+    union {
+        float o[W][16][OS];
+        __attribute__((aligned(16))) uint8_t kv[2][3][PRE ? kTileBytes : 16];   // rings of keys and of values
+    };
+    float m[W][16], l[W][16];
+    int64_t row[W][kAttnTile];
+    int least[W];
+};
+
+// One sequence's own keys (or all keys, prefix included, of a joint plan): waves take different tiles.
+template <typename CT, int D, bool PRE, bool P16>
+__device__ __forceinline__ void own_part(const AttnShared &a, AttnLds<D, PRE> &lds, int id, int tid) {
+    constexpr int W = attn_waves(D, PRE);
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), j = lane & 15, g = lane >> 4;
+    int u = a.groups_o.div((uint32_t)id);
+    const int rg = id - u * (int)a.groups_o.d;
+    const int v = a.heads.div((uint32_t)u), kvh = u - v * a.n_kv;
+    const int seq = a.splits_o.div((uint32_t)v), split = v - seq * (int)a.splits_o.d;
+    const int splits = (int)a.splits_o.d, r0 = rg * 16, tok0 = seq * a.n_qt, k_lo = a.own_from;
+
+    Rows<CT, D, 1> w;
+    w.init(a, r0, a.rows_o, tok0, kvh, k_lo, 0x7fffffff, j, g);
+    // key tiles of this split: tiles [ta, tb) of the keys [k_lo, lim_hi)
+    const int t_first = k_lo / kAttnTile;
+    const int ntile = max(0, (w.lim_hi > k_lo ? (w.lim_hi + kAttnTile - 1) / kAttnTile : t_first) - t_first);
+    const int per = a.splits_o.div((uint32_t)(ntile + splits - 1));
+    const int ta = t_first + min(ntile, per * split), tb = t_first + min(ntile, per * (split + 1));
+    // tiles from t_split on hold keys that only some of the rows see
+    const int t_split = w.lim_lo < w.lim_hi ? max(ta, min(tb, w.lim_lo / kAttnTile)) : tb;
+
+    KeyTile<CT, D, P16> kt{a, a.table + (int64_t)seq * a.ld_table, static_cast<const uint8_t *>(a.kc) + 2 * (int64_t)kvh * a.head_stride,
+                           static_cast<const uint8_t *>(a.vc) + 2 * (int64_t)kvh * a.head_stride, lds.row[wave], {0, 0}};
+    int tile = ta + wave;
+    uint32_t next_bad = 0;
+    if (tile < t_split) {
+        next_bad = kt.find(tile * kAttnTile, k_lo, w.lim_hi, lane);
+        kt.load_k(w, j, g);
+        kt.load_v(w, j, g);
+    }
+    for (; tile < t_split; tile += W) {
+        const uint32_t bad = next_bad;
+        const bool more = tile + W < t_split;
+        if (more) next_bad = kt.find((tile + W) * kAttnTile, k_lo, w.lim_hi, lane);
+        const int key0 = tile * kAttnTile;
+        const bool edge = key0 < k_lo || key0 + kAttnTile > w.lim_hi || bad != 0;   // some key needs a mask
+        float4_t s[2];
+        u32x4_t p[1];
+        w.scores(s, 0);
+        if (more) kt.load_k(w, j, g);
+        if (edge) w.mask(s, 0, key0, k_lo, bad, g);
+        w.raise(s, 0, a.scale2);
+        p[0] = w.weights(s, 0, a.scale2);
+        if (edge) w.clear_unseen(key0, k_lo, g);
+        w.values(p);
+        if (more) kt.load_v(w, j, g);
+    }
+    for (; tile < tb; tile += W) {
+        const int key0 = tile * kAttnTile;
+        const uint32_t bad = kt.find(key0, k_lo, w.lim_hi, lane);
+        w.mixed_tile(kt, 0, a.scale2, key0, k_lo, bad, &lds.o[wave][0][0], j, g);
+    }
+    // join the waves' results
+    w.finish(k_lo);
+    if (g == 0) {
+        lds.m[wave][j] = w.m[0];
+        lds.l[wave][j] = w.l[0];
+    }
+    w.o_to_lds(&lds.o[wave][0][0], 0, j, g);
     __syncthreads();
-    const int rows_here = min(nrows - r0, RT * 16);
-    const int nsplit = a.splits_p + (a.wgs_o ? (int)a.splits_o.d : 0);
-    const int sidx = pre ? split : a.splits_p + split;
+    const int grp = (int)a.group.d, rows_here = min(a.rows_o - r0, 16);
+    const int nsplit = a.splits_p + splits;
 #pragma unroll 1
     for (int x = tid; x < rows_here * (D / 4); x += 64 * W) {
         const int r = x / (D / 4), d = 4 * (x % (D / 4));
         float mm = -__builtin_inff();
 #pragma unroll
-        for (int w = 0; w < W; ++w) mm = fmaxf(mm, lds_m[w][r]);
+        for (int i = 0; i < W; ++i) mm = fmaxf(mm, lds.m[i][r]);
         const float mb = mm == -__builtin_inff() ? 0.f : mm;
         float ll = 0.f;
         float4_t oo = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-        for (int w = 0; w < W; ++w) {
-            const float f = __builtin_amdgcn_exp2f(lds_m[w][r] - mb);
-            ll = __builtin_fmaf(f, lds_l[w][r], ll);
-            const float4_t v = *reinterpret_cast<const float4_t *>(&lds_o[w][r][d]);
+        for (int i = 0; i < W; ++i) {
+            const float f = __builtin_amdgcn_exp2f(lds.m[i][r] - mb);
+            ll = __builtin_fmaf(f, lds.l[i][r], ll);
+            const float4_t t = *reinterpret_cast<const float4_t *>(&lds.o[i][r][d]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) oo[i] = __builtin_fmaf(f, v[i], oo[i]);
+            for (int c = 0; c < 4; ++c) oo[c] = __builtin_fmaf(f, t[c], oo[c]);
         }
-        const int tok = row_token(r0 + r);
-        const int head = kvh * grp + (r0 + r - (tok - tok0) * grp);
-        if (nsplit == 1) {
-            const int len = a.lens[a.queries.div((uint32_t)tok)];
-            const float nv = len < 0 || len > a.max_len ? __builtin_nanf("") : 0.f;
-            const float inv = 1.f / ll;
-            float4_t res;
+        const int tr = a.group.div((uint32_t)(r0 + r));
+        store_row<CT, D>(a, nsplit, a.splits_p + split, tok0 + tr, kvh * grp + r0 + r - tr * grp, d, oo, mm, ll);
+    }
+}
+
+// The shared prefix: waves take different rows of the same tiles.
+template <typename CT, int D, int RT, bool P16>
+__device__ __forceinline__ void prefix_part(const AttnShared &a, AttnLds<D, true> &lds, int id, int tid) {
+    constexpr int W = attn_waves(D, true), kBytes = AttnLds<D, true>::kTileBytes;
+    constexpr int RI = 512 / D;              // rows of a 1 KiB load
+    constexpr int LR = D / 8;                // 16-byte pieces of a row
+    constexpr int NK = kAttnTile / RI;       // loads for a tile's keys, and as many for its values
+    constexpr int NI = 2 * NK / W;           // loads of a wave per tile
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), j = lane & 15, g = lane >> 4;
+    const int x = a.xcd_p ? id & 7 : 0;
+    int u = a.xcd_p ? id >> 3 : id;
+    const int y = a.groups_p.div((uint32_t)u), rg = u - y * (int)a.groups_p.d;
+    u = a.xcd_p ? y * 8 + x : y;
+    const int split = a.heads.div((uint32_t)u), kvh = u - split * a.n_kv;
+    const int r0 = (rg * W + wave) * RT * 16;
+
+    Rows<CT, D, RT> w;
+    w.init(a, r0, a.rows_p, 0, kvh, 0, a.prefix_len, j, g);
+    const int ntile = (a.prefix_len + kAttnTile - 1) / kAttnTile;
+    const int per = a.div_p.div((uint32_t)(ntile + a.splits_p - 1));
+    const int ta = min(ntile, per * split), tb = min(ntile, per * (split + 1));
+    // the first tile some wave's rows see differently (to the end: theirs alone)
+    if (lane == 0) lds.least[wave] = w.lim_lo < w.lim_hi ? w.lim_lo / kAttnTile : tb;
+    __syncthreads();
+    int t_split = tb;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) res[i] = ll == 0.f ? nv : oo[i] * inv;
-            CT *op = static_cast<CT *>(a.out) + (int64_t)tok * a.ldo + (int64_t)head * D + d;
-            *reinterpret_cast<u32x2_t *>(op) = u32x2_t{pack2<CT>(res[0], res[1]), pack2<CT>(res[2], res[3])};
+    for (int i = 0; i < W; ++i) t_split = min(t_split, lds.least[i]);
+    t_split = __builtin_amdgcn_readfirstlane(max(ta, t_split));
+
+    KeyTile<CT, D, P16> kt{a, a.table, static_cast<const uint8_t *>(a.kc) + 2 * (int64_t)kvh * a.head_stride,
+                           static_cast<const uint8_t *>(a.vc) + 2 * (int64_t)kvh * a.head_stride, lds.row[wave], {0, 0}};
+    // This wave's share of a tile's loads: loads q = wave NI .. + NI, of which load q covers rows RI (q % NK) ..
+    // of the keys (q < NK) or values; all lie in one half of the tile.  Lane l takes piece l % LR of row
+    // l / LR, keys' pieces swizzled.
+    const uint32_t buf0 = (uint32_t)(uintptr_t)&lds.kv[0][0][0];
+    const auto swizzle = [](int row) { return (D == 64 ? row >> 1 : row) & (LR < 16 ? LR - 1 : 15); };
+    const bool my_keys = wave * NI < NK;
+    const int row0 = wave * NI % NK * RI;
+    const uint32_t my_lds = buf0 + (uint32_t)((my_keys ? 0 : 3 * kBytes) + row0 * 2 * D);
+    const uint8_t *my_base = my_keys ? kt.kbase : kt.vbase;
+    const auto piece = [&](int i) {
+        const int row = row0 + i * RI + lane / LR, slot = lane % LR;
+        return 16 * (my_keys ? slot ^ swizzle(row) : slot);
+    };
+    // The next tile to load (P16): this wave's half's index in the table, place in the page, page number (read
+    // a tile ahead) and address.  What lies past the prefix takes its last page (and is masked).  Where a page
+    // does not exist, NaN stands for its rows.
+    int pi = 0, off = 0, page = 0;
+    bool fresh = true;                       // (a new page: the address is still to be worked out)
+    const uint8_t *src = nullptr;
+    uint32_t voff[NI];
+    const int last_pi = a.page.div((uint32_t)(a.prefix_len - 1)), psz = (int)a.page.d;
+    if constexpr (P16) {
+        const int key = ta * kAttnTile + (row0 & 16);
+        pi = a.page.div((uint32_t)key);
+        off = key - pi * psz;
+        page = table_at(a.table, min(pi, last_pi));
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            voff[i] = (uint32_t)(2 * (((row0 & 15) + i * RI + lane / LR) * (int)a.token_stride) + piece(i));
+    }
+    int next = ta;
+    const auto issue = [&](int buf) {
+        const uint32_t dst = my_lds + (uint32_t)(buf * kBytes);
+        if constexpr (P16) {
+            const bool ok = (uint32_t)page < (uint32_t)a.n_pages;
+            if (fresh) src = my_base + 2 * ((int64_t)(ok ? page : 0) * a.page_stride + (int64_t)off * a.token_stride);
+            if (ok) {
+#pragma unroll
+                for (int i = 0; i < NI; i += 2) lds_dma16x2(src, voff[i], voff[i + 1], dst + 1024 * i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NI; i += 2) lds_dma16x2(kNanRow, 0, 0, dst + 1024 * i);
+            }
+            off += kAttnTile;
+            src += 2 * kAttnTile * (int)a.token_stride;
+            fresh = off >= psz;
+            if (fresh) {
+                off -= psz, ++pi;
+                if (off >= psz) off -= psz, ++pi;    // (a page has 16 places at least)
+                page = table_at(a.table, min(pi, last_pi));
+            }
         } else {
-            const int64_t row = ((int64_t)tok * a.n_q + head) * nsplit + sidx;
-            *reinterpret_cast<float4_t *>(a.part_o + row * D + d) = oo;
-            if (d == 0) *reinterpret_cast<float2_t *>(a.part_ml + 2 * row) = float2_t{mm, ll};
+            const uint32_t bad = kt.find(next * kAttnTile, 0, a.prefix_len, lane);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int row = row0 + i * RI + lane / LR;
+                const uint8_t *p = my_base + kt.row(row) + piece(i);
+                lds_dma16((bad >> row) & 1u ? reinterpret_cast<const uint8_t *>(kNanRow) : p, dst + 1024 * i);
+            }
+        }
+        ++next;
+    };
+    // A tile's keys are needed a tile earlier than its values: its scores are worked out beside the softmax
+    // of the tile before.  So the waves that load keys are three tiles ahead, the others two.
+    const int ahead = my_keys ? 3 : 2;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        if (i < ahead && next < t_split) issue(i);
+    const auto load_k = [&](int buf) {
+        const uint8_t *kb = lds.kv[0][buf];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int s = 0; s < D / 32; ++s)
+                w.k[h][s] = *reinterpret_cast<const u32x4_t *>(kb + (16 * h + j) * 2 * D + 16 * ((4 * s + g) ^ swizzle(16 * h + j)));
+    };
+    float4_t sc[RT][2];
+    if (ta < t_split) {
+        if (my_keys && ta + 2 < t_split) wait_vmcnt<2 * NI>();
+        else wait_vmcnt<0>();
+        __syncthreads();
+        load_k(0);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) w.scores(sc[t], t);
+        settle();
+    }
+    int buf = 0;
+    for (int tile = ta; tile < t_split; ++tile) {
+        const int buf1 = buf == 2 ? 0 : buf + 1, buf2 = buf == 0 ? 2 : buf - 1;
+        // this wave's share of this tile's values (the next tile's keys) is here, its next NI loads may still be
+        // on their way ...
+        if (next > tile + ahead - 1) wait_vmcnt<NI>();
+        else wait_vmcnt<0>();
+        __syncthreads();                     // ... and everyone's; and what was here before is read
+        const int key0 = tile * kAttnTile;
+        const bool work = w.lim_hi > key0;
+        if (next < t_split) issue(my_keys ? buf : buf2);
+        if (work) {
+            load_k(buf1);                    // (past the last tile: not used)
+            const uint8_t *vb = lds.kv[1][buf];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) load_dwords<D / 32>(vb + (16 * (i / 4) + 4 * g + i % 4) * 2 * D + D / 8 * j, w.v[i]);
+            const bool edge = key0 + kAttnTile > w.lim_hi;
+            u32x4_t p[RT];
+            if (edge) {
+#pragma unroll
+                for (int t = 0; t < RT; ++t) w.mask(sc[t], t, key0, 0, 0, g);
+                w.clear_unseen(key0, 0, g);
+            }
+#pragma unroll
+            for (int t = 0; t < RT; ++t) w.raise(sc[t], t, a.scale2);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                p[t] = w.weights(sc[t], t, a.scale2);
+                w.scores(sc[t], t);          // of the next tile
+            }
+            w.values(p);
+        }
+        buf = buf1;
+    }
+    __syncthreads();                         // (the tile buffers become O areas)
+    float *area = &lds.o[wave][0][0];
+    for (int tile = t_split; tile < tb; ++tile) {
+        const int key0 = tile * kAttnTile;
+        if (w.lim_hi <= key0) break;
+        const uint32_t bad = kt.find(key0, 0, w.lim_hi, lane);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) w.mixed_tile(kt, t, a.scale2, key0, 0, bad, area, j, g);
+    }
+    w.finish(0);
+    const int grp = (int)a.group.d, nsplit = a.splits_p + (a.wgs_o ? (int)a.splits_o.d : 0);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        w.o_to_lds(area, t, j, g);
+        if (g == 0) lds.m[wave][j] = w.m[t], lds.l[wave][j] = w.l[t];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const int rows_here = min(a.rows_p - r0 - 16 * t, 16);
+#pragma unroll 1
+        for (int i = lane; i < rows_here * (D / 4); i += 64) {
+            const int r = i / (D / 4), d = 4 * (i % (D / 4)), rr = r0 + 16 * t + r;
+            const int tok = a.group.div((uint32_t)rr);
+            store_row<CT, D>(a, nsplit, split, tok, kvh * grp + rr - tok * grp, d,
+                             *reinterpret_cast<const float4_t *>(area + r * (D + 4) + d), lds.m[wave][r], lds.l[wave][r]);
         }
     }
+}
+
+// RTP: 16-row tiles of a wave in the prefix part; 0: there is none.
+template <typename CT, int D, int RTP, bool P16>
+__global__ __launch_bounds__(64 * attn_waves(D, RTP > 0), D == 256 ? 1 : 2) void attn_rows(AttnShared a) {
+    __shared__ AttnLds<D, (RTP > 0)> lds;
+    if constexpr (RTP > 0) {
+        if ((int)blockIdx.x < a.wgs_p) {
+            prefix_part<CT, D, RTP, P16>(a, lds, blockIdx.x, threadIdx.x);
+            return;
+        }
+    }
+    own_part<CT, D, (RTP > 0), P16>(a, lds, (int)blockIdx.x - a.wgs_p, threadIdx.x);
 }
 
 // Joins the splits (at most 64) of a row: a workgroup per row, D/4 lanes for a split's O.
@@ -527,38 +747,36 @@ __global__ __launch_bounds__(256) void attn_join(AttnShared a, int nsplit) {
     }
 }
 
-// 8 waves where two of them fit a SIMD's registers with one row tile each
-constexpr int attn_waves(int64_t dim, int row_tiles) { return row_tiles == 1 && dim < 256 ? 8 : 4; }
-
 AttnPlan attn_plan(int64_t n_seqs, int64_t n_q, int64_t n_kv, int64_t dim, int64_t n_qt, int64_t prefix_len,
                    int64_t max_len) {
     AttnPlan p{};
     const int64_t rows_o = n_qt * (n_q / n_kv), rows_p = n_seqs * rows_o;
     const auto tiles = [](int64_t keys) { return (keys + kAttnTile - 1) / kAttnTile; };
-    const auto groups = [&](int64_t rows) { return (rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles); };
-    // enough workgroups for the chip, but two tiles for each of a workgroup's waves
-    const auto splits = [&](int64_t units, int64_t t) {
-        int64_t s = (512 + units - 1) / units;
-        if (s > t / (2 * p.waves)) s = t / (2 * p.waves);
-        if (s > kAttnMaxSplits) s = kAttnMaxSplits;
-        return s < 1 ? (int64_t)1 : s;
+    const auto div_up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
+    const auto splits = [&](int64_t want, int64_t most) {
+        const int64_t s = want < most ? want : most;
+        return s < 1 ? (int64_t)1 : s > kAttnMaxSplits ? (int64_t)kAttnMaxSplits : s;
     };
-    // Short and few: one workgroup per sequence and key head takes all keys, prefix included
-    // (read once per sequence, from the L2), and writes the result itself: no join.
-    const int big = dim == 256 ? 1 : 2;
-    p.row_tiles = rows_o <= 16 ? 1 : big;
-    p.waves = attn_waves(dim, p.row_tiles);
-    p.joint = prefix_len > 0 && tiles(max_len) <= 5 * p.waves && n_seqs * n_kv * groups(rows_o) <= 256;
+    p.groups_o = div_up(rows_o, 16);
+    // The prefix has a part of its own unless it is of one sequence with one tile of rows, or all is
+    // short and few: then a workgroup takes all of a sequence's keys, prefix included (read once per
+    // sequence, from the L2), and writes the result itself, without a join.
+    const int64_t wgs = n_seqs * n_kv * p.groups_o;
+    p.joint = prefix_len > 0 && ((n_seqs == 1 && rows_p <= 16) ||
+                                 (tiles(max_len) <= 5 * attn_waves((int)dim, false) && wgs <= 256));
     const bool shared = prefix_len > 0 && !p.joint;
+    const int w = attn_waves((int)dim, shared);
     if (shared) {
-        p.row_tiles = rows_p <= 16 ? 1 : big;
-        p.waves = attn_waves(dim, p.row_tiles);
+        // as few rows a wave as hold them all, up to 32 (16 for 256 dims: registers)
+        p.row_tiles = dim < 256 && rows_p > 16 * w ? 2 : 1;
+        p.groups_p = div_up(rows_p, 16 * w * p.row_tiles);
+        // two workgroups a CU, each with at least four tiles
+        p.splits_p = splits(div_up(512, p.groups_p * n_kv), tiles(prefix_len) / 4);
     }
-    p.groups_p = groups(rows_p);
-    p.groups_o = groups(rows_o);
-    p.splits_p = shared ? splits(p.groups_p * n_kv, tiles(prefix_len)) : 0;
     const int64_t own = shared ? tiles(max_len) - prefix_len / kAttnTile : tiles(max_len);
-    p.splits_o = !shared || max_len > prefix_len ? (own <= 5 * p.waves ? 1 : splits(n_seqs * p.groups_o * n_kv, own)) : 0;
+    // own keys: up to five tiles a wave are taken at once; beyond, enough workgroups for the chip, two tiles
+    // a wave at least
+    if (!shared || max_len > prefix_len) p.splits_o = own <= 5 * w ? 1 : splits(div_up(512, wgs), own / (2 * w));
     const int64_t n = p.splits_p + p.splits_o;
     p.ws_bytes = n <= 1 ? 0 : (size_t)(n * rows_p * n_kv) * (size_t)(dim + 2) * 4;
     return p;
@@ -575,8 +793,8 @@ hipError_t launch_attn_shared(AttnShared a, const AttnPlan &p, Act ct, int dim, 
     a.splits_p = (int)p.splits_p;
     a.rows_o = a.n_qt * (int)a.group.d;
     a.rows_p = a.n_seqs * a.rows_o;
-    a.own_from = p.joint ? 0 : a.prefix_len;
-    a.joint_len = p.joint ? a.prefix_len : 0;
+    a.own_from = p.splits_p ? a.prefix_len : 0;
+    a.joint_len = p.joint && a.n_seqs > 1 ? a.prefix_len : 0;   // (one sequence: row 0 is its own)
     const int64_t units_p = a.n_kv * p.splits_p;
     a.xcd_p = p.groups_p > 1 && units_p % 8 == 0;
     a.wgs_p = (int)(p.groups_p * units_p);
@@ -585,26 +803,27 @@ hipError_t launch_attn_shared(AttnShared a, const AttnPlan &p, Act ct, int dim, 
     const int nsplit = (int)(p.splits_p + p.splits_o);
     a.part_ml = a.part_o + nsplit * n_out * dim;
     const dim3 grid((unsigned)(a.wgs_p + a.wgs_o));
-    const bool p16 = a.page.d % 16 == 0 && (!p.joint || a.prefix_len % 16 == 0);
-    auto run = [&](auto ctag, auto d, auto rt) -> hipError_t {
+    const bool p16 = a.page.d % 16 == 0 && a.joint_len % 16 == 0;
+    auto run = [&](auto ctag, auto d, auto rtp) -> hipError_t {
         using CT = decltype(ctag);
-        constexpr int D = decltype(d)::value, RT = decltype(rt)::value, W = attn_waves(D, RT);
-        if (p16) attn_rows<CT, D, RT, W, true><<<grid, 64 * W, 0, s>>>(a);
-        else attn_rows<CT, D, RT, W, false><<<grid, 64 * W, 0, s>>>(a);
+        constexpr int D = decltype(d)::value, RTP = decltype(rtp)::value, T = 64 * attn_waves(D, RTP > 0);
+        if (p16) attn_rows<CT, D, RTP, true><<<grid, T, 0, s>>>(a);
+        else attn_rows<CT, D, RTP, false><<<grid, T, 0, s>>>(a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || nsplit == 1) return e;
         attn_join<CT, D><<<dim3((unsigned)n_out), 256, 0, s>>>(a, nsplit);
         return hipGetLastError();
     };
-    auto by_rt = [&](auto ctag, auto d) -> hipError_t {
+    auto by_rows = [&](auto ctag, auto d) -> hipError_t {
         constexpr int big = decltype(d)::value == 256 ? 1 : 2;
+        if (p.row_tiles == 0) return run(ctag, d, std::integral_constant<int, 0>{});
         if (p.row_tiles == 1) return run(ctag, d, std::integral_constant<int, 1>{});
         return run(ctag, d, std::integral_constant<int, big>{});
     };
     auto by_dim = [&](auto ctag) -> hipError_t {
-        if (dim == 64) return by_rt(ctag, std::integral_constant<int, 64>{});
-        if (dim == 128) return by_rt(ctag, std::integral_constant<int, 128>{});
-        return by_rt(ctag, std::integral_constant<int, 256>{});
+        if (dim == 64) return by_rows(ctag, std::integral_constant<int, 64>{});
+        if (dim == 128) return by_rows(ctag, std::integral_constant<int, 128>{});
+        return by_rows(ctag, std::integral_constant<int, 256>{});
     };
     return ct == Act::F16 ? by_dim(_Float16{}) : by_dim(bf16_t{});
 }

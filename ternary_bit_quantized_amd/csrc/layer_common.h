@@ -105,7 +105,7 @@ struct AttnShared {
     int xcd_p;                             // row groups of the same prefix keys 8 workgroups apart
 };
 struct AttnPlan {
-    int row_tiles, waves;                  // 16-row tiles a wave carries, waves of a workgroup
+    int row_tiles;                         // 16-row tiles of a wave in the prefix part; 0: no such part
     bool joint;                            // the own part takes the prefix too
     int64_t groups_p, splits_p, groups_o, splits_o;
     size_t ws_bytes;
