@@ -770,8 +770,17 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t n_q, int64_t n_kv, int64_t dim, int64
         // as few rows a wave as hold them all, up to 32 (16 for 256 dims: registers)
         p.row_tiles = dim < 256 && rows_p > 16 * w ? 2 : 1;
         p.groups_p = div_up(rows_p, 16 * w * p.row_tiles);
-        // two workgroups a CU, each with at least four tiles
-        p.splits_p = splits(div_up(512, p.groups_p * n_kv), tiles(prefix_len) / 4);
+        // The number of splits weighs the tiles of one (750 ns each with a workgroup a CU, 1150 ns with two)
+        // against the splits' results (0.75 MB a us, written and read back; at 64 sequences
+        // of 32 heads 33 MB for 32 splits: 16 took 77 us, 32 took 88 us over 32768 keys, 220 and 198 us over
+        // 131072).  At least four tiles each.
+        const int64_t t = tiles(prefix_len), units = p.groups_p * n_kv, part = rows_p * n_kv * dim * 4;
+        double best = 0;
+        for (int64_t n = 1; n <= kAttnMaxSplits && (n == 1 || 4 * n <= t); ++n) {
+            const double rounds = n * units <= 256 ? 0.75 : 1.15 * (double)div_up(n * units, 512);
+            const double us = (double)div_up(t, n) * rounds + (double)(n * part) / 0.75e6;
+            if (n == 1 || us < best) best = us, p.splits_p = n;
+        }
     }
     const int64_t own = shared ? tiles(max_len) - prefix_len / kAttnTile : tiles(max_len);
     // own keys: up to five tiles a wave are taken at once; beyond, enough workgroups for the chip, two tiles
