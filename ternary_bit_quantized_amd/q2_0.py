@@ -614,8 +614,9 @@ def q2_0_moe_route(logits, n_used: int, normalise: bool = True, ids=None, weight
         ids = torch.empty((n, n_used), dtype=torch.int32, device=logits.device)
     if weights is None:
         weights = torch.empty((n, n_used), dtype=torch.float32, device=logits.device)
-    if weights.dtype != torch.float32 or weights.shape != (n, n_used) or not weights.is_contiguous():
-        raise ValueError("weights must be a contiguous float32 tensor (n_tokens, n_used)")
+    if weights.dtype != torch.float32 or weights.shape != (n, n_used) or not weights.is_cuda or \
+            not weights.is_contiguous():
+        raise ValueError("weights must be a contiguous float32 CUDA tensor (n_tokens, n_used)")
     _check(moe_route_raw(logits.data_ptr(), xt, ld, n, n_expert, n_used, int(bool(normalise)),
                          _int32(ids, (n, n_used), "ids"), weights.data_ptr(), _stream(stream)), "q2_0_moe_route")
     return ids, weights
@@ -630,11 +631,13 @@ def q2_0_moe_layer(w_gate, w_up, w_down, n_expert: int, n_ff: int, K: int, x, id
     import torch
     xp, n, ldx, xt = _xcols(x, K, "x")
     n_used = ids.shape[1]
-    if weights.dtype != torch.float32 or weights.shape != (n, n_used) or not weights.is_contiguous():
-        raise ValueError("weights must be a contiguous float32 tensor (n_tokens, n_used)")
+    if weights.dtype != torch.float32 or weights.shape != (n, n_used) or not weights.is_cuda or \
+            not weights.is_contiguous():
+        raise ValueError("weights must be a contiguous float32 CUDA tensor (n_tokens, n_used)")
     for w, name in ((w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down")):
-        if not w.is_contiguous() or w.numel() * w.element_size() < n_expert * n_ff * K // BLOCK_WEIGHTS * BLOCK_BYTES:
-            raise ValueError("%s must be contiguous and hold n_expert matrices" % name)
+        if not w.is_cuda or not w.is_contiguous() or \
+                w.numel() * w.element_size() < n_expert * n_ff * K // BLOCK_WEIGHTS * BLOCK_BYTES:
+            raise ValueError("%s must be a contiguous CUDA tensor that holds n_expert matrices" % name)
     if y is None:
         y = torch.empty((n, K), dtype=torch.float32, device=x.device)
     yp, yn, ldy = _cols(y, K, "y")
