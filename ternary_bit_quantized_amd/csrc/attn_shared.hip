@@ -309,6 +309,21 @@ struct Rows {
     }
 };
 
+// Two 16-byte LDS-DMA loads per lane (lds_dma.h) to consecutive kilobytes, with a uniform base and a byte offset per lane.
+__device__ __forceinline__ void lds_dma16x2(const void *base, uint32_t off0, uint32_t off1, uint32_t lds) {
+    uint32_t saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %4\n\t"
+        "global_load_lds_dwordx4 %1, %3\n\t"
+        "s_add_u32 m0, m0, 0x400\n\t"
+        "global_load_lds_dwordx4 %2, %3\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "v"(off0), "v"(off1), "s"(base), "s"(lds)
+        : "memory", "scc");
+}
+
 // Stands for rows of pages that do not exist: NaN in either type.
 __device__ const uint32_t kNanRow[4] = {0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu};
 

@@ -25,21 +25,6 @@ __device__ __forceinline__ void lds_dma16(const void *src, uint32_t lds) {
         : "memory");
 }
 
-// Two of them to consecutive kilobytes, with a uniform base and a byte offset per lane.
-__device__ __forceinline__ void lds_dma16x2(const void *base, uint32_t off0, uint32_t off1, uint32_t lds) {
-    uint32_t saved;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %4\n\t"
-        "global_load_lds_dwordx4 %1, %3\n\t"
-        "s_add_u32 m0, m0, 0x400\n\t"
-        "global_load_lds_dwordx4 %2, %3\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
-        : "v"(off0), "v"(off1), "s"(base), "s"(lds)
-        : "memory", "scc");
-}
-
 // s_waitcnt with only the vector-memory count set (expcnt and lgkmcnt at their maxima).
 template <int N>
 __device__ __forceinline__ void wait_vmcnt() {
