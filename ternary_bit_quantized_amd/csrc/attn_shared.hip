@@ -79,7 +79,7 @@ constexpr int kAttnMaxSplits = 32;
 
 template <int CTRL>
 __device__ __forceinline__ int dpp_int(int v) {
-    return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, false);
+    return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xf, 0xf, false);
 }
 
 // Over the 16 lanes of a DPP row (row_ror 8, 4, 2, 1).
@@ -246,19 +246,22 @@ struct Rows {
                 *reinterpret_cast<float4_t *>(area + j * OS + DPL * (4 * g + i) + e) =
                     float4_t{o[t][e][i], o[t][e + 1][i], o[t][e + 2][i], o[t][e + 3][i]};
     }
-    __device__ __forceinline__ void o_from_lds(const float *area, int t, int j, int g) {
+    // and back, where the row is to have it (a select, not a branch: see mixed_tile)
+    __device__ __forceinline__ void o_from_lds(const float *area, int t, int j, int g, bool back) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int e = 0; e < DPL; e += 4) {
                 const float4_t w = *reinterpret_cast<const float4_t *>(area + j * OS + DPL * (4 * g + i) + e);
 #pragma unroll
-                for (int d = 0; d < 4; ++d) o[t][e + d][i] = w[d];
+                for (int d = 0; d < 4; ++d) o[t][e + d][i] = back ? w[d] : o[t][e + d][i];
             }
     }
     // A tile whose keys only some rows see: its values are multiplied once per distinct limit, lowest
     // first, with value rows at or past it zeroed; the rows of other limits take back what they
-    // had (a zeroed P would not do: 0 * NaN reaches them).
+    // had (a zeroed P would not do: 0 * NaN reaches them).  Nothing in the loop branches by lane: a
+    // branch on lim == cur was carried into the next pass by the compiler, whose minimum over the rows
+    // then missed lanes and never came to an end.
     template <typename Tile>
     __device__ __forceinline__ void mixed_tile(const Tile &tile, int t, float scale2, int key0, int k_lo, uint32_t bad, float *area,
                                                int j, int g) {
@@ -271,7 +274,8 @@ struct Rows {
         const u32x4_t p = weights(s, t, scale2);
         tile.load_v(*this, j, g);
         int done = max(key0, k_lo);             // (rows of limits up to here see nothing in this tile)
-        while (true) {
+#pragma unroll 1
+        for (int pass = 0; pass < 16; ++pass) { // (16 rows: no more limits)
             const int cur = __builtin_amdgcn_readfirstlane(row_min(lim[t] > done ? lim[t] : 0x7fffffff));
             if (cur == 0x7fffffff) break;
             done = cur;
@@ -290,14 +294,15 @@ struct Rows {
                 o[t][e] = Mma<CT>::mul(va, p, o[t][e]);
             }
             settle();
-            if (lim[t] != cur) o_from_lds(area, t, j, g);
+            o_from_lds(area, t, j, g, lim[t] != cur);
         }
     }
-    // Row j's final reference and sum; rows that saw nothing hold nothing.
+    // Row j's final reference and sum; rows that saw nothing hold nothing (a row that saw nothing but NaN has
+    // no reference either, and keeps its NaN).
     __device__ __forceinline__ void finish(int k_lo) {
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            if (lim[t] <= k_lo || m[t] == -__builtin_inff()) {
+            if (lim[t] <= k_lo) {
                 m[t] = -__builtin_inff();
                 l[t] = 0.f;
 #pragma unroll

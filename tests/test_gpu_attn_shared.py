@@ -257,6 +257,85 @@ def test_empty_cache_bound():
     assert (got == 0).all()
 
 
+def shared_run(seed, n_seqs, n_qt, n_q, n_kv, dim, ct, page, prefix, own, lens=None, bad=None, **kw):
+    """As run, with a table wide enough (by a bound far above the lengths) that the prefix's rows of
+    all sequences are taken together.  bad: (sequence row of the table, column) whose page does not exist."""
+    import torch
+    q, k, v, table, ln = make(seed, n_seqs, n_qt, n_q, n_kv, dim, ct, page, prefix, own, **kw)
+    wide = torch.zeros(n_seqs, max(table.shape[1], 3000 // page + 1), dtype=torch.int32, device="cuda")
+    wide[:, : table.shape[1]] = table
+    if lens is not None:
+        ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    if bad is not None:
+        wide[bad[0], bad[1]] = 1 << 30
+    scale = dim ** -0.5
+    got = B.q2_0_attn_shared(q, k, v, wide, ln, scale, prefix_len=prefix, n_qt=n_qt)
+    assert torch.equal(got.isnan(), B.q2_0_attn_shared(q, k, v, wide, ln, scale, prefix_len=prefix, n_qt=n_qt).isnan())
+    ref, tol = reference(q, k, v, table, ln, scale, n_qt, U[ct])
+    return got, ref, tol
+
+
+@pytest.mark.parametrize("prefix", [1, 16, 31, 32, 33, 63, 64, 65, 97, 129, 300])
+@pytest.mark.parametrize("page", [16, 24, 32, 48, 64])
+def test_prefix_of_all_sequences(prefix, page):
+    check(*shared_run(20, 5, 1, 8, 1, 128, "bf16", page, prefix, [1, 2, 17, 64, 40]))
+
+
+@pytest.mark.parametrize("ct", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("n_seqs,n_qt,n_q,n_kv", [(2, 1, 4, 4), (3, 1, 16, 2), (4, 4, 4, 1), (5, 1, 13, 1), (16, 1, 8, 2), (9, 2, 8, 1),
+                                                  (33, 1, 8, 1)])
+def test_prefix_rows(ct, dim, n_seqs, n_qt, n_q, n_kv):
+    """Rows of a key head from 2 to 264: one or several waves, one or two tiles of 16 each, several workgroups."""
+    own = [n_qt + 7 * i % 60 for i in range(n_seqs)]
+    check(*shared_run(21, n_seqs, n_qt, n_q, n_kv, dim, ct, 16, 150, own))
+
+
+@pytest.mark.parametrize("prefix", [1501, 4097, 9000])
+@pytest.mark.parametrize("page", [16, 40, 256])
+def test_long_prefix(prefix, page):
+    check(*shared_run(22, 12, 1, 8, 1, 64, "f16", page, prefix, [1 + 31 * i % 300 for i in range(12)], layout="tokens"))
+
+
+@pytest.mark.parametrize("dim,n_q", [(64, 8), (128, 4), (128, 20), (256, 4)])
+@pytest.mark.parametrize("page", [16, 24])
+@pytest.mark.parametrize("hole", [float("nan"), float("inf")])
+def test_prefix_seen_in_part(dim, n_q, page, hole):
+    """Sequences that end inside the prefix, one of them empty: what they do not see, NaN there too, does not
+    count, and the others see it all."""
+    lens = [300, 1, 0, 33, 64, 95, 310, 160]
+    got, ref, tol = shared_run(23, 8, 1, n_q, 1, dim, "bf16", page, 300, [10] * 8, lens=lens)
+    check(got, ref, tol)
+    # the prefix from key 160 on is a hole, which sequences 0 and 6 alone see
+    import torch
+    q, k, v, table, _ = make(23, 8, 1, n_q, 1, dim, "bf16", page, 300, [10] * 8)
+    wide = torch.zeros(8, 3000 // page + 1, dtype=torch.int32, device="cuda")
+    wide[:, : table.shape[1]] = table
+    tab = table.cpu().numpy()
+    for i in range(160, 300):
+        k[int(tab[0][i // page]), :, i % page] = hole
+        v[int(tab[0][i // page]), :, i % page] = hole
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    holed = B.q2_0_attn_shared(q, k, v, wide, ln, dim ** -0.5, prefix_len=300)
+    rows = [1, 2, 3, 4, 5, 7]
+    check(holed[rows], ref[rows], tol[rows])
+    if hole != hole:
+        assert holed[[0, 6]].isnan().all()
+
+
+@pytest.mark.parametrize("page", [16, 24, 32, 64])
+@pytest.mark.parametrize("col", [0, 1, 3, 4])
+def test_bad_page_in_the_prefix(page, col):
+    """A prefix page that does not exist: NaN where a query sees one of its tokens, the others as ever."""
+    first = col * page
+    lens = [300 + 5 * i for i in range(6)] + [first, first + 1]
+    got, ref, tol = shared_run(24, 8, 1, 8, 1, 128, "bf16", page, 300, [5 * i + 1 for i in range(8)], lens=lens, bad=(0, col))
+    sees = [n > first for n in lens]
+    assert got[sees].isnan().all()
+    rest = [not s for s in sees]
+    check(got[rest], ref[rest], tol[rest])
+
+
 def test_row_strides_and_streams():
     """Strided q rows, and a call on another stream than the tensors' own."""
     import torch

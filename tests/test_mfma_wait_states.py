@@ -96,3 +96,66 @@ def test_wait_states(src, tmp_path):
         total += n
         bad += ["%s: %s" % (name, x) for x in b]
     assert total > 0 and not bad, "\n".join(bad[:20])
+
+
+def masked_loops(body):
+    """(number, lane mask changes) of the shortest cycles of the control flow through a row minimum (row_ror):
+    with lanes masked it misses what is in another pass of the loop."""
+    blocks, names = [[]], {}
+    for line in body:
+        t = line.split(";")[0].strip()
+        if re.match(r"^\.LBB\w+:$", t):
+            blocks.append([])
+            names[t[:-1]] = len(blocks) - 1
+        elif re.match(r"^[a-z]", t):
+            blocks[-1].append(t)
+            if t.startswith("s_cbranch"):
+                blocks.append([])
+    nexts = []
+    for i, b in enumerate(blocks):
+        last = b[-1] if b else ""
+        to = [names[last.split()[1]]] if re.match(r"^s_c?branch", last) else []
+        if not last.startswith(("s_branch", "s_endpgm")) and i + 1 < len(blocks):
+            to.append(i + 1)
+        nexts.append(to)
+    loops, changes = 0, []
+    for start, b in enumerate(blocks):
+        if not any("row_ror" in x for x in b):
+            continue
+        came, queue = {}, [start]
+        while queue and start not in came:
+            at = queue.pop(0)
+            for to in nexts[at]:
+                if to not in came:
+                    came[to] = at
+                    queue.append(to)
+        if start in came:
+            loops += 1
+            at = start
+            while True:
+                changes += [x for x in blocks[at] if re.match(r"^s_\w+ exec,|^s_\w+_saveexec", x)]
+                at = came[at]
+                if at == start:
+                    break
+    return loops, changes
+
+
+def test_a_masked_loop_is_found():
+    loop = [".LBB0_1:", "\tv_min_i32_dpp v1, v1, v1 row_ror:8 row_mask:0xf bank_mask:0xf", "\ts_cbranch_scc0 .LBB0_1"]
+    assert masked_loops(loop) == (1, [])
+    loop[2:2] = ["\ts_andn2_b64 exec, exec, s[2:3]"]
+    assert len(masked_loops(loop)[1]) == 1
+
+
+def test_the_loop_over_limits_has_all_its_lanes(tmp_path):
+    out = str(tmp_path / "k.s")
+    r = subprocess.run([BUILD.HIPCC, *BUILD.FLAGS, "--cuda-device-only", "-S", os.path.join(BUILD.CSRC, "attn_shared.hip"), "-o", out],
+                       capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
+    kernels = 0
+    for name, body in functions(open(out).read()):
+        if "attn_rows" in name:
+            loops, bad = masked_loops(body)
+            kernels += 1
+            assert loops >= 1 and not bad, (name, loops, bad[:3])
+    assert kernels
