@@ -336,6 +336,38 @@ def test_bad_page_in_the_prefix(page, col):
     check(got[rest], ref[rest], tol[rest])
 
 
+@pytest.mark.parametrize("page", [16, 24])
+@pytest.mark.parametrize("prefix", [0, 100, 2000])
+def test_pages_past_32_bits(page, prefix):
+    """Pages whose elements lie past 2^31 in the pool: written by the append, read by the attention."""
+    import torch
+    n_kv, dim, seqs = 8, 128, 4
+    lens = [prefix + n for n in (1, 17, 40, 90)]
+    cols = -(-max(lens) // page)
+    shared = prefix // page
+    need = shared + seqs * (cols - shared)
+    n_pages = 2 ** 32 // (n_kv * page * dim) + need + 1              # 8 GiB a pool; the last pages are used
+    k, v = (torch.empty(n_pages, n_kv, page, dim, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    own = n_pages - 1 - torch.arange(need, device="cuda")
+    table = torch.cat([own[:shared].expand(seqs, -1), own[shared:].view(seqs, -1)], 1).to(torch.int32).contiguous()
+    g = torch.Generator(device="cuda").manual_seed(30)
+    seq = torch.cat([torch.full((n,), s) for s, n in enumerate(lens)]).to(torch.int32).cuda()
+    pos = torch.cat([torch.arange(n) for n in lens]).to(torch.int32).cuda()
+    first = torch.randn(max(lens), 2, n_kv * dim, generator=g, device="cuda")[pos.long()]        # alike at equal positions
+    B.q2_0_kv_append(k, v, table, seq, pos, first[:, 0].contiguous(), first[:, 1].contiguous())
+    q = torch.randn(seqs, 2 * n_kv * dim, generator=g, device="cuda").bfloat16()
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = B.q2_0_attn_shared(q, k, v, table, ln, dim ** -0.5, prefix_len=prefix)
+    small = (table - (n_pages - need)).contiguous()
+    ks, vs = k[n_pages - need:].clone(), v[n_pages - need:].clone()
+    kept = torch.zeros(need, page, dtype=torch.bool, device="cuda")
+    kept[small[seq.long(), (pos // page).long()].long(), (pos % page).long()] = True
+    for t in (ks, vs):
+        t.transpose(1, 2)[~kept] = 0
+    ref, tol = reference(q, ks, vs, small, ln, dim ** -0.5, 1, U["bf16"])
+    check(got, ref, tol)
+
+
 def test_row_strides_and_streams():
     """Strided q rows, and a call on another stream than the tensors' own."""
     import torch

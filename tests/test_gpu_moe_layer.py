@@ -237,6 +237,74 @@ def test_layer_nan_token_stays_alone():
     assert np.all(np.abs(got - y)[[0, 2]] <= tol[[0, 2]])
 
 
+@pytest.mark.parametrize("tokens", [1, 33])
+def test_layer_outlier_at_the_limit(tokens):
+    """One activation so large that max|x| sum|W| is 0.9 of the 2^12 times sum|W x| of every row that the fixed-point
+    contract allows: where its weight is 0 the other products keep their accuracy."""
+    ff, K, ne = 64, 128, 3
+    rng = np.random.default_rng(40)
+
+    def mat(rows, cols):                       # the first column's weights 0, the others +-1 by the same scale
+        codes = rng.choice([0, 2], size=(ne * rows, cols)).astype(np.uint8)
+        codes[:, 0] = 1
+        return synth.pack(codes, np.full((ne * rows, cols // 64), 0.05, np.float16)).reshape(ne, rows, -1)
+
+    wg, wu, wd = mat(ff, K), mat(ff, K), mat(K, ff)
+    x = rng.uniform(0.5, 1.0, (tokens, K)).astype(np.float32)
+    # sum|W| = 127 * 0.05, sum|W x| >= 127 * 0.05 * 0.5
+    x[:, 0] = 0.9 * 2.0 ** 12 * 0.5
+    ids = rng.integers(0, ne, (tokens, 2)).astype(np.int32)
+    w = rng.dirichlet(np.ones(2), tokens).astype(np.float32)
+    got = B.q2_0_moe_layer(dev(wg), dev(wu), dev(wd), ne, ff, K, dev(x), dev(ids), dev(w)).double().cpu().numpy()
+    y, tol = layer(wg, wu, wd, ff, K, x, ids, w)
+    assert np.all(np.abs(got - y) <= tol), np.max(np.abs(got - y) / tol)
+
+
+def test_layer_weights_past_32_bits():
+    """Experts that lie more than 4 GiB into their tensors give what they give in small ones."""
+    import torch
+    ff, K, ne = 1024, 4096, 3700                       # 1.18 MB an expert's matrix, 4.4 GB in all
+    nb = ff * K // 64 * 18
+    wg, wu, wd = (experts(50 + i, 2, *s) for i, s in enumerate(((ff, K), (ff, K), (K, ff))))
+    big = []
+    for w in (wg, wu, wd):
+        b = torch.zeros(ne * nb, dtype=torch.uint8, device="cuda")
+        b[(ne - 2) * nb:] = dev(w.reshape(-1))
+        big.append(b)
+    assert (ne - 2) * nb > 2 ** 32
+    for tokens in (1, 40):
+        x = dev(synth.activations(51, 0, 0, tokens, K))
+        ids = torch.zeros(tokens, 2, dtype=torch.int32, device="cuda")
+        ids[:, 1] = 1
+        w = torch.full((tokens, 2), 0.5, device="cuda")
+        small = B.q2_0_moe_layer(dev(wg), dev(wu), dev(wd), 2, ff, K, x, ids, w)
+        got = B.q2_0_moe_layer(*big, ne, ff, K, x, ids + (ne - 2), w)
+        if tokens == 1:
+            assert torch.equal(got, small)
+        else:                                           # (the larger expert count may take fewer pairs a pass)
+            size = small.abs().max()
+            assert (got - small).abs().max() <= 2e-6 * size
+
+
+def test_layer_and_choice_on_another_stream():
+    import torch
+    ff, K, ne = 128, 192, 6
+    wg, wu, wd = (dev(experts(60 + i, ne, *s)) for i, s in enumerate(((ff, K), (ff, K), (K, ff))))
+    x = dev(synth.activations(60, 0, 0, 33, K))
+    logits = dev(synth.activations(61, 0, 0, 33, 64))[:, :ne].contiguous()
+    want_ids, want_w = B.q2_0_moe_route(logits, 2)
+    want = B.q2_0_moe_layer(wg, wu, wd, ne, ff, K, x, want_ids, want_w)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    ids, w = (torch.empty_like(t) for t in (want_ids, want_w))
+    y = torch.empty_like(want)
+    ws = torch.empty(B.moe_layer_workspace_bytes(ff, K, 2, 33), dtype=torch.uint8, device="cuda")
+    B.q2_0_moe_route(logits, 2, ids=ids, weights=w, stream=st.cuda_stream)
+    B.q2_0_moe_layer(wg, wu, wd, ne, ff, K, x, ids, w, y=y, workspace=ws, stream=st.cuda_stream)
+    st.synchronize()
+    assert torch.equal(ids, want_ids) and torch.equal(w, want_w) and torch.equal(y, want)
+
+
 def test_layer_refusals():
     import torch
     x = torch.zeros(3, 64, device="cuda")
