@@ -493,23 +493,89 @@ __device__ __forceinline__ void store_record(uint8_t *rec, int blk, int ig, int 
     if (lane == 0) *reinterpret_cast<float *>(r + kRecS + b / 2 * 4) = scale;
 }
 
+// What moe_stream is told of its experts: one entry per expert that some pair chose, those with the most
+// pairs first, then entries of no pairs; and the pairs, an expert's together.
+struct Entry {
+    int32_t expert, start, n, unused;
+};
+
+struct MoePrepare {
+    const void *x;
+    int64_t ldx;
+    int nb;
+    uint8_t *rec;
+    const int32_t *ids;
+    int n_expert, n_pairs, entries;     // entries: the fewer of experts and pairs
+    Entry *entry;
+    int32_t *list;
+    int entry_blocks, token_blocks;     // workgroups of the entries; of a token's digits
+    FastDiv per_token;
+};
+
+// Wave r of the first workgroups places the expert r (or the expert of pair r, where pairs are the fewer and r
+// is the first that chose it) from the counts of all experts, which every workgroup makes for itself in LDS:
+// the sums and ranks do not depend on the order of its atomics.  The others write x's records.
 template <typename XT>
-__global__ __launch_bounds__(256) void moe_digits(const XT *__restrict__ x, int64_t ldx, int nb, uint8_t *__restrict__ rec) {
-    const int it = blockIdx.x * 256 + threadIdx.x, blk = it >> 2, ig = it & 3;
-    const int nst = stages(nb);
-    if (blk >= nst * kMlSB) return;
-    float4_t v[4];
+__global__ __launch_bounds__(256) void moe_prepare(MoePrepare a) {
+    extern __shared__ int cnt[];
+    const int tid = threadIdx.x;
+    if ((int)blockIdx.x >= a.entry_blocks) {
+        const int u = (int)blockIdx.x - a.entry_blocks, token = a.per_token.div((uint32_t)u);
+        const int it = (u - token * a.token_blocks) * 256 + tid, blk = it >> 2, ig = it & 3;
+        const int nst = stages(a.nb);
+        if (blk >= nst * kMlSB) return;
+        float4_t v[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = float4_t{0.f, 0.f, 0.f, 0.f};
-    if (blk < nb) load_share(x + blockIdx.y * ldx, blk, ig, v);
-    store_record(rec + (int64_t)blockIdx.y * nst * kRec, blk, ig, it & 7, v);
+        for (int k = 0; k < 4; ++k) v[k] = float4_t{0.f, 0.f, 0.f, 0.f};
+        if (blk < a.nb) load_share(static_cast<const XT *>(a.x) + token * a.ldx, blk, ig, v);
+        store_record(a.rec + (int64_t)token * nst * kRec, blk, ig, it & 7, v);
+        return;
+    }
+    for (int i = tid; i < a.n_expert; i += 256) cnt[i] = 0;
+    __syncthreads();
+    for (int p = tid; p < a.n_pairs; p += 256) {
+        const int e = a.ids[p];
+        if (e >= 0 && e < a.n_expert) atomicAdd(&cnt[e], 1);
+    }
+    __syncthreads();
+    const int lane = tid & 63, r = (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(tid >> 6);
+    if (r >= a.entries) return;
+    const bool by_expert = a.entries == a.n_expert;
+    const int e = by_expert ? r : __builtin_amdgcn_readfirstlane(a.ids[r]);
+    const int n = e >= 0 && e < a.n_expert ? __builtin_amdgcn_readfirstlane(cnt[e]) : 0;
+    int start = 0, rank = 0, active = 0;
+    for (int i = lane; i < a.n_expert; i += 64) {
+        const int c = cnt[i];
+        start += i < e ? c : 0;
+        rank += c > n || (c == n && i < e) ? 1 : 0;
+        active += c > 0 ? 1 : 0;
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+        start += __shfl_xor(start, off);
+        rank += __shfl_xor(rank, off);
+        active += __shfl_xor(active, off);
+    }
+    if (r >= active && lane == 0) a.entry[r] = Entry{0, 0, 0, 0};
+    if (n == 0) return;
+    int before = 0;
+    for (int b = 0; b < a.n_pairs; b += 64) {
+        const bool hit = b + lane < a.n_pairs && a.ids[b + lane] == e;
+        const uint64_t m = __ballot(hit);
+        if (!by_expert && before == 0 && m && b + (int)__ffsll((unsigned long long)m) - 1 < r) return;   // an earlier pair's
+        if (hit) a.list[start + before + (int)__popcll(m & (((uint64_t)1 << lane) - 1))] = b + lane;
+        before += (int)__popcll(m);
+    }
+    if (lane == 0) a.entry[rank] = Entry{e, start, n, 0};
 }
 
 struct MoeStream {
     const uint8_t *w0, *w1;     // gate and up, or down (w0)
     int64_t expert_bytes;
     const uint8_t *x;           // records, row r at r * stages(nb) * kRec
-    Choice c;
+    const Entry *entry;
+    const int32_t *list;
+    FastDiv used;               // a pair's token: pair / slots per token
     int M, nb;
     uint8_t *rec;               // UP: h as records, row = pair
     float *out;                 // otherwise: [pair][M]
@@ -526,14 +592,15 @@ __global__ __launch_bounds__(64 * kMlWaves, 4) void moe_stream(MoeStream a) {
     __shared__ __attribute__((aligned(16))) uint8_t lds_w[kMlWaves][2 * kMlTileBytes];
     __shared__ __attribute__((aligned(16))) i32x4_t lds_x[2][kMlSB * CG * 64];   // [block][column group][lane]
     __shared__ __attribute__((aligned(16))) i32x4_t lds_m[2][64 * CG];           // sums [block][column], scales [column][pair]
-    __shared__ uint64_t lds_hit[kMlWaves];
-    __shared__ uint16_t lds_list[kMlMaxPairs];
 
+    // (through the scalar cache: one entry per workgroup)
+    typedef const __attribute__((address_space(4))) Entry *EntryPtr;
+    const EntryPtr entry = (EntryPtr)(uintptr_t)(a.entry + blockIdx.y);
+    const int e = entry->expert, n = entry->n;
+    if (n == 0) return;
+    const int32_t *list = a.list + entry->start;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15, g = lane >> 4;
-    int e;
-    const int n = chosen(a.c, e, lds_hit, lds_list, tid);
-    if (n == 0) return;
 
     const int unit = blockIdx.x * kMlWaves + wave;        // tile pair of this wave
     const bool mine = unit * (UP ? 1 : 2) * kMvTile < a.M;
@@ -548,8 +615,8 @@ __global__ __launch_bounds__(64 * kMlWaves, 4) void moe_stream(MoeStream a) {
         const int ncg = min(CG, (n - c0 + 3) / 4);
         // where this lane's share of a column's record is (columns past n repeat the last one)
         const auto record = [&](int col) {
-            const int q = lds_list[min(c0 + col, n - 1)];
-            return a.x + (int64_t)(UP ? a.c.used.div((uint32_t)q) : q) * nst * kRec;
+            const int q = list[min(c0 + col, n - 1)];
+            return a.x + (int64_t)(UP ? a.used.div((uint32_t)q) : q) * nst * kRec;
         };
         const uint8_t *xs[CG];
 #pragma unroll
@@ -571,8 +638,8 @@ __global__ __launch_bounds__(64 * kMlWaves, 4) void moe_stream(MoeStream a) {
         float r[2][CG];
 #pragma unroll
         for (int c = 0; c < CG; ++c) r[0][c] = r[1][c] = 0.f;
+        issue_w(0);           // (first: they need only the expert)
         issue_x(0, 0);
-        issue_w(0);
 #pragma unroll 1
         for (int s = 0; s < nst; ++s) {
             const int buf = s & 1;
@@ -622,7 +689,7 @@ __global__ __launch_bounds__(64 * kMlWaves, 4) void moe_stream(MoeStream a) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     v[k] = *reinterpret_cast<const float4_t *>(hb + 8 * (k < 2 ? half_lo(ig, b) : half_hi(ig, b)) + 4 * (k & 1));
-                store_record(a.rec + (int64_t)lds_list[c0 + col] * stages(a.M / kBlockWeights) * kRec, 2 * blockIdx.x + b, ig,
+                store_record(a.rec + (int64_t)list[c0 + col] * stages(a.M / kBlockWeights) * kRec, 2 * blockIdx.x + b, ig,
                              te & 7, v);
             }
             __syncthreads();
@@ -631,7 +698,7 @@ __global__ __launch_bounds__(64 * kMlWaves, 4) void moe_stream(MoeStream a) {
             for (int c = 0; c < CG; ++c) {
                 const int col = c0 + 4 * c + g;
                 if (col >= n) continue;
-                float *o = a.out + (int64_t)lds_list[col] * a.M + unit * 2 * kMvTile + j;
+                float *o = a.out + (int64_t)list[col] * a.M + unit * 2 * kMvTile + j;
                 o[0] = r[0][c];
                 o[kMvTile] = r[1][c];
             }
@@ -671,7 +738,8 @@ static int records(int k) { return stages(k / kBlockWeights) * kRec; }   // byte
 size_t moe_layer_ws_bytes(int64_t n_ff, int64_t K, int64_t n_used, int64_t n_tokens) {
     // hidden activations (f32, or records, which are larger), the experts' results, x as records
     const size_t pairs = (size_t)(n_tokens * n_used);
-    return pairs * ((size_t)records((int)n_ff) + (size_t)K * 4) + (size_t)n_tokens * records((int)K);
+    // (and the experts' entries and pairs)
+    return pairs * ((size_t)records((int)n_ff) + (size_t)K * 4 + sizeof(Entry) + 4) + (size_t)n_tokens * records((int)K);
 }
 
 // Pairs up to which the two launches for few pairs run.  128 experts of 768 x 2048, 8 used, in us,
@@ -702,8 +770,7 @@ static hipError_t launch_few(const uint8_t *wg, const uint8_t *wu, const uint8_t
 }
 
 template <int CG>
-static void launch_stream(const MoeStream &up, const MoeStream &down, hipStream_t s) {
-    const unsigned rows = (unsigned)(up.c.by_expert ? up.c.n_expert : up.c.n_pairs);
+static void launch_stream(const MoeStream &up, const MoeStream &down, unsigned rows, hipStream_t s) {
     const auto grid = [&](int units) { return dim3((unsigned)((units + kMlWaves - 1) / kMlWaves), rows); };
     moe_stream<CG, true><<<grid(up.M / kMvTile), 64 * kMlWaves, 0, s>>>(up);
     moe_stream<CG, false><<<grid(down.M / kMvTile / 2), 64 * kMlWaves, 0, s>>>(down);
@@ -725,16 +792,20 @@ hipError_t launch_moe_layer(const uint8_t *wg, const uint8_t *wu, const uint8_t 
         uint8_t *const xrec = hrec + (int64_t)n_pairs * records(n_ff);
         float *const z = reinterpret_cast<float *>(xrec + (int64_t)n_tokens * records(K));
         if (n_pairs) {
-            const dim3 grid((unsigned)((stages(K / kBlockWeights) * kMlSB * 4 + 255) / 256), (unsigned)n_tokens);
-            moe_digits<XT><<<grid, 256, 0, s>>>(x, ldx, K / kBlockWeights, xrec);
-            const MoeStream up{wg, wu, (int64_t)n_ff * (K / kBlockWeights) * kBlockBytes, xrec, c, n_ff, K / kBlockWeights, hrec,
-                               nullptr};
-            const MoeStream down{wd, nullptr, (int64_t)K * (n_ff / kBlockWeights) * kBlockBytes, hrec, c, K,
+            Entry *const entry = reinterpret_cast<Entry *>(z + (int64_t)n_pairs * K);
+            int32_t *const list = reinterpret_cast<int32_t *>(entry + n_pairs);
+            const int rows = n_pairs < n_expert ? n_pairs : n_expert, tb = (stages(K / kBlockWeights) * kMlSB * 4 + 255) / 256;
+            const MoePrepare prep{x, ldx, K / kBlockWeights, xrec, ids, n_expert, n_pairs, rows, entry, list, (rows + 3) / 4, tb,
+                                  FastDiv::make((uint32_t)tb)};
+            moe_prepare<XT><<<prep.entry_blocks + n_tokens * tb, 256, (size_t)n_expert * 4, s>>>(prep);
+            const MoeStream up{wg, wu, (int64_t)n_ff * (K / kBlockWeights) * kBlockBytes, xrec, entry, list, c.used, n_ff,
+                               K / kBlockWeights, hrec, nullptr};
+            const MoeStream down{wd, nullptr, (int64_t)K * (n_ff / kBlockWeights) * kBlockBytes, hrec, entry, list, c.used, K,
                                  n_ff / kBlockWeights, nullptr, z};
             // 8 pairs a pass where an expert's pairs would often pass 4: 128 experts of 768 x 2048, in us with
             // 4 and 8: 16 tokens 56 / 57, 24 tokens 71 / 66, 32 tokens 79 / 70, 64 tokens 100 / 86
-            if (4 * n_pairs <= 5 * n_expert) launch_stream<1>(up, down, s);
-            else launch_stream<2>(up, down, s);
+            if (4 * n_pairs <= 5 * n_expert) launch_stream<1>(up, down, (unsigned)rows, s);
+            else launch_stream<2>(up, down, (unsigned)rows, s);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
