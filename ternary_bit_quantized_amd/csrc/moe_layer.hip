@@ -598,7 +598,8 @@ __global__ __launch_bounds__(64 * kMlWaves, 4) void moe_stream(MoeStream a) {
     const EntryPtr entry = (EntryPtr)(uintptr_t)(a.entry + blockIdx.y);
     const int e = entry->expert, n = entry->n;
     if (n == 0) return;
-    const int32_t *list = a.list + entry->start;
+    typedef const __attribute__((address_space(4))) int32_t *ListPtr;
+    const ListPtr list = (ListPtr)(uintptr_t)(a.list + entry->start);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15, g = lane >> 4;
 
@@ -613,9 +614,38 @@ __global__ __launch_bounds__(64 * kMlWaves, 4) void moe_stream(MoeStream a) {
 
     for (int c0 = 0; c0 < n; c0 += NC) {
         const int ncg = min(CG, (n - c0 + 3) / 4);
+        // The pass's pairs, through the scalar cache as well: a vector load would have to be waited for together
+        // with the weights issued before it, or hold these up.  (Past n they are not this expert's, or not
+        // pairs: pick clamps.)
+        // (vectors: of an array of integers the compiler made indexed memory)
+        static_assert(CG <= 2, "pick");
+        const i32x4_t qa = {list[c0], list[c0 + 1], list[c0 + 2], list[c0 + 3]};
+        i32x4_t qb = qa;
+        if (CG > 1) qb = i32x4_t{list[c0 + 4], list[c0 + 5], list[c0 + 6], list[c0 + 7]};
+        const auto pick = [qa, qb, c0, n](int col) {
+            const int c = min(col, n - 1 - c0);
+            int r = qa[0];
+            r = c >= 1 ? qa[1] : r;
+            r = c >= 2 ? qa[2] : r;
+            r = c >= 3 ? qa[3] : r;
+            if (CG > 1) {
+                r = c >= 4 ? qb[0] : r;
+                r = c >= 5 ? qb[1] : r;
+                r = c >= 6 ? qb[2] : r;
+                r = c >= 7 ? qb[3] : r;
+            }
+            return r;
+        };
+        WStage<2> wreg;
+        const auto issue_w = [&](int s) {
+            const int sb = mine ? min(kMlSB, a.nb - s * kMlSB) : 0;
+            const uint8_t *const w[2] = {w0 + s * kMlRow, w1 + s * kMlRow};
+            if (sb > 0) wreg.load(w, rowbytes, sb, lane);
+        };
+        issue_w(0);           // (first: they need only the expert)
         // where this lane's share of a column's record is (columns past n repeat the last one)
         const auto record = [&](int col) {
-            const int q = list[min(c0 + col, n - 1)];
+            const int q = pick(col);
             return a.x + (int64_t)(UP ? a.used.div((uint32_t)q) : q) * nst * kRec;
         };
         const uint8_t *xs[CG];
@@ -629,16 +659,9 @@ __global__ __launch_bounds__(64 * kMlWaves, 4) void moe_stream(MoeStream a) {
                 if (c < ncg) lds_dma16(xs[c] + (int64_t)s * kRec, lx + buf * (uint32_t)sizeof(lds_x[0]) + (wave * CG + c) * 1024);
             if (wave < CG) lds_dma16(ms + (int64_t)s * kRec, lm + buf * (uint32_t)sizeof(lds_m[0]) + wave * 1024);
         };
-        WStage<2> wreg;
-        const auto issue_w = [&](int s) {
-            const int sb = mine ? min(kMlSB, a.nb - s * kMlSB) : 0;
-            const uint8_t *const w[2] = {w0 + s * kMlRow, w1 + s * kMlRow};
-            if (sb > 0) wreg.load(w, rowbytes, sb, lane);
-        };
         float r[2][CG];
 #pragma unroll
         for (int c = 0; c < CG; ++c) r[0][c] = r[1][c] = 0.f;
-        issue_w(0);           // (first: they need only the expert)
         issue_x(0, 0);
 #pragma unroll 1
         for (int s = 0; s < nst; ++s) {
@@ -689,7 +712,7 @@ __global__ __launch_bounds__(64 * kMlWaves, 4) void moe_stream(MoeStream a) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     v[k] = *reinterpret_cast<const float4_t *>(hb + 8 * (k < 2 ? half_lo(ig, b) : half_hi(ig, b)) + 4 * (k & 1));
-                store_record(a.rec + (int64_t)list[c0 + col] * stages(a.M / kBlockWeights) * kRec, 2 * blockIdx.x + b, ig,
+                store_record(a.rec + (int64_t)pick(col) * stages(a.M / kBlockWeights) * kRec, 2 * blockIdx.x + b, ig,
                              te & 7, v);
             }
             __syncthreads();
@@ -698,7 +721,7 @@ __global__ __launch_bounds__(64 * kMlWaves, 4) void moe_stream(MoeStream a) {
             for (int c = 0; c < CG; ++c) {
                 const int col = c0 + 4 * c + g;
                 if (col >= n) continue;
-                float *o = a.out + (int64_t)list[col] * a.M + unit * 2 * kMvTile + j;
+                float *o = a.out + (int64_t)pick(4 * c + g) * a.M + unit * 2 * kMvTile + j;
                 o[0] = r[0][c];
                 o[kMvTile] = r[1][c];
             }
@@ -738,14 +761,14 @@ static int records(int k) { return stages(k / kBlockWeights) * kRec; }   // byte
 size_t moe_layer_ws_bytes(int64_t n_ff, int64_t K, int64_t n_used, int64_t n_tokens) {
     // hidden activations (f32, or records, which are larger), the experts' results, x as records
     const size_t pairs = (size_t)(n_tokens * n_used);
-    // (and the experts' entries and pairs)
-    return pairs * ((size_t)records((int)n_ff) + (size_t)K * 4 + sizeof(Entry) + 4) + (size_t)n_tokens * records((int)K);
+    // (and the experts' entries and pairs, with room for a read of 8 pairs at the last)
+    return pairs * ((size_t)records((int)n_ff) + (size_t)K * 4 + sizeof(Entry) + 4) + (size_t)n_tokens * records((int)K) + 32;
 }
 
 // Pairs up to which the two launches for few pairs run.  128 experts of 768 x 2048, 8 used, in us,
 // two launches against four: 1 token 14.4 / 24.4, 4 tokens 24.3 / 28.0, 8 tokens 37.2 / 37.5,
 // 12 tokens 46.9 / 45.2, 16 tokens 64 / 56.
-constexpr int kFewPairs = 64;
+constexpr int kFewPairs = 24;
 
 template <typename XT>
 static hipError_t launch_few(const uint8_t *wg, const uint8_t *wu, const uint8_t *wd, const Choice &c, int n_ff, int K,
@@ -804,7 +827,7 @@ hipError_t launch_moe_layer(const uint8_t *wg, const uint8_t *wu, const uint8_t 
                                  n_ff / kBlockWeights, nullptr, z};
             // 8 pairs a pass where an expert's pairs would often pass 4: 128 experts of 768 x 2048, in us with
             // 4 and 8: 16 tokens 56 / 57, 24 tokens 71 / 66, 32 tokens 79 / 70, 64 tokens 100 / 86
-            if (4 * n_pairs <= 5 * n_expert) launch_stream<1>(up, down, (unsigned)rows, s);
+            if (2 * n_pairs <= 5 * n_expert) launch_stream<1>(up, down, (unsigned)rows, s);
             else launch_stream<2>(up, down, (unsigned)rows, s);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
