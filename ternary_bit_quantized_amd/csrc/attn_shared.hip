@@ -32,8 +32,9 @@
 //    x 4 pieces: with every wave reading them so, the L1's tag rate held 64 sequences over
 //    32768 keys at 123 us.)  Issue-bound: ~150 VALU instructions per 32 keys x 32 rows.
 //    Few rows, or a short prefix of few sequences, go the own part's way instead.
-// Workgroups that read the same prefix keys for other rows get launch numbers 8 apart: the same XCD,
-// whose L2 then serves all but one of them.  Splits of the key axis join in attn_join.
+// Workgroups that read the same prefix keys for other rows get launch numbers 8 apart: the same XCD, whose
+// L2 then serves all but one of them (four row groups over 8192 keys: 56 us spread over the XCDs, 48 so).
+// Splits of the key axis join in attn_join.
 //
 // Masks.  A row sees keys below its limit.  Scores past it become -inf before the maximum, value
 // rows nobody sees are zeroed, and tiles whose keys only some of a wave's rows see (draft tokens,
@@ -105,10 +106,10 @@ __device__ __forceinline__ void load_dwords(const uint8_t *p, uint32_t *v) {
     }
 }
 
-// Waves of a workgroup.  With a prefix part 4, so that two workgroups share a CU and are not in step: one's
-// softmax then runs beside the other's matrix instructions.  Without, 8 (one sequence's keys are read
-// by more waves), or 4 where a wave needs more than half a SIMD's registers.
-constexpr int attn_waves(int dim, bool prefix) { return dim < 256 && !prefix ? 8 : 4; }
+// Waves of a workgroup: 4, so that two workgroups share a CU and are not in step (one's softmax then runs
+// beside the other's matrix instructions), and a sequence's keys split finely.  With 8, 777 keys of one
+// sequence took 10.6 instead of 9.3 us, 2000 12.9 instead of 9.5, 16 sequences of 2000 36 instead of 31.
+constexpr int kAttnWaves = 4;
 
 // The page table through the scalar cache (uniform index).
 __device__ __forceinline__ int table_at(const int32_t *t, int i) {
@@ -427,7 +428,7 @@ __device__ __forceinline__ void store_row(const AttnShared &a, int nsplit, int s
 // buffers (then its O areas); and the row tables.
 template <int D, bool PRE>
 struct AttnLds {
-    static constexpr int W = attn_waves(D, PRE), OS = D + 4;
+    static constexpr int W = kAttnWaves, OS = D + 4;
     static constexpr int kTileBytes = kAttnTile * D * 2;                   // keys, or values, of a tile
     union {
         float o[W][16][OS];
@@ -441,7 +442,7 @@ struct AttnLds {
 // One sequence's own keys (or all keys, prefix included, of a joint plan): waves take different tiles.
 template <typename CT, int D, bool PRE, bool P16>
 __device__ __forceinline__ void own_part(const AttnShared &a, AttnLds<D, PRE> &lds, int id, int tid) {
-    constexpr int W = attn_waves(D, PRE);
+    constexpr int W = kAttnWaves;
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), j = lane & 15, g = lane >> 4;
     int u = a.groups_o.div((uint32_t)id);
     const int rg = id - u * (int)a.groups_o.d;
@@ -525,16 +526,15 @@ __device__ __forceinline__ void own_part(const AttnShared &a, AttnLds<D, PRE> &l
 // The shared prefix: waves take different rows of the same tiles.
 template <typename CT, int D, int RT, bool P16>
 __device__ __forceinline__ void prefix_part(const AttnShared &a, AttnLds<D, true> &lds, int id, int tid) {
-    constexpr int W = attn_waves(D, true), kBytes = AttnLds<D, true>::kTileBytes;
+    constexpr int W = kAttnWaves, kBytes = AttnLds<D, true>::kTileBytes;
     constexpr int RI = 512 / D;              // rows of a 1 KiB load
     constexpr int LR = D / 8;                // 16-byte pieces of a row
     constexpr int NK = kAttnTile / RI;       // loads for a tile's keys, and as many for its values
     constexpr int NI = 2 * NK / W;           // loads of a wave per tile
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), j = lane & 15, g = lane >> 4;
-    const int x = a.xcd_p ? id & 7 : 0;
-    int u = a.xcd_p ? id >> 3 : id;
-    const int y = a.groups_p.div((uint32_t)u), rg = u - y * (int)a.groups_p.d;
-    u = a.xcd_p ? y * 8 + x : y;
+    const int x = a.xcd_p ? id & 7 : 0, id8 = a.xcd_p ? id >> 3 : id;
+    const int y = a.groups_p.div((uint32_t)id8), rg = id8 - y * (int)a.groups_p.d;
+    const int u = a.xcd_p ? y * 8 + x : y;
     const int split = a.heads.div((uint32_t)u), kvh = u - split * a.n_kv;
     const int r0 = (rg * W + wave) * RT * 16;
 
@@ -705,7 +705,7 @@ __device__ __forceinline__ void prefix_part(const AttnShared &a, AttnLds<D, true
 
 // RTP: 16-row tiles of a wave in the prefix part; 0: there is none.
 template <typename CT, int D, int RTP, bool P16>
-__global__ __launch_bounds__(64 * attn_waves(D, RTP > 0), D == 256 ? 1 : 2) void attn_rows(AttnShared a) {
+__global__ __launch_bounds__(64 * kAttnWaves, D == 256 ? 1 : 2) void attn_rows(AttnShared a) {
     __shared__ AttnLds<D, (RTP > 0)> lds;
     if constexpr (RTP > 0) {
         if ((int)blockIdx.x < a.wgs_p) {
@@ -780,32 +780,37 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t n_q, int64_t n_kv, int64_t dim, int64
     p.groups_o = div_up(rows_o, 16);
     // The prefix has a part of its own unless it is of one sequence with one tile of rows, or all is
     // short and few: then a workgroup takes all of a sequence's keys, prefix included (read once per
-    // sequence, from the L2), and writes the result itself, without a join.
+    // sequence, from the L2), and writes the result itself, without a join: 8 sequences of 2 key heads
+    // with 1001 keys 9.4 against 10.4 us; 16 of 8 key heads with 1200 keys 14.7 against 13.8, 32 of them 19.6
+    // against 17.1.
     const int64_t wgs = n_seqs * n_kv * p.groups_o;
-    p.joint = prefix_len > 0 && ((n_seqs == 1 && rows_p <= 16) ||
-                                 (tiles(max_len) <= 5 * attn_waves((int)dim, false) && wgs <= 256));
+    p.joint = prefix_len > 0 && ((n_seqs == 1 && rows_p <= 16) || (tiles(max_len) <= 40 && wgs <= 64));
     const bool shared = prefix_len > 0 && !p.joint;
-    const int w = attn_waves((int)dim, shared);
     if (shared) {
-        // as few rows a wave as hold them all, up to 32 (16 for 256 dims: registers)
-        p.row_tiles = dim < 256 && rows_p > 16 * w ? 2 : 1;
-        p.groups_p = div_up(rows_p, 16 * w * p.row_tiles);
-        // The number of splits weighs the tiles of one (750 ns each with a workgroup a CU, 1150 ns with two)
-        // against the splits' results (0.75 MB a us, written and read back; at 64 sequences
-        // of 32 heads 33 MB for 32 splits: 16 took 77 us, 32 took 88 us over 32768 keys, 220 and 198 us over
-        // 131072).  At least four tiles each.
-        const int64_t t = tiles(prefix_len), units = p.groups_p * n_kv, part = rows_p * n_kv * dim * 4;
+        // Row tiles of a wave (2 read the tiles from LDS half as often, 1 gives twice the workgroups; 256 dims
+        // have registers for 1) and the number of splits weigh the tiles of a split, in us of a workgroup
+        // alone on its CU or beside another, against the splits' results (0.75 MB a us, written and read
+        // back).  64 sequences of 32 heads, 33 MB of results for 32 splits: over 32768 keys 16 splits took
+        // 77 us and 32 took 88, over 131072 220 and 198; 2 row tiles against 1 79 and 95 us over 32768
+        // keys, 50 and 48 over 8192.  At least four tiles each.
+        constexpr double alone[2] = {0.55, 0.75}, beside[2] = {0.98, 1.15};
+        const int64_t t = tiles(prefix_len), part = rows_p * n_kv * dim * 4;
         double best = 0;
-        for (int64_t n = 1; n <= kAttnMaxSplits && (n == 1 || 4 * n <= t); ++n) {
-            const double rounds = n * units <= 256 ? 0.75 : 1.15 * (double)div_up(n * units, 512);
-            const double us = (double)div_up(t, n) * rounds + (double)(n * part) / 0.75e6;
-            if (n == 1 || us < best) best = us, p.splits_p = n;
+        for (int rt = 1; rt <= (dim < 256 && rows_p > 16 * kAttnWaves ? 2 : 1); ++rt) {
+            const int64_t groups = div_up(rows_p, 16 * kAttnWaves * rt), units = groups * n_kv;
+            for (int64_t n = 1; n <= kAttnMaxSplits && (n == 1 || 4 * n <= t); ++n) {
+                const double tile = n * units <= 256 ? alone[rt - 1] : beside[rt - 1] * (double)div_up(n * units, 512);
+                const double us = (double)div_up(t, n) * tile + (double)(n * part) / 0.75e6;
+                if (p.splits_p == 0 || us < best) best = us, p.splits_p = n, p.row_tiles = rt, p.groups_p = groups;
+            }
         }
     }
     const int64_t own = shared ? tiles(max_len) - prefix_len / kAttnTile : tiles(max_len);
-    // own keys: up to five tiles a wave are taken at once; beyond, enough workgroups for the chip, two tiles
-    // a wave at least
-    if (!shared || max_len > prefix_len) p.splits_o = own <= 5 * w ? 1 : splits(div_up(512, wgs), own / (2 * w));
+    // own keys: a few tiles a wave are taken at once (777 keys of one sequence: 11.0 us so, 9.2 in 3 splits and
+    // a join; 1000 keys of 16: 14.7 and 16.6); beyond, enough workgroups for the chip, two tiles a wave at least
+    const int64_t few = !shared && wgs >= 128 ? 40 : 20;
+    if (!shared || max_len > prefix_len)
+        p.splits_o = own <= few ? 1 : splits(div_up(512, wgs), own / (2 * kAttnWaves));
     const int64_t n = p.splits_p + p.splits_o;
     p.ws_bytes = n <= 1 ? 0 : (size_t)(n * rows_p * n_kv) * (size_t)(dim + 2) * 4;
     return p;
@@ -835,7 +840,7 @@ hipError_t launch_attn_shared(AttnShared a, const AttnPlan &p, Act ct, int dim, 
     const bool p16 = a.page.d % 16 == 0 && a.joint_len % 16 == 0;
     auto run = [&](auto ctag, auto d, auto rtp) -> hipError_t {
         using CT = decltype(ctag);
-        constexpr int D = decltype(d)::value, RTP = decltype(rtp)::value, T = 64 * attn_waves(D, RTP > 0);
+        constexpr int D = decltype(d)::value, RTP = decltype(rtp)::value, T = 64 * kAttnWaves;
         if (p16) attn_rows<CT, D, RTP, true><<<grid, T, 0, s>>>(a);
         else attn_rows<CT, D, RTP, false><<<grid, T, 0, s>>>(a);
         const hipError_t e = hipGetLastError();
