@@ -807,8 +807,9 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t n_q, int64_t n_kv, int64_t dim, int64
     }
     const int64_t own = shared ? tiles(max_len) - prefix_len / kAttnTile : tiles(max_len);
     // own keys: a few tiles a wave are taken at once (777 keys of one sequence: 11.0 us so, 9.2 in 3 splits and
-    // a join; 1000 keys of 16: 14.7 and 16.6); beyond, enough workgroups for the chip, two tiles a wave at least
-    const int64_t few = !shared && wgs >= 128 ? 40 : 20;
+    // a join, whose launch costs the caller more than that; 1200 keys: 14.4 and 9.4; 1000 keys of 16: 14.7
+    // and 16.6); beyond, enough workgroups for the chip, two tiles a wave at least
+    const int64_t few = shared ? 20 : wgs >= 128 ? 40 : 28;
     if (!shared || max_len > prefix_len)
         p.splits_o = own <= few ? 1 : splits(div_up(512, wgs), own / (2 * kAttnWaves));
     const int64_t n = p.splits_p + p.splits_o;

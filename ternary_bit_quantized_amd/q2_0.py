@@ -274,6 +274,7 @@ def attn_shared_raw(cache: KvCache, table: int, n_seqs: int, table_len: int, ld_
                                   stream)
 
 
+@functools.lru_cache(maxsize=1024)      # (a function of the sizes alone)
 def attn_shared_workspace_bytes(n_seqs: int, n_q: int, n_kv: int, head_dim: int, n_qt: int, prefix_len: int,
                                 max_len: int) -> int:
     return lib().q2_0_attn_shared_workspace_bytes(n_seqs, n_q, n_kv, head_dim, n_qt, prefix_len, max_len)
@@ -291,6 +292,7 @@ def moe_layer_raw(w_gate: int, w_up: int, w_down: int, n_expert: int, n_ff: int,
                                 y, ldy, workspace, ws_bytes, stream)
 
 
+@functools.lru_cache(maxsize=1024)      # (a function of the sizes alone)
 def moe_layer_workspace_bytes(n_ff: int, K: int, n_used: int, n_tokens: int) -> int:
     return lib().q2_0_moe_layer_workspace_bytes(n_ff, K, n_used, n_tokens)
 
@@ -493,10 +495,12 @@ def _act_types():
 
 def _rows(t, rows, cols, name):
     """A 2-D CUDA tensor of `rows` rows of at least `cols` elements, unit inner stride -> row stride."""
-    if not t.is_cuda or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < cols or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError("%s must be a 2-D CUDA tensor of %d rows of at least %d elements with unit inner stride"
-                         % (name, rows, cols))
-    return t.stride(0) if rows > 1 else max(t.stride(0), t.shape[1])
+    if t.is_cuda and t.dim() == 2:
+        (n, c), (ld, inner) = t.shape, t.stride()
+        if n == rows and c >= cols and (inner == 1 or c <= 1):
+            return ld if rows > 1 else max(ld, c)
+    raise ValueError("%s must be a 2-D CUDA tensor of %d rows of at least %d elements with unit inner stride"
+                     % (name, rows, cols))
 
 
 def _int32(t, shape, name):
@@ -508,23 +512,24 @@ def _int32(t, shape, name):
 
 def _table(t):
     import torch
-    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError("table must be a 2-D int32 CUDA tensor with unit inner stride")
-    n, cols = t.shape
-    return t.data_ptr(), n, cols, t.stride(0) if n > 1 else max(t.stride(0), cols)
+    if t.dtype == torch.int32 and t.is_cuda and t.dim() == 2:
+        (n, cols), (ld, inner) = t.shape, t.stride()
+        if inner == 1 or cols <= 1:
+            return t.data_ptr(), n, cols, ld if n > 1 else max(ld, cols)
+    raise ValueError("table must be a 2-D int32 CUDA tensor with unit inner stride")
 
 
 def _cache(k_cache, v_cache):
     """Pools (n_pages, n_kv, page_size, head_dim) with unit inner stride and equal strides -> KvCache."""
-    st = k_cache.stride()
-    if k_cache.dim() != 4 or not k_cache.is_cuda or not v_cache.is_cuda or st[3] != 1 or \
-            v_cache.shape != k_cache.shape or v_cache.stride() != st or v_cache.dtype != k_cache.dtype:
+    shape, st = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or not k_cache.is_cuda or not v_cache.is_cuda or st[3] != 1 or v_cache.shape != shape or \
+            v_cache.stride() != st or v_cache.dtype != k_cache.dtype:
         raise ValueError("k_cache and v_cache must be CUDA tensors (n_pages, n_kv, page_size, head_dim) of one dtype "
                          "and equal strides, unit inner stride")
     dtype = _act_types().get(k_cache.dtype)
     if dtype is None or dtype == Q2_0_ACT_F32:
         raise ValueError("the cache must be float16 or bfloat16")
-    n_pages, n_kv, page, dim = k_cache.shape
+    n_pages, n_kv, page, dim = shape
     return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), dtype, n_pages, page, n_kv, dim, st[0], st[1], st[2])
 
 
