@@ -53,6 +53,7 @@ template <typename CT>
 struct Mma;
 template <>
 struct Mma<_Float16> {
+    static constexpr uint32_t kOnes = 0x3c003c00u;
     static __device__ __forceinline__ float4_t mul(u32x4_t a, u32x4_t b, float4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c,
                                                       0, 0, 0);
@@ -60,6 +61,7 @@ struct Mma<_Float16> {
 };
 template <>
 struct Mma<bf16_t> {
+    static constexpr uint32_t kOnes = 0x3f803f80u;
     static __device__ __forceinline__ float4_t mul(u32x4_t a, u32x4_t b, float4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8_t, a), __builtin_bit_cast(bf8_t, b), c, 0,
                                                        0, 0);
@@ -127,7 +129,8 @@ struct Rows {
 
     u32x4_t q[RT][KS];       // queries as the scores' B operand
     float4_t o[RT][DPL];
-    float m[RT], ms[RT], l[RT];   // reference (-inf: none yet), the same as a number, sum of this lane
+    float m[RT], ms[RT];     // reference (-inf: none yet), the same as a number
+    float4_t l[RT];          // row j's sum, four times
     int lim[RT];             // keys row j sees
     int lim_lo, lim_hi;      // the least (of rows that see some key past k_lo) and most of the wave's rows
     u32x4_t k[2][KS];        // a key tile's operands
@@ -140,7 +143,7 @@ struct Rows {
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             const int r = r0 + 16 * t + j;
-            lim[t] = 0, m[t] = -__builtin_inff(), ms[t] = 0.f, l[t] = 0.f;
+            lim[t] = 0, m[t] = -__builtin_inff(), ms[t] = 0.f, l[t] = float4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < DPL; ++e) o[t][e] = float4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -194,21 +197,19 @@ struct Rows {
             const float f = m[t] == mx ? 1.f : __builtin_amdgcn_exp2f(m[t] - mn);
             m[t] = mx;
             ms[t] = mn;
-            l[t] *= f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l[t][i] *= f;
 #pragma unroll
             for (int e = 0; e < DPL; ++e)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[t][e][i] *= f;
         }
     }
-    // Scores to weights: the running sum, and P rounded to the cache's type (the matrix cores' operand).
+    // Scores to weights P, rounded to the cache's type (the matrix cores' operand).
     __device__ __forceinline__ u32x4_t weights(const float4_t (&s)[2], int t, float scale2) {
         float w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 4][i % 4], scale2, -ms[t]));
-            l[t] += w[i];
-        }
+        for (int i = 0; i < 8; ++i) w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 4][i % 4], scale2, -ms[t]));
         return u32x4_t{pack2<CT>(w[0], w[1]), pack2<CT>(w[2], w[3]), pack2<CT>(w[4], w[5]), pack2<CT>(w[6], w[7])};
     }
     // the value tile's operand of dim e: its 8 keys' halves
@@ -219,84 +220,78 @@ struct Rows {
         for (int i = 0; i < 4; ++i) r[i] = __builtin_amdgcn_perm(v[2 * i + 1][e / 2], v[2 * i][e / 2], sel);
         return r;
     }
-    // Value rows that nobody sees may hold NaN: zeroed.
-    __device__ __forceinline__ void clear_unseen(int key0, int k_lo, int g) {
+    // Which halves of a value operand's four dwords are keys in [k_lo, end)
+    static __device__ __forceinline__ u32x4_t keys_kept(int key0, int k_lo, int end, int g) {
+        u32x4_t keep;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int kk = key0 + 16 * (i / 4) + 4 * g + i % 4;
-            const bool seen = kk < lim_hi && kk >= k_lo;
-#pragma unroll
-            for (int d = 0; d < VD; ++d) v[i][d] = seen ? v[i][d] : 0u;
+        for (int i = 0; i < 4; ++i) {
+            const int k0 = key0 + 16 * (i / 2) + 4 * g + 2 * (i % 2);
+            keep[i] = (k0 < end && k0 >= k_lo ? 0xffffu : 0u) | (k0 + 1 < end && k0 + 1 >= k_lo ? 0xffff0000u : 0u);
         }
+        return keep;
     }
-    // O += P V
-    __device__ __forceinline__ void values(const u32x4_t (&p)[RT]) {
-#pragma unroll
-        for (int e = 0; e < DPL; ++e) {
-            const u32x4_t va = v_operand(e);
-#pragma unroll
-            for (int t = 0; t < RT; ++t) o[t][e] = Mma<CT>::mul(va, p[t], o[t][e]);
-        }
+    // l += P 1, from the rounded weights, as the values are.
+    __device__ __forceinline__ void sums(const u32x4_t &p, int t) {
+        constexpr uint32_t one = Mma<CT>::kOnes;
+        l[t] = Mma<CT>::mul(u32x4_t{one, one, one, one}, p, l[t]);
     }
-    // Row tile t's O in a wave's LDS area of 16 rows.
+    // O += P V; va[e]: the operands
+    __device__ __forceinline__ void values(const u32x4_t (&p)[RT], const u32x4_t (&va)[DPL]) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) sums(p[t], t);
+#pragma unroll
+        for (int e = 0; e < DPL; ++e)
+#pragma unroll
+            for (int t = 0; t < RT; ++t) o[t][e] = Mma<CT>::mul(va[e], p[t], o[t][e]);
+    }
+    // Row tile t's O in a wave's LDS area of 16 rows; an operand's dims are DPL apart, or 16 in a row (ROW16).
+    template <bool ROW16>
     __device__ __forceinline__ void o_to_lds(float *area, int t, int j, int g) const {
+        if constexpr (ROW16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int e = 0; e < DPL; ++e) *reinterpret_cast<float4_t *>(area + j * OS + 16 * e + 4 * g) = o[t][e];
+        } else {
 #pragma unroll
-            for (int e = 0; e < DPL; e += 4)
-                *reinterpret_cast<float4_t *>(area + j * OS + DPL * (4 * g + i) + e) =
-                    float4_t{o[t][e][i], o[t][e + 1][i], o[t][e + 2][i], o[t][e + 3][i]};
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < DPL; e += 4)
+                    *reinterpret_cast<float4_t *>(area + j * OS + DPL * (4 * g + i) + e) =
+                        float4_t{o[t][e][i], o[t][e + 1][i], o[t][e + 2][i], o[t][e + 3][i]};
+        }
     }
-    // and back, where the row is to have it (a select, not a branch: see mixed_tile)
-    __device__ __forceinline__ void o_from_lds(const float *area, int t, int j, int g, bool back) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < DPL; e += 4) {
-                const float4_t w = *reinterpret_cast<const float4_t *>(area + j * OS + DPL * (4 * g + i) + e);
-#pragma unroll
-                for (int d = 0; d < 4; ++d) o[t][e + d][i] = back ? w[d] : o[t][e + d][i];
-            }
-    }
-    // A tile whose keys only some rows see: its values are multiplied once per distinct limit, lowest
-    // first, with value rows at or past it zeroed; the rows of other limits take back what they
-    // had (a zeroed P would not do: 0 * NaN reaches them).  Nothing in the loop branches by lane: a
+    // A tile whose keys only some rows see (its keys in k): its values are multiplied once per distinct limit,
+    // lowest first, with value rows at or past it zeroed, and only the rows of that limit take the product
+    // (a zeroed P would not do: 0 * NaN reaches the others).  Nothing in the loop branches by lane: a
     // branch on lim == cur was carried into the next pass by the compiler, whose minimum over the rows
     // then missed lanes and never came to an end.
-    template <typename Tile>
-    __device__ __forceinline__ void mixed_tile(const Tile &tile, int t, float scale2, int key0, int k_lo, uint32_t bad, float *area,
-                                               int j, int g) {
+    template <typename Operand>
+    __device__ __forceinline__ void mixed_tile(int t, float scale2, int key0, int k_lo, uint32_t bad, int g, const Operand &operand) {
         float4_t s[2];
-        tile.load_k(*this, j, g);
         scores(s, t);
         settle();
         mask(s, t, key0, k_lo, bad, g);
         raise(s, t, scale2);
         const u32x4_t p = weights(s, t, scale2);
-        tile.load_v(*this, j, g);
+        sums(p, t);
         int done = max(key0, k_lo);             // (rows of limits up to here see nothing in this tile)
 #pragma unroll 1
         for (int pass = 0; pass < 16; ++pass) { // (16 rows: no more limits)
             const int cur = __builtin_amdgcn_readfirstlane(row_min(lim[t] > done ? lim[t] : 0x7fffffff));
             if (cur == 0x7fffffff) break;
             done = cur;
-            uint32_t keep[4];                   // per pair of keys: which halves stay
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k0 = key0 + 16 * (i / 2) + 4 * g + 2 * (i % 2);
-                keep[i] = (k0 < cur && k0 >= k_lo ? 0xffffu : 0u) | (k0 + 1 < cur && k0 + 1 >= k_lo ? 0xffff0000u : 0u);
-            }
-            o_to_lds(area, t, j, g);
+            const u32x4_t keep = keys_kept(key0, k_lo, cur, g);
+            const bool mine = lim[t] == cur;
 #pragma unroll
             for (int e = 0; e < DPL; ++e) {
-                u32x4_t va = v_operand(e);
+                u32x4_t va = operand(e);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) va[i] &= keep[i];
-                o[t][e] = Mma<CT>::mul(va, p, o[t][e]);
+                const float4_t r = Mma<CT>::mul(va, p, float4_t{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[t][e][i] = mine ? o[t][e][i] + r[i] : o[t][e][i];
             }
-            settle();
-            o_from_lds(area, t, j, g, lim[t] != cur);
         }
+        settle();
     }
     // Row j's final reference and sum; rows that saw nothing hold nothing (a row that saw nothing but NaN has
     // no reference either, and keeps its NaN).
@@ -305,29 +300,35 @@ struct Rows {
         for (int t = 0; t < RT; ++t) {
             if (lim[t] <= k_lo) {
                 m[t] = -__builtin_inff();
-                l[t] = 0.f;
+                l[t] = float4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int e = 0; e < DPL; ++e) o[t][e] = float4_t{0.f, 0.f, 0.f, 0.f};
             }
-            l[t] += __shfl_xor(l[t], 16);
-            l[t] += __shfl_xor(l[t], 32);
         }
     }
 };
 
-// Two 16-byte LDS-DMA loads per lane (lds_dma.h) to consecutive kilobytes, with a uniform base and a byte offset per lane.
-__device__ __forceinline__ void lds_dma16x2(const void *base, uint32_t off0, uint32_t off1, uint32_t lds) {
+// Two 16-byte LDS-DMA loads per lane (lds_dma.h) to kilobytes step apart, with a uniform base and a byte offset per lane.
+__device__ __forceinline__ void lds_dma16x2(const void *base, uint32_t off0, uint32_t off1, uint32_t lds, uint32_t step) {
     uint32_t saved;
     asm volatile(
         "s_mov_b32 %0, m0\n\t"
         "s_mov_b32 m0, %4\n\t"
         "global_load_lds_dwordx4 %1, %3\n\t"
-        "s_add_u32 m0, m0, 0x400\n\t"
+        "s_add_u32 m0, m0, %5\n\t"
         "global_load_lds_dwordx4 %2, %3\n\t"
         "s_mov_b32 m0, %0"
         : "=&s"(saved)
-        : "v"(off0), "v"(off1), "s"(base), "s"(lds)
+        : "v"(off0), "v"(off1), "s"(base), "s"(lds), "s"(step)
         : "memory", "scc");
+}
+
+// 4 rows x 16 elements from LDS, the lanes of a 16-lane group 8 bytes each along the rows (lane l: row l / 4);
+// lane l gets element l of the four rows.
+__device__ __forceinline__ u32x2_t read_transposed(const uint8_t *p) {
+    typedef short Four __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) Four *LdsPtr;
+    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(p)));
 }
 
 // Stands for rows of pages that do not exist: NaN in either type.
@@ -429,14 +430,18 @@ __device__ __forceinline__ void store_row(const AttnShared &a, int nsplit, int s
 template <int D, bool PRE>
 struct AttnLds {
     static constexpr int W = kAttnWaves, OS = D + 4;
-    static constexpr int kTileBytes = kAttnTile * D * 2;                   // keys, or values, of a tile
+    static constexpr int kTileBytes = kAttnTile * D * 2;                   // keys of a tile
+    static constexpr int kBlock = 1024 + (D == 64 ? 0 : D == 128 ? 128 : 64);       // a kilobyte of values, apart for the banks
+    static constexpr int kValueBytes = kAttnTile * D * 2 / 1024 * kBlock;
     union {
         float o[W][16][OS];
-        __attribute__((aligned(16))) uint8_t kv[2][3][PRE ? kTileBytes : 16];   // rings of keys and of values
+        struct {
+            __attribute__((aligned(16))) uint8_t k[3][PRE ? kTileBytes : 16], v[3][PRE ? kValueBytes : 16];
+        } ring;
     };
     float m[W][16], l[W][16];
     int64_t row[W][kAttnTile];
-    int least[W];
+    int least[W], most[W];
 };
 
 // One sequence's own keys (or all keys, prefix included, of a joint plan): waves take different tiles.
@@ -476,28 +481,38 @@ __device__ __forceinline__ void own_part(const AttnShared &a, AttnLds<D, PRE> &l
         const int key0 = tile * kAttnTile;
         const bool edge = key0 < k_lo || key0 + kAttnTile > w.lim_hi || bad != 0;   // some key needs a mask
         float4_t s[2];
-        u32x4_t p[1];
+        u32x4_t p[1], va[D / 16];
         w.scores(s, 0);
         if (more) kt.load_k(w, j, g);
         if (edge) w.mask(s, 0, key0, k_lo, bad, g);
         w.raise(s, 0, a.scale2);
         p[0] = w.weights(s, 0, a.scale2);
-        if (edge) w.clear_unseen(key0, k_lo, g);
-        w.values(p);
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) va[e] = w.v_operand(e);
+        if (edge) {           // what nobody sees may be NaN
+            const u32x4_t keep = w.keys_kept(key0, k_lo, w.lim_hi, g);
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) va[e][i] &= keep[i];
+        }
+        w.values(p, va);
         if (more) kt.load_v(w, j, g);
     }
     for (; tile < tb; tile += W) {
         const int key0 = tile * kAttnTile;
         const uint32_t bad = kt.find(key0, k_lo, w.lim_hi, lane);
-        w.mixed_tile(kt, 0, a.scale2, key0, k_lo, bad, &lds.o[wave][0][0], j, g);
+        kt.load_k(w, j, g);
+        kt.load_v(w, j, g);
+        w.mixed_tile(0, a.scale2, key0, k_lo, bad, g, [&](int e) { return w.v_operand(e); });
     }
     // join the waves' results
     w.finish(k_lo);
     if (g == 0) {
         lds.m[wave][j] = w.m[0];
-        lds.l[wave][j] = w.l[0];
+        lds.l[wave][j] = w.l[0][0];
     }
-    w.o_to_lds(&lds.o[wave][0][0], 0, j, g);
+    w.template o_to_lds<false>(&lds.o[wave][0][0], 0, j, g);
     __syncthreads();
     const int grp = (int)a.group.d, rows_here = min(a.rows_o - r0, 16);
     const int nsplit = a.splits_p + splits;
@@ -526,7 +541,8 @@ __device__ __forceinline__ void own_part(const AttnShared &a, AttnLds<D, PRE> &l
 // The shared prefix: waves take different rows of the same tiles.
 template <typename CT, int D, int RT, bool P16>
 __device__ __forceinline__ void prefix_part(const AttnShared &a, AttnLds<D, true> &lds, int id, int tid) {
-    constexpr int W = kAttnWaves, kBytes = AttnLds<D, true>::kTileBytes;
+    using Lds = AttnLds<D, true>;
+    constexpr int W = kAttnWaves;
     constexpr int RI = 512 / D;              // rows of a 1 KiB load
     constexpr int LR = D / 8;                // 16-byte pieces of a row
     constexpr int NK = kAttnTile / RI;       // loads for a tile's keys, and as many for its values
@@ -544,27 +560,30 @@ __device__ __forceinline__ void prefix_part(const AttnShared &a, AttnLds<D, true
     const int per = a.div_p.div((uint32_t)(ntile + a.splits_p - 1));
     const int ta = min(ntile, per * split), tb = min(ntile, per * (split + 1));
     // the first tile some wave's rows see differently (to the end: theirs alone)
-    if (lane == 0) lds.least[wave] = w.lim_lo < w.lim_hi ? w.lim_lo / kAttnTile : tb;
+    if (lane == 0) lds.least[wave] = w.lim_lo < w.lim_hi ? w.lim_lo / kAttnTile : tb, lds.most[wave] = w.lim_hi;
     __syncthreads();
-    int t_split = tb;
+    int t_split = tb, t_last = 0;
 #pragma unroll
-    for (int i = 0; i < W; ++i) t_split = min(t_split, lds.least[i]);
+    for (int i = 0; i < W; ++i) t_split = min(t_split, lds.least[i]), t_last = max(t_last, lds.most[i]);
     t_split = __builtin_amdgcn_readfirstlane(max(ta, t_split));
+    t_last = __builtin_amdgcn_readfirstlane(min(tb, (t_last + kAttnTile - 1) / kAttnTile));
 
     KeyTile<CT, D, P16> kt{a, a.table, static_cast<const uint8_t *>(a.kc) + 2 * (int64_t)kvh * a.head_stride,
                            static_cast<const uint8_t *>(a.vc) + 2 * (int64_t)kvh * a.head_stride, lds.row[wave], {0, 0}};
     // This wave's share of a tile's loads: loads q = wave NI .. + NI, of which load q covers rows RI (q % NK) ..
-    // of the keys (q < NK) or values; all lie in one half of the tile.  Lane l takes piece l % LR of row
-    // l / LR, keys' pieces swizzled.
-    const uint32_t buf0 = (uint32_t)(uintptr_t)&lds.kv[0][0][0];
+    // of the keys (q < NK) or values; all lie in one half of the tile.  Lane l takes the 16 bytes whose place
+    // in the load's kilobyte is l: of the keys piece l % LR of row l / LR, swizzled by the row; of the values
+    // [16 dims][row][half of them], so that a transposing read finds 16 dims of 4 rows in 128 bytes.
     const auto swizzle = [](int row) { return (D == 64 ? row >> 1 : row) & (LR < 16 ? LR - 1 : 15); };
     const bool my_keys = wave * NI < NK;
     const int row0 = wave * NI % NK * RI;
-    const uint32_t my_lds = buf0 + (uint32_t)((my_keys ? 0 : 3 * kBytes) + row0 * 2 * D);
+    const uint32_t my_step = my_keys ? 1024u : (uint32_t)Lds::kBlock, my_ring = my_keys ? Lds::kTileBytes : Lds::kValueBytes;
+    const uint32_t my_lds = (my_keys ? (uint32_t)(uintptr_t)&lds.ring.k[0][0] : (uint32_t)(uintptr_t)&lds.ring.v[0][0]) +
+                            (uint32_t)(row0 / RI) * my_step;
     const uint8_t *my_base = my_keys ? kt.kbase : kt.vbase;
+    const int in_row = my_keys ? lane / LR : D == 64 ? (lane >> 3 & 1) * 4 + (lane >> 1 & 3) : lane >> 1 & (RI - 1);
     const auto piece = [&](int i) {
-        const int row = row0 + i * RI + lane / LR, slot = lane % LR;
-        return 16 * (my_keys ? slot ^ swizzle(row) : slot);
+        return 16 * (my_keys ? (lane % LR) ^ swizzle(row0 + i * RI + in_row) : 2 * (lane / (D == 64 ? 16 : 2 * RI)) + (lane & 1));
     };
     // The next tile to load (P16): this wave's half's index in the table, place in the page, page number (read
     // a tile ahead) and address.  What lies past the prefix takes its last page (and is masked).  Where a page
@@ -581,20 +600,20 @@ __device__ __forceinline__ void prefix_part(const AttnShared &a, AttnLds<D, true
         page = table_at(a.table, min(pi, last_pi));
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-            voff[i] = (uint32_t)(2 * (((row0 & 15) + i * RI + lane / LR) * (int)a.token_stride) + piece(i));
+            voff[i] = (uint32_t)(2 * (((row0 & 15) + i * RI + in_row) * (int)a.token_stride) + piece(i));
     }
     int next = ta;
     const auto issue = [&](int buf) {
-        const uint32_t dst = my_lds + (uint32_t)(buf * kBytes);
+        const uint32_t dst = my_lds + (uint32_t)buf * my_ring;
         if constexpr (P16) {
             const bool ok = (uint32_t)page < (uint32_t)a.n_pages;
             if (fresh) src = my_base + 2 * ((int64_t)(ok ? page : 0) * a.page_stride + (int64_t)off * a.token_stride);
             if (ok) {
 #pragma unroll
-                for (int i = 0; i < NI; i += 2) lds_dma16x2(src, voff[i], voff[i + 1], dst + 1024 * i);
+                for (int i = 0; i < NI; i += 2) lds_dma16x2(src, voff[i], voff[i + 1], dst + i * my_step, my_step);
             } else {
 #pragma unroll
-                for (int i = 0; i < NI; i += 2) lds_dma16x2(kNanRow, 0, 0, dst + 1024 * i);
+                for (int i = 0; i < NI; i += 2) lds_dma16x2(kNanRow, 0, 0, dst + i * my_step, my_step);
             }
             off += kAttnTile;
             src += 2 * kAttnTile * (int)a.token_stride;
@@ -608,9 +627,9 @@ __device__ __forceinline__ void prefix_part(const AttnShared &a, AttnLds<D, true
             const uint32_t bad = kt.find(next * kAttnTile, 0, a.prefix_len, lane);
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int row = row0 + i * RI + lane / LR;
+                const int row = row0 + i * RI + in_row;
                 const uint8_t *p = my_base + kt.row(row) + piece(i);
-                lds_dma16((bad >> row) & 1u ? reinterpret_cast<const uint8_t *>(kNanRow) : p, dst + 1024 * i);
+                lds_dma16((bad >> row) & 1u ? reinterpret_cast<const uint8_t *>(kNanRow) : p, dst + i * my_step);
             }
         }
         ++next;
@@ -622,12 +641,27 @@ __device__ __forceinline__ void prefix_part(const AttnShared &a, AttnLds<D, true
     for (int i = 0; i < 3; ++i)
         if (i < ahead && next < t_split) issue(i);
     const auto load_k = [&](int buf) {
-        const uint8_t *kb = lds.kv[0][buf];
+        const uint8_t *kb = lds.ring.k[buf];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int s = 0; s < D / 32; ++s)
                 w.k[h][s] = *reinterpret_cast<const u32x4_t *>(kb + (16 * h + j) * 2 * D + 16 * ((4 * s + g) ^ swizzle(16 * h + j)));
+    };
+    // the values' operands: of 16 dims 16 e .. and 4 keys each, read transposed
+    u32x4_t va[D / 16];
+    const int v_at = D == 64    ? (g >> 1) * Lds::kBlock + (g & 1) * 128 + 8 * j
+                     : D == 128 ? g * Lds::kBlock + 8 * j
+                                : (2 * g + (j >> 3)) * Lds::kBlock + 8 * (j & 7);
+    const auto load_v = [&](int buf) {
+        const uint8_t *vb = lds.ring.v[buf] + v_at;
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const u32x2_t r = read_transposed(vb + h * (16 / RI) * Lds::kBlock + e * (D == 64 ? 256 : 32 * RI));
+                va[e][2 * h] = r.x, va[e][2 * h + 1] = r.y;
+            }
     };
     float4_t sc[RT][2];
     if (ta < t_split) {
@@ -652,15 +686,17 @@ __device__ __forceinline__ void prefix_part(const AttnShared &a, AttnLds<D, true
         if (next < t_split) issue(my_keys ? buf : buf2);
         if (work) {
             load_k(buf1);                    // (past the last tile: not used)
-            const uint8_t *vb = lds.kv[1][buf];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) load_dwords<D / 32>(vb + (16 * (i / 4) + 4 * g + i % 4) * 2 * D + D / 8 * j, w.v[i]);
+            load_v(buf);
             const bool edge = key0 + kAttnTile > w.lim_hi;
             u32x4_t p[RT];
             if (edge) {
 #pragma unroll
                 for (int t = 0; t < RT; ++t) w.mask(sc[t], t, key0, 0, 0, g);
-                w.clear_unseen(key0, 0, g);
+                const u32x4_t keep = w.keys_kept(key0, 0, w.lim_hi, g);
+#pragma unroll
+                for (int e = 0; e < D / 16; ++e)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) va[e][i] &= keep[i];
             }
 #pragma unroll
             for (int t = 0; t < RT; ++t) w.raise(sc[t], t, a.scale2);
@@ -669,27 +705,33 @@ __device__ __forceinline__ void prefix_part(const AttnShared &a, AttnLds<D, true
                 p[t] = w.weights(sc[t], t, a.scale2);
                 w.scores(sc[t], t);          // of the next tile
             }
-            w.values(p);
+            w.values(p, va);
         }
         buf = buf1;
     }
+    for (int tile = t_split; tile < t_last; ++tile) {
+        const int key0 = tile * kAttnTile;
+        __syncthreads();
+        issue(0);
+        wait_vmcnt<0>();
+        __syncthreads();
+        if (w.lim_hi > key0) {
+            load_k(0);
+            load_v(0);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) w.mixed_tile(t, a.scale2, key0, 0, 0, g, [&](int e) { return va[e]; });
+        }
+    }
     __syncthreads();                         // (the tile buffers become O areas)
     float *area = &lds.o[wave][0][0];
-    for (int tile = t_split; tile < tb; ++tile) {
-        const int key0 = tile * kAttnTile;
-        if (w.lim_hi <= key0) break;
-        const uint32_t bad = kt.find(key0, 0, w.lim_hi, lane);
-#pragma unroll
-        for (int t = 0; t < RT; ++t) w.mixed_tile(kt, t, a.scale2, key0, 0, bad, area, j, g);
-    }
     w.finish(0);
     const int grp = (int)a.group.d, nsplit = a.splits_p + (a.wgs_o ? (int)a.splits_o.d : 0);
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        w.o_to_lds(area, t, j, g);
-        if (g == 0) lds.m[wave][j] = w.m[t], lds.l[wave][j] = w.l[t];
+        w.template o_to_lds<true>(area, t, j, g);
+        if (g == 0) lds.m[wave][j] = w.m[t], lds.l[wave][j] = w.l[t][0];
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         const int rows_here = min(a.rows_p - r0 - 16 * t, 16);
