@@ -12,12 +12,13 @@
 //    scores of keys 4g..4g+3 of each 16-key half for row j.
 //  * O^T += V^T P^T: B = P^T needs, in lane (j, g), 8 keys of row j: exactly the two
 //    halves' scores of that lane, rounded.  A = V^T takes the same 8 keys {4g+i, 16+4g+i} of
-//    dims d = DPL*c + e (c = lane%16, one MFMA per e): a lane holds DPL consecutive dims
-//    of those 8 value rows and pairs keys up with one v_perm_b32 a dword.
+//    16 dims per MFMA e (c = lane%16): d = DPL*c + e in the own part, where a lane holds DPL
+//    consecutive dims of those 8 value rows and pairs keys up with one v_perm_b32 a dword, and
+//    d = 16 e + c in the prefix part, which reads them transposed from LDS.
+//  * l += 1 P^T, one more MFMA: the sum takes the rounded weights that the values take.
 // So a score never leaves its lane: no lane exchange per step.  The reference m_r is only
-// raised when some score passes it by 2^8 (a ballot decides), and the sum of a row stays
-// spread over its four lanes until the end; f32 has room for terms up to 2^8 and the 16-bit
-// P for them too.
+// raised when some score passes it by 2^8 (a ballot decides); f32 has room for terms up to 2^8
+// and the 16-bit P for them too.
 //
 // A key head's rows are (query token, query head of its group).  Two parts, one launch:
 //  * own keys (own_part): a workgroup takes up to 16 rows of one sequence; its waves take
@@ -28,9 +29,12 @@
 //    different rows (16 RTP each) of the same key tiles, which go to LDS once per workgroup by
 //    16-byte LDS-DMA loads, two tiles ahead, one barrier a tile.  A key row's 16-byte pieces
 //    sit XOR-swizzled by its number, so that the 16 rows of an operand read meet 16 different
-//    bank groups.  (Key operands straight from the cache touch 64 lines an instruction, 16 rows
+//    bank groups; values sit so that a transposing read's 4 rows x 16 dims are 128 bytes in a row.
+//    (Key operands straight from the cache touch 64 lines an instruction, 16 rows
 //    x 4 pieces: with every wave reading them so, the L1's tag rate held 64 sequences over
-//    32768 keys at 123 us.)  Issue-bound: ~150 VALU instructions per 32 keys x 32 rows.
+//    32768 keys at 123 us.)  Of 32 keys x 32 rows ~100
+//    VALU and 34 matrix instructions: bound by issue with two workgroups on a CU (0.9 us a tile for
+//    both), by the latency of a tile's steps with one (0.75).
 //    Few rows, or a short prefix of few sequences, go the own part's way instead.
 // Workgroups that read the same prefix keys for other rows get launch numbers 8 apart: the same XCD, whose
 // L2 then serves all but one of them (four row groups over 8192 keys: 56 us spread over the XCDs, 48 so).
@@ -749,8 +753,8 @@ __device__ __forceinline__ void prefix_part(const AttnShared &a, AttnLds<D, true
 // Measured with 32 query and 8 key heads of 128, bfloat16, in a graph: one sequence of 777 keys 11.0 us (3.2 MB:
 // latency of seven dependent tiles); of 100000 75.7 us (410 MB, 5.4 TB/s); 16 sequences over 4096 shared keys
 // and up to 513 own 15.9 us with the join (36 MB); 64 over 32768 and up to 1025 77 us (270 MB, 3.5 TB/s: a
-// prefix tile costs ~0.75 us of issue per 256 rows on a CU, of which HBM needs 0.65, and the splits' results
-// are written and read back, 2 x 17 MB).
+// prefix tile takes 0.75 us where HBM would need 0.35, and the splits' results are written and read back,
+// 2 x 17 MB).
 template <typename CT, int D, int RTP, bool P16>
 __global__ __launch_bounds__(64 * kAttnWaves, D == 256 ? 1 : 2) void attn_rows(AttnShared a) {
     __shared__ AttnLds<D, (RTP > 0)> lds;
