@@ -195,6 +195,32 @@ def test_layer_one_expert_takes_all():
     run(5, 1, 8, 4, 64, 64, ids=[[7, 7, 7, 7]])
 
 
+def test_layer_many_pairs():
+    """The most tokens with the most experts each, some experts chosen far more often than others, a token's twice."""
+    rng = np.random.default_rng(70)
+    ids = np.minimum(rng.geometric(0.08, (64, 32)) - 1, 39)
+    run(70, 64, 40, 32, 64, 64, ids=ids)
+    ids[rng.random(ids.shape) < 0.3] = -1                              # most tokens are NaN then; the others not
+    ids[10:20] = np.arange(32)
+    run(71, 64, 40, 32, 64, 128, ids=ids)
+
+
+@pytest.mark.parametrize("ne", [300, 8192])
+def test_layer_many_experts(ne):
+    """More experts than pairs, few of them chosen, the last among them."""
+    ff, K, tokens = 64, 64, 33
+    few = [experts(80 + i, 8, *s) for i, s in enumerate(((ff, K), (ff, K), (K, ff)))]
+    wg, wu, wd = (np.concatenate([w] * (ne // 8 + 1))[:ne] for w in few)
+    rng = np.random.default_rng(ne)
+    ids = rng.integers(0, ne, (tokens, 2)).astype(np.int32)
+    ids[::5, 0], ids[1::7, 1] = ne - 1, 0
+    w = rng.dirichlet(np.ones(2), tokens).astype(np.float32)
+    x = synth.activations(81, 0, 0, tokens, K)
+    got = B.q2_0_moe_layer(dev(wg), dev(wu), dev(wd), ne, ff, K, dev(x), dev(ids), dev(w)).double().cpu().numpy()
+    y, tol = layer(wg, wu, wd, ff, K, x, ids, w)
+    assert np.all(np.abs(got - y) <= tol)
+
+
 def test_layer_ids_out_of_range():
     ids = np.array([[0, 1], [-1, 2], [3, 4], [2, 0], [1000000, -5]])
     run(6, 5, 4, 2, 128, 192, ids=ids)
