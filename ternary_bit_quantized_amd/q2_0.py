@@ -557,7 +557,7 @@ def q2_0_kv_append(k_cache, v_cache, table, seq, pos, k, v, rope=None, style: in
             raise ValueError("q must have whole heads of %d elements" % c.head_dim)
         ldq, qp = _rows(q, n, q.shape[1], "q"), q.data_ptr()
         if q_out is None:
-            q_out = torch.empty((n, q.shape[1]), dtype=k_cache.dtype, device=q.device)
+            q_out = k_cache.new_empty((n, q.shape[1]))
         elif q_out.dtype != k_cache.dtype:
             raise ValueError("q_out must have the cache's dtype")
         ldo, op = _rows(q_out, n, q.shape[1], "q_out"), q_out.data_ptr()
@@ -589,7 +589,7 @@ def q2_0_attn_shared(q, k_cache, v_cache, table, lens, scale: float, prefix_len:
         raise ValueError("q must have the cache's dtype and whole heads of %d elements" % c.head_dim)
     ldq = _rows(q, n_seqs * n_qt, width, "q")
     if out is None:
-        out = torch.empty((n_seqs * n_qt, width), dtype=q.dtype, device=q.device)
+        out = q.new_empty((n_seqs * n_qt, width))
     elif out.dtype != q.dtype:
         raise ValueError("out must have the cache's dtype")
     ldo = _rows(out, n_seqs * n_qt, width, "out")
@@ -597,7 +597,7 @@ def q2_0_attn_shared(q, k_cache, v_cache, table, lens, scale: float, prefix_len:
         max_len = cols * c.page_size
     need = attn_shared_workspace_bytes(n_seqs, n_q, c.n_kv, c.head_dim, n_qt, prefix_len, max_len)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(need, dtype=torch.uint8)
     wsp = workspace.data_ptr() if workspace is not None else 0
     wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(attn_shared_raw(c, tp, n_seqs, cols, ldt, _int32(lens, (n_seqs,), "lens"), prefix_len, max_len, q.data_ptr(),
@@ -616,9 +616,9 @@ def q2_0_moe_route(logits, n_used: int, normalise: bool = True, ids=None, weight
         raise ValueError("logits must be float32, float16 or bfloat16")
     ld = _rows(logits, n, n_expert, "logits")
     if ids is None:
-        ids = torch.empty((n, n_used), dtype=torch.int32, device=logits.device)
+        ids = logits.new_empty((n, n_used), dtype=torch.int32)
     if weights is None:
-        weights = torch.empty((n, n_used), dtype=torch.float32, device=logits.device)
+        weights = logits.new_empty((n, n_used), dtype=torch.float32)
     if weights.dtype != torch.float32 or weights.shape != (n, n_used) or not weights.is_cuda or \
             not weights.is_contiguous():
         raise ValueError("weights must be a contiguous float32 CUDA tensor (n_tokens, n_used)")
@@ -644,13 +644,13 @@ def q2_0_moe_layer(w_gate, w_up, w_down, n_expert: int, n_ff: int, K: int, x, id
                 w.numel() * w.element_size() < n_expert * n_ff * K // BLOCK_WEIGHTS * BLOCK_BYTES:
             raise ValueError("%s must be a contiguous CUDA tensor that holds n_expert matrices" % name)
     if y is None:
-        y = torch.empty((n, K), dtype=torch.float32, device=x.device)
+        y = x.new_empty((n, K), dtype=torch.float32)
     yp, yn, ldy = _cols(y, K, "y")
     if yn != n:
         raise ValueError("y must have n_tokens rows")
     need = moe_layer_workspace_bytes(n_ff, K, n_used, n)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = x.new_empty(need, dtype=torch.uint8)
     wsp = workspace.data_ptr() if workspace is not None else 0
     wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(moe_layer_raw(w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), n_expert, n_ff, K, xp, xt, ldx,
