@@ -832,12 +832,12 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t n_q, int64_t n_kv, int64_t dim, int64
     };
     p.groups_o = div_up(rows_o, 16);
     // The prefix has a part of its own unless it is of one sequence with one tile of rows, or all is
-    // short and few: then a workgroup takes all of a sequence's keys, prefix included (read once per
-    // sequence, from the L2), and writes the result itself, without a join: 8 sequences of 2 key heads
-    // with 1001 keys 9.4 against 10.4 us; 16 of 8 key heads with 1200 keys 14.7 against 13.8, 32 of them 19.6
-    // against 17.1.
+    // short and few: then a sequence's workgroups take all of its keys, prefix included (read once per
+    // sequence, from the L2).  In us, so and with a part of its own: 8 sequences of 4 query tokens and 2 key
+    // heads with 1300 keys 9.3 and 10.1, with 1750 9.9 and 10.3; 8 sequences of 8 key heads with 1000 keys
+    // 9.4 and 9.5, with 1300 11.6 and 11.4, with 1600 12.7 and 11.3; 16 of them with 1200 keys 14.7 and 13.8.
     const int64_t wgs = n_seqs * n_kv * p.groups_o;
-    p.joint = prefix_len > 0 && ((n_seqs == 1 && rows_p <= 16) || (tiles(max_len) <= 40 && wgs <= 64));
+    p.joint = prefix_len > 0 && ((n_seqs == 1 && rows_p <= 16) || (tiles(max_len) <= 56 && tiles(max_len) * wgs <= 2304));
     const bool shared = prefix_len > 0 && !p.joint;
     if (shared) {
         // Row tiles of a wave (2 read the tiles from LDS half as often, 1 gives twice the workgroups; 256 dims
