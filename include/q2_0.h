@@ -428,13 +428,15 @@ int q2_0_kv_append(const q2_0_kv_cache *cache, const int32_t *table, int64_t n_s
  *            through their sequence's row.
  *   lens   : DEVICE int32 [n_seqs]: tokens of each sequence, the prefix and its own query
  *            tokens included, so query j of sequence s sees keys i < lens[s] - n_qt + 1 + j.
+ *            A sequence may end inside the prefix; it then costs the sequences that share its
+ *            workgroup about twice the time for the rest of the prefix (length 0 costs nothing).
  *   max_len: bound on lens (host), prefix_len <= max_len <= table_len*page_size; it only
  *            sets how the work is split.
  *   scale  : finite and positive; scores are scale * (q . k).
  *   out    : rows as q's, element type of the cache, at out + row*ldo.
  * The result is sum_i softmax_i(score) v_i, softmax statistics and sums in f32; the softmax
- * weights are rounded to the cache's type for the matrix cores (relative 2^-8 for BF16 at most,
- * 2^-11 for F16, each key by itself), the result once more.  A query that sees no key (or only
+ * weights are rounded to the cache's type for the matrix cores, in their sum as in the values'
+ * (relative 2^-8 for BF16 at most, 2^-11 for F16, each key by itself), the result once more.  A query that sees no key (or only
  * scores of -inf) gives zeros.  Keys and values that a query does not see are never part
  * of its result, whatever they hold (NaN and inf included).  lens[s] outside
  * [0, max_len], or a page outside [0, n_pages) among the keys a query sees, gives NaN
