@@ -312,14 +312,17 @@ struct Rows {
     }
 };
 
-// Two 16-byte LDS-DMA loads per lane (lds_dma.h) to kilobytes step apart, with a uniform base and a byte offset per lane.
+// Two 16-byte LDS-DMA loads per lane (lds_dma.h, the wait after a write of M0 too) to kilobytes step apart, with a uniform
+// base and a byte offset per lane.
 __device__ __forceinline__ void lds_dma16x2(const void *base, uint32_t off0, uint32_t off1, uint32_t lds, uint32_t step) {
     uint32_t saved;
     asm volatile(
         "s_mov_b32 %0, m0\n\t"
         "s_mov_b32 m0, %4\n\t"
+        "s_nop 0\n\t"
         "global_load_lds_dwordx4 %1, %3\n\t"
         "s_add_u32 m0, m0, %5\n\t"
+        "s_nop 0\n\t"
         "global_load_lds_dwordx4 %2, %3\n\t"
         "s_mov_b32 m0, %0"
         : "=&s"(saved)

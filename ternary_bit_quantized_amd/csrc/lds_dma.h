@@ -12,12 +12,15 @@ namespace q2_0 {
 // loads (it cannot tell that they fill a different buffer).  The caller orders them
 // with wait_vmcnt before the barrier that publishes the tile.
 // M0 (the LDS address) is saved and restored around the load, so the compiler's view of
-// it does not change.
+// it does not change.  Between a scalar write of M0 and an LDS-DMA load that uses it the
+// hardware needs one wait state, which the compiler's hazard pass cannot add inside the
+// assembly: the s_nop.
 __device__ __forceinline__ void lds_dma16(const void *src, uint32_t lds) {
     uint32_t saved;
     asm volatile(
         "s_mov_b32 %0, m0\n\t"
         "s_mov_b32 m0, %2\n\t"
+        "s_nop 0\n\t"
         "global_load_lds_dwordx4 %1, off\n\t"
         "s_mov_b32 m0, %0"
         : "=&s"(saved)
