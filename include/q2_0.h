@@ -436,7 +436,9 @@ int q2_0_kv_append(const q2_0_kv_cache *cache, const int32_t *table, int64_t n_s
  *   out    : rows as q's, element type of the cache, at out + row*ldo.
  * The result is sum_i softmax_i(score) v_i, softmax statistics and sums in f32; the softmax
  * weights are rounded to the cache's type for the matrix cores, in their sum as in the values'
- * (relative 2^-8 for BF16 at most, 2^-11 for F16, each key by itself), the result once more.  A query that sees no key (or only
+ * (relative 2^-8 for BF16 at most, 2^-11 for F16, each key by itself; in F16 by 2^-35 of the row's largest weight at least,
+ * which only keys below 2^-24 of it feel), the result once more.  Scores beyond 2^20 either way are past what f32 exponents
+ * resolve; their weights may come out as NaN.  A query that sees no key (or only
  * scores of -inf) gives zeros.  Keys and values that a query does not see are never part
  * of its result, whatever they hold (NaN and inf included).  lens[s] outside
  * [0, max_len], or a page outside [0, n_pages) among the keys a query sees, gives NaN

@@ -17,8 +17,10 @@
 //    d = 16 e + c in the prefix part, which reads them transposed from LDS.
 //  * l += 1 P^T, one more MFMA: the sum takes the rounded weights that the values take.
 // So a score never leaves its lane: no lane exchange per step.  The reference m_r is only
-// raised when some score passes it by 2^8 (a ballot decides); f32 has room for terms up to 2^8
-// and the 16-bit P for them too.
+// raised when some score passes it by a headroom (a ballot decides), for which f32 and P have room.
+// f16 has no room below: weights under 2^-25 would be lost, which tens of thousands of keys behind a
+// leading one add up to (30000 of them at 2^-26 are 4e-4 of the sum).  So its weights carry a factor 2^11, in O and l
+// alike, which puts their last place at 2^-35 of the reference's, and the headroom is 2^4.
 //
 // A key head's rows are (query token, query head of its group).  Two parts, one launch:
 //  * own keys (own_part): a workgroup takes up to 16 rows of one sequence; its waves take
@@ -58,6 +60,7 @@ struct Mma;
 template <>
 struct Mma<_Float16> {
     static constexpr uint32_t kOnes = 0x3c003c00u;
+    static constexpr float kHead = 4.f, kBias = 11.f;     // of the weights, as powers of two; together at most 15
     static __device__ __forceinline__ float4_t mul(u32x4_t a, u32x4_t b, float4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c,
                                                       0, 0, 0);
@@ -66,6 +69,7 @@ struct Mma<_Float16> {
 template <>
 struct Mma<bf16_t> {
     static constexpr uint32_t kOnes = 0x3f803f80u;
+    static constexpr float kHead = 8.f, kBias = 0.f;
     static __device__ __forceinline__ float4_t mul(u32x4_t a, u32x4_t b, float4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8_t, a), __builtin_bit_cast(bf8_t, b), c, 0,
                                                        0, 0);
@@ -133,7 +137,7 @@ struct Rows {
 
     u32x4_t q[RT][KS];       // queries as the scores' B operand
     float4_t o[RT][DPL];
-    float m[RT], ms[RT];     // reference (-inf: none yet), the same as a number
+    float m[RT], ms[RT];     // reference (-inf: none yet); the weights' exponents are relative to ms
     float4_t l[RT];          // row j's sum, four times
     int lim[RT];             // keys row j sees
     int lim_lo, lim_hi;      // the least (of rows that see some key past k_lo) and most of the wave's rows
@@ -187,18 +191,18 @@ struct Rows {
                 if (key0 + kk >= lim[t] || key0 + kk < k_lo) s[h][i] = -__builtin_inff();
             }
     }
-    // Where a score passes its row's reference by 2^8: raises the rows' references to their maxima so far
+    // Where a score passes its row's reference by 2^kHead: raises the rows' references to their maxima so far
     // and rescales what they hold.
     __device__ __forceinline__ void raise(const float4_t (&s)[2], int t, float scale2) {
         const float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
                                 fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3]))) *
                           scale2;
-        if (__ballot(top > m[t] + 8.f)) {
+        if (__ballot(top > m[t] + Mma<CT>::kHead)) {
             float mx = fmaxf(m[t], top);
             mx = fmaxf(mx, __shfl_xor(mx, 16));
             mx = fmaxf(mx, __shfl_xor(mx, 32));
-            const float mn = mx == -__builtin_inff() ? 0.f : mx;
-            const float f = m[t] == mx ? 1.f : __builtin_amdgcn_exp2f(m[t] - mn);
+            const float mn = mx == -__builtin_inff() ? 0.f : mx - Mma<CT>::kBias;
+            const float f = m[t] == mx ? 1.f : __builtin_amdgcn_exp2f(m[t] == -__builtin_inff() ? m[t] : ms[t] - mn);
             m[t] = mx;
             ms[t] = mn;
 #pragma unroll
@@ -297,8 +301,8 @@ struct Rows {
         }
         settle();
     }
-    // Row j's final reference and sum; rows that saw nothing hold nothing (a row that saw nothing but NaN has
-    // no reference either, and keeps its NaN).
+    // Row j's final reference, which its weights were relative to, and sum; rows that saw nothing hold nothing (a
+    // row that saw nothing but NaN has no reference either, and keeps its NaN).
     __device__ __forceinline__ void finish(int k_lo) {
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
@@ -308,6 +312,7 @@ struct Rows {
 #pragma unroll
                 for (int e = 0; e < DPL; ++e) o[t][e] = float4_t{0.f, 0.f, 0.f, 0.f};
             }
+            if (m[t] != -__builtin_inff()) m[t] = ms[t];
         }
     }
 };
