@@ -11,11 +11,16 @@
 //    the cache; B = Q^T, loaded once.  D: lane (row j = lane%16, g = lane/16) holds the
 //    scores of keys 4g..4g+3 of each 16-key half for row j.
 //  * O^T += V^T P^T: B = P^T needs, in lane (j, g), 8 keys of row j: exactly the two
-//    halves' scores of that lane, rounded.  A = V^T takes the same 8 keys {4g+i, 16+4g+i} of
+//    halves' scores of that lane, as two operands: the weight rounded to 16 bits and what that left, again
+//    in 16 bits.  With the first alone results erred 1.4 times as much as with weights in f32 (relative to
+//    64 bits 2.3e-3 against 1.65e-3 in bfloat16, whose own rounding is most of that), and the difference of
+//    nearly equal weights was lost; with both the two err alike, for half as many matrix
+//    instructions again (64 sequences over 32768 keys 77 -> 87 us, 16 over 4096 15.9 -> 16.5, one of 777 11.1 -> 11.5).
+//    A = V^T takes the same 8 keys {4g+i, 16+4g+i} of
 //    16 dims per MFMA e (c = lane%16): d = DPL*c + e in the own part, where a lane holds DPL
 //    consecutive dims of those 8 value rows and pairs keys up with one v_perm_b32 a dword, and
 //    d = 16 e + c in the prefix part, which reads them transposed from LDS.
-//  * l += 1 P^T, one more MFMA: the sum takes the rounded weights that the values take.
+//  * l += 1 P^T, two more MFMAs: the sum takes the same operands as the values.
 // So a score never leaves its lane: no lane exchange per step.  The reference m_r is only
 // raised when some score passes it by a headroom (a ballot decides), for which f32 and P have room.
 // f16 has no room below: weights under 2^-25 would be lost, which tens of thousands of keys behind a
@@ -34,9 +39,9 @@
 //    bank groups; values sit so that a transposing read's 4 rows x 16 dims are 128 bytes in a row.
 //    (Key operands straight from the cache touch 64 lines an instruction, 16 rows
 //    x 4 pieces: with every wave reading them so, the L1's tag rate held 64 sequences over
-//    32768 keys at 123 us.)  Of 32 keys x 32 rows ~100
-//    VALU and 34 matrix instructions: bound by issue with two workgroups on a CU (0.9 us a tile for
-//    both), by the latency of a tile's steps with one (0.75).
+//    32768 keys at 123 us.)  Of 32 keys x 32 rows ~120
+//    VALU and 52 matrix instructions: bound by issue with two workgroups on a CU, by the latency of a
+//    tile's steps with one.
 //    Few rows, or a short prefix of few sequences, go the own part's way instead.
 // Workgroups that read the same prefix keys for other rows get launch numbers 8 apart: the same XCD, whose
 // L2 then serves all but one of them (four row groups over 8192 keys: 56 us spread over the XCDs, 48 so).
@@ -127,6 +132,24 @@ __device__ __forceinline__ int table_at(const int32_t *t, int i) {
     return ((ConstPtr)(uintptr_t)t)[i];
 }
 
+// Softmax weights of 8 keys for a row, as the second product takes them: the weight in the cache's type and what
+// that rounding left, again in that type.
+struct Weights {
+    u32x4_t hi, lo;
+};
+
+template <typename CT>
+__device__ __forceinline__ float2_t unpack2(uint32_t v);
+template <>
+__device__ __forceinline__ float2_t unpack2<_Float16>(uint32_t v) {
+    const half2_t h = __builtin_bit_cast(half2_t, v);
+    return float2_t{(float)h.x, (float)h.y};
+}
+template <>
+__device__ __forceinline__ float2_t unpack2<bf16_t>(uint32_t v) {
+    return float2_t{__builtin_bit_cast(float, v << 16), __builtin_bit_cast(float, v & 0xffff0000u)};
+}
+
 // What a wave knows of its rows, RT tiles of 16, and holds of their results.
 template <typename CT, int D, int RT>
 struct Rows {
@@ -213,12 +236,20 @@ struct Rows {
                 for (int i = 0; i < 4; ++i) o[t][e][i] *= f;
         }
     }
-    // Scores to weights P, rounded to the cache's type (the matrix cores' operand).
-    __device__ __forceinline__ u32x4_t weights(const float4_t (&s)[2], int t, float scale2) {
-        float w[8];
+    // Scores to weights P, as two operands of the matrix cores.
+    __device__ __forceinline__ Weights weights(const float4_t (&s)[2], int t, float scale2) {
+        Weights p;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 4][i % 4], scale2, -ms[t]));
-        return u32x4_t{pack2<CT>(w[0], w[1]), pack2<CT>(w[2], w[3]), pack2<CT>(w[4], w[5]), pack2<CT>(w[6], w[7])};
+        for (int i = 0; i < 4; ++i) {
+            float w[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) w[h] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 2][2 * (i % 2) + h], scale2, -ms[t]));
+            const uint32_t hi = pack2<CT>(w[0], w[1]);
+            const float2_t r = unpack2<CT>(hi);
+            p.hi[i] = hi;
+            p.lo[i] = pack2<CT>(w[0] - r.x, w[1] - r.y);
+        }
+        return p;
     }
     // the value tile's operand of dim e: its 8 keys' halves
     __device__ __forceinline__ u32x4_t v_operand(int e) const {
@@ -238,19 +269,24 @@ struct Rows {
         }
         return keep;
     }
-    // l += P 1, from the rounded weights, as the values are.
-    __device__ __forceinline__ void sums(const u32x4_t &p, int t) {
+    // l += P 1, from the same operands as the values' sum.
+    __device__ __forceinline__ void sums(const Weights &p, int t) {
         constexpr uint32_t one = Mma<CT>::kOnes;
-        l[t] = Mma<CT>::mul(u32x4_t{one, one, one, one}, p, l[t]);
+        const u32x4_t ones = {one, one, one, one};
+        l[t] = Mma<CT>::mul(ones, p.lo, Mma<CT>::mul(ones, p.hi, l[t]));
     }
     // O += P V; va[e]: the operands
-    __device__ __forceinline__ void values(const u32x4_t (&p)[RT], const u32x4_t (&va)[DPL]) {
+    __device__ __forceinline__ void values(const Weights (&p)[RT], const u32x4_t (&va)[DPL]) {
 #pragma unroll
         for (int t = 0; t < RT; ++t) sums(p[t], t);
 #pragma unroll
         for (int e = 0; e < DPL; ++e)
 #pragma unroll
-            for (int t = 0; t < RT; ++t) o[t][e] = Mma<CT>::mul(va[e], p[t], o[t][e]);
+            for (int t = 0; t < RT; ++t) o[t][e] = Mma<CT>::mul(va[e], p[t].hi, o[t][e]);
+#pragma unroll
+        for (int e = 0; e < DPL; ++e)
+#pragma unroll
+            for (int t = 0; t < RT; ++t) o[t][e] = Mma<CT>::mul(va[e], p[t].lo, o[t][e]);
     }
     // Row tile t's O in a wave's LDS area of 16 rows; an operand's dims are DPL apart, or 16 in a row (ROW16).
     template <bool ROW16>
@@ -279,7 +315,7 @@ struct Rows {
         settle();
         mask(s, t, key0, k_lo, bad, g);
         raise(s, t, scale2);
-        const u32x4_t p = weights(s, t, scale2);
+        const Weights p = weights(s, t, scale2);
         sums(p, t);
         int done = max(key0, k_lo);             // (rows of limits up to here see nothing in this tile)
 #pragma unroll 1
@@ -294,7 +330,7 @@ struct Rows {
                 u32x4_t va = operand(e);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) va[i] &= keep[i];
-                const float4_t r = Mma<CT>::mul(va, p, float4_t{0.f, 0.f, 0.f, 0.f});
+                const float4_t r = Mma<CT>::mul(va, p.lo, Mma<CT>::mul(va, p.hi, float4_t{0.f, 0.f, 0.f, 0.f}));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[t][e][i] = mine ? o[t][e][i] + r[i] : o[t][e][i];
             }
@@ -493,7 +529,8 @@ __device__ __forceinline__ void own_part(const AttnShared &a, AttnLds<D, PRE> &l
         const int key0 = tile * kAttnTile;
         const bool edge = key0 < k_lo || key0 + kAttnTile > w.lim_hi || bad != 0;   // some key needs a mask
         float4_t s[2];
-        u32x4_t p[1], va[D / 16];
+        Weights p[1];
+        u32x4_t va[D / 16];
         w.scores(s, 0);
         if (more) kt.load_k(w, j, g);
         if (edge) w.mask(s, 0, key0, k_lo, bad, g);
@@ -700,7 +737,7 @@ __device__ __forceinline__ void prefix_part(const AttnShared &a, AttnLds<D, true
             load_k(buf1);                    // (past the last tile: not used)
             load_v(buf);
             const bool edge = key0 + kAttnTile > w.lim_hi;
-            u32x4_t p[RT];
+            Weights p[RT];
             if (edge) {
 #pragma unroll
                 for (int t = 0; t < RT; ++t) w.mask(sc[t], t, key0, 0, 0, g);
