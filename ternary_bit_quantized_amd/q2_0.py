@@ -310,6 +310,25 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(like, shape, dtype, stream, result=True):
+    """A new tensor on like's device for a call whose kernels run on `stream`.  Its memory is that stream's: what the
+    allocator gives and takes back is in order with the kernels, though another stream is current.  The caller may
+    read a result on the current stream and free it then, so the allocator is told of that one too."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+    handle, current = _stream(stream), torch.cuda.current_stream()
+    if handle == current.cuda_stream:
+        return like.new_empty(shape, dtype=dtype)
+    if not isinstance(stream, torch.cuda.Stream):       # (a handle of 0 is the default stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    if result:
+        t.record_stream(current)
+    return t
+
+
 def _cols(t, K, name):
     """A (N, >=K) float32 device tensor with unit column stride -> (ptr, N, ld)."""
     import torch
@@ -348,11 +367,11 @@ def q2_0_mul_mat_id(w, n_expert: int, M: int, K: int, x, ids, precision: int = Q
         raise ValueError("x must have n_tokens or n_tokens * n_used rows")
     x_slots = 1 if rows == n_tokens else n_used
     if y is None:
-        y = torch.empty((n_tokens * n_used, M), dtype=torch.float32, device=x.device)
+        y = _empty(x, (n_tokens * n_used, M), torch.float32, stream)
     yp, _, ldy = _cols(y, M, "y")
     need = mul_mat_id_workspace_bytes(n_expert, M, K, n_used, n_tokens, precision)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        workspace = _empty(x, max(need, 16), torch.uint8, stream, result=False)
     wsb = workspace.numel() * workspace.element_size()
     _check(mul_mat_id_raw(w.data_ptr(), n_expert, M, K, xp, xt, ldx, x_slots, ids.data_ptr(), n_used, n_tokens,
                           yp, ldy, precision, workspace.data_ptr(), wsb, _stream(stream)), "q2_0_mul_mat_id")
@@ -365,7 +384,7 @@ def q2_0_quantize(src, w=None, stream=None):
     M, K = src.shape
     ptr, _, ld = _cols(src, K, "src")
     if w is None:
-        w = torch.empty((M, K // BLOCK_WEIGHTS * BLOCK_BYTES), dtype=torch.uint8, device=src.device)
+        w = _empty(src, (M, K // BLOCK_WEIGHTS * BLOCK_BYTES), torch.uint8, stream)
     _check(quantize_raw(ptr, M, K, ld, w.data_ptr(), _stream(stream)), "q2_0_quantize")
     return w
 
@@ -374,7 +393,7 @@ def q2_0_repack_g128(w128, M: int, K: int, w=None, stream=None):
     """The group-64 Q2_0 tensor of a legacy group-128 tensor w128 (uint8, M rows of K/128*34 bytes)."""
     import torch
     if w is None:
-        w = torch.empty((M, K // BLOCK_WEIGHTS * BLOCK_BYTES), dtype=torch.uint8, device=w128.device)
+        w = _empty(w128, (M, K // BLOCK_WEIGHTS * BLOCK_BYTES), torch.uint8, stream)
     _check(repack_g128_raw(w128.data_ptr(), M, K, w.data_ptr(), _stream(stream)), "q2_0_repack_g128")
     return w
 
@@ -384,7 +403,7 @@ def q2_0_get_rows(w, M: int, K: int, ids, out=None, stream=None):
     import torch
     n = ids.numel()
     if out is None:
-        out = torch.empty((n, K), dtype=torch.float32, device=w.device)
+        out = _empty(w, (n, K), torch.float32, stream)
     ptr, rows, ld = _cols(out, K, "out")
     if ids.dtype != torch.int32 or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int32 tensor")
@@ -398,7 +417,7 @@ def q2_0_mul_mat_vec(w, M: int, K: int, x, y=None, stream=None):
     import torch
     xp, N, ldx, xt = _xcols(x, K, "x")
     if y is None:
-        y = torch.empty((N, M), dtype=torch.float32, device=x.device)
+        y = _empty(x, (N, M), torch.float32, stream)
     yp, _, ldy = _cols(y, M, "y")
     _check(mul_mat_vec_act_raw(w.data_ptr(), M, K, xp, xt, ldx, N, yp, ldy, _stream(stream)),
            "q2_0_mul_mat_vec_act")
@@ -411,7 +430,7 @@ def q2_0_mul_mat_vec_group(mats, K: int, x, ys=None, stream=None):
     import torch
     xp, N, ldx, xt = _xcols(x, K, "x")
     if ys is None:
-        ys = [torch.empty((N, M), dtype=torch.float32, device=x.device) for (_, M) in mats]
+        ys = [_empty(x, (N, M), torch.float32, stream) for (_, M) in mats]
     entries = []
     for (w, M), y in zip(mats, ys):
         yp, _, ldy = _cols(y, M, "y")
@@ -434,7 +453,7 @@ def q2_0_mul_mat_vec_batch(products, x_type_tensor=None, ys=None, stream=None):
             xt0, N0 = xt, N
         elif xt != xt0 or N != N0:
             raise ValueError("every x of a batch must have the same dtype and column count")
-        y = ys[i] if ys is not None else torch.empty((N, M), dtype=torch.float32, device=x.device)
+        y = ys[i] if ys is not None else _empty(x, (N, M), torch.float32, stream)
         yp, _, ldy = _cols(y, M, "y")
         entries.append((w.data_ptr(), M, K, xp, ldx, yp, ldy))
         out.append(y)
@@ -450,11 +469,11 @@ def q2_0_mul_mat(w, M: int, K: int, x, precision: int = Q2_0_PREC_F16_MFMA, y=No
     import torch
     xp, N, ldx, xt = _xcols(x, K, "x")
     if y is None:
-        y = torch.empty((N, M), dtype=torch.float32, device=x.device)
+        y = _empty(x, (N, M), torch.float32, stream)
     yp, _, ldy = _cols(y, M, "y")
     need = mul_mat_workspace_bytes(M, K, N, precision)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty(x, need, torch.uint8, stream, result=False)
     wsp = workspace.data_ptr() if workspace is not None else 0
     wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(mul_mat_act_raw(w.data_ptr(), M, K, xp, xt, ldx, N, yp, ldy, precision, wsp, wsb, _stream(stream)),
@@ -469,7 +488,7 @@ def q2_0_mul_mat_group(mats, K: int, x, precision: int = Q2_0_PREC_F16_MFMA, ys=
     import torch
     xp, N, ldx, xt = _xcols(x, K, "x")
     if ys is None:
-        ys = [torch.empty((N, M), dtype=torch.float32, device=x.device) for (_, M) in mats]
+        ys = [_empty(x, (N, M), torch.float32, stream) for (_, M) in mats]
     entries = []
     for (w, M), y in zip(mats, ys):
         yp, _, ldy = _cols(y, M, "y")
@@ -477,7 +496,7 @@ def q2_0_mul_mat_group(mats, K: int, x, precision: int = Q2_0_PREC_F16_MFMA, ys=
     items = make_items(entries)
     need = mul_mat_group_workspace_bytes(items, len(entries), K, N, precision)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty(x, need, torch.uint8, stream, result=False)
     wsp = workspace.data_ptr() if workspace is not None else 0
     wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(mul_mat_group_act_raw(items, len(entries), K, xp, xt, ldx, N, precision, wsp, wsb, _stream(stream)),
@@ -557,7 +576,7 @@ def q2_0_kv_append(k_cache, v_cache, table, seq, pos, k, v, rope=None, style: in
             raise ValueError("q must have whole heads of %d elements" % c.head_dim)
         ldq, qp = _rows(q, n, q.shape[1], "q"), q.data_ptr()
         if q_out is None:
-            q_out = k_cache.new_empty((n, q.shape[1]))
+            q_out = _empty(k_cache, (n, q.shape[1]), k_cache.dtype, stream)
         elif q_out.dtype != k_cache.dtype:
             raise ValueError("q_out must have the cache's dtype")
         ldo, op = _rows(q_out, n, q.shape[1], "q_out"), q_out.data_ptr()
@@ -589,7 +608,7 @@ def q2_0_attn_shared(q, k_cache, v_cache, table, lens, scale: float, prefix_len:
         raise ValueError("q must have the cache's dtype and whole heads of %d elements" % c.head_dim)
     ldq = _rows(q, n_seqs * n_qt, width, "q")
     if out is None:
-        out = q.new_empty((n_seqs * n_qt, width))
+        out = _empty(q, (n_seqs * n_qt, width), q.dtype, stream)
     elif out.dtype != q.dtype:
         raise ValueError("out must have the cache's dtype")
     ldo = _rows(out, n_seqs * n_qt, width, "out")
@@ -597,7 +616,7 @@ def q2_0_attn_shared(q, k_cache, v_cache, table, lens, scale: float, prefix_len:
         max_len = cols * c.page_size
     need = attn_shared_workspace_bytes(n_seqs, n_q, c.n_kv, c.head_dim, n_qt, prefix_len, max_len)
     if workspace is None and need:
-        workspace = q.new_empty(need, dtype=torch.uint8)
+        workspace = _empty(q, need, torch.uint8, stream, result=False)
     wsp = workspace.data_ptr() if workspace is not None else 0
     wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(attn_shared_raw(c, tp, n_seqs, cols, ldt, _int32(lens, (n_seqs,), "lens"), prefix_len, max_len, q.data_ptr(),
@@ -616,9 +635,9 @@ def q2_0_moe_route(logits, n_used: int, normalise: bool = True, ids=None, weight
         raise ValueError("logits must be float32, float16 or bfloat16")
     ld = _rows(logits, n, n_expert, "logits")
     if ids is None:
-        ids = logits.new_empty((n, n_used), dtype=torch.int32)
+        ids = _empty(logits, (n, n_used), torch.int32, stream)
     if weights is None:
-        weights = logits.new_empty((n, n_used), dtype=torch.float32)
+        weights = _empty(logits, (n, n_used), torch.float32, stream)
     if weights.dtype != torch.float32 or weights.shape != (n, n_used) or not weights.is_cuda or \
             not weights.is_contiguous():
         raise ValueError("weights must be a contiguous float32 CUDA tensor (n_tokens, n_used)")
@@ -644,13 +663,13 @@ def q2_0_moe_layer(w_gate, w_up, w_down, n_expert: int, n_ff: int, K: int, x, id
                 w.numel() * w.element_size() < n_expert * n_ff * K // BLOCK_WEIGHTS * BLOCK_BYTES:
             raise ValueError("%s must be a contiguous CUDA tensor that holds n_expert matrices" % name)
     if y is None:
-        y = x.new_empty((n, K), dtype=torch.float32)
+        y = _empty(x, (n, K), torch.float32, stream)
     yp, yn, ldy = _cols(y, K, "y")
     if yn != n:
         raise ValueError("y must have n_tokens rows")
     need = moe_layer_workspace_bytes(n_ff, K, n_used, n)
     if workspace is None and need:
-        workspace = x.new_empty(need, dtype=torch.uint8)
+        workspace = _empty(x, need, torch.uint8, stream, result=False)
     wsp = workspace.data_ptr() if workspace is not None else 0
     wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(moe_layer_raw(w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), n_expert, n_ff, K, xp, xt, ldx,
