@@ -303,10 +303,12 @@ def version() -> str:
 
 # ----------------------------------------------------------------------------- torch tensors
 
-def _stream(stream):
+def _stream(stream, dev=None):
     import torch
     if stream is None:      # the current stream's handle, without the Stream object around it (2.8 us)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
+    if dev is not None and getattr(stream, "device_index", dev) != dev:
+        raise ValueError("stream must be one of the current device")
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -512,39 +514,60 @@ def _act_types():
     return {torch.float32: Q2_0_ACT_F32, torch.float16: Q2_0_ACT_F16, torch.bfloat16: Q2_0_ACT_BF16}
 
 
-def _rows(t, rows, cols, name):
-    """A 2-D CUDA tensor of `rows` rows of at least `cols` elements, unit inner stride -> row stride."""
-    if t.is_cuda and t.dim() == 2:
+# These calls launch on the current device, dev: every tensor has to be there (get_device() of a CPU tensor is -1).
+
+def _rows(t, rows, cols, name, dev):
+    """A 2-D tensor of `rows` rows of at least `cols` elements, unit inner stride -> row stride."""
+    if t.get_device() == dev and t.dim() == 2:
         (n, c), (ld, inner) = t.shape, t.stride()
         if n == rows and c >= cols and (inner == 1 or c <= 1):
             return ld if rows > 1 else max(ld, c)
-    raise ValueError("%s must be a 2-D CUDA tensor of %d rows of at least %d elements with unit inner stride"
-                     % (name, rows, cols))
+    raise ValueError("%s must be a 2-D tensor on the current CUDA device of %d rows of at least %d elements with unit "
+                     "inner stride" % (name, rows, cols))
 
 
-def _int32(t, shape, name):
-    import torch
-    if t.dtype != torch.int32 or not t.is_cuda or t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous int32 CUDA tensor of shape %s" % (name, tuple(shape)))
+def _dense(t, dtype, shape, name, dev):
+    if t.dtype != dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on the current CUDA device"
+                         % (name, str(dtype).split(".")[-1], tuple(shape)))
     return t.data_ptr()
 
 
-def _table(t):
+def _wide(t, name):
+    """Columns of a 2-D tensor."""
+    if t.dim() != 2:
+        raise ValueError("%s must be a 2-D tensor" % name)
+    return t.shape[1]
+
+
+def _work(workspace, need, like, stream, dev):
+    """The workspace given, or one of `need` bytes -> (tensor or None, address, bytes)."""
+    if workspace is None:
+        if not need:
+            return None, 0, 0
+        import torch
+        workspace = _empty(like, need, torch.uint8, stream, result=False)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _table(t, dev):
     import torch
-    if t.dtype == torch.int32 and t.is_cuda and t.dim() == 2:
+    if t.dtype == torch.int32 and t.get_device() == dev and t.dim() == 2:
         (n, cols), (ld, inner) = t.shape, t.stride()
         if inner == 1 or cols <= 1:
             return t.data_ptr(), n, cols, ld if n > 1 else max(ld, cols)
-    raise ValueError("table must be a 2-D int32 CUDA tensor with unit inner stride")
+    raise ValueError("table must be a 2-D int32 tensor on the current CUDA device with unit inner stride")
 
 
-def _cache(k_cache, v_cache):
+def _cache(k_cache, v_cache, dev):
     """Pools (n_pages, n_kv, page_size, head_dim) with unit inner stride and equal strides -> KvCache."""
     shape, st = k_cache.shape, k_cache.stride()
-    if len(shape) != 4 or not k_cache.is_cuda or not v_cache.is_cuda or st[3] != 1 or v_cache.shape != shape or \
-            v_cache.stride() != st or v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache must be CUDA tensors (n_pages, n_kv, page_size, head_dim) of one dtype "
-                         "and equal strides, unit inner stride")
+    if len(shape) != 4 or k_cache.get_device() != dev or v_cache.get_device() != dev or st[3] != 1 or shape[3] == 0 or \
+            v_cache.shape != shape or v_cache.stride() != st or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must be tensors (n_pages, n_kv, page_size, head_dim) on the current CUDA "
+                         "device, of one dtype and equal strides, unit inner stride")
     dtype = _act_types().get(k_cache.dtype)
     if dtype is None or dtype == Q2_0_ACT_F32:
         raise ValueError("the cache must be float16 or bfloat16")
@@ -561,34 +584,36 @@ def q2_0_kv_append(k_cache, v_cache, table, seq, pos, k, v, rope=None, style: in
     and q (n_tokens, n_q*head_dim) float32, float16 or bfloat16, all of one dtype; rope (n_pos, rot_dim) float32, cos then
     sin of a position's angles (None: no rotation).  Returns the rotated q in the cache's dtype (None without q)."""
     import torch
-    c = _cache(k_cache, v_cache)
-    n = k.shape[0]
+    dev = torch.cuda.current_device()
+    c = _cache(k_cache, v_cache, dev)
+    n = k.shape[0] if k.dim() == 2 else -1
     xt = _act_types().get(k.dtype)
     if xt is None or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
         raise ValueError("q, k and v must be float32, float16 or bfloat16, all of one dtype")
-    tp, n_seqs, cols, ldt = _table(table)
+    tp, n_seqs, cols, ldt = _table(table, dev)
     kv = c.n_kv * c.head_dim
-    ldk, ldv = _rows(k, n, kv, "k"), _rows(v, n, kv, "v")
+    ldk, ldv = _rows(k, n, kv, "k", dev), _rows(v, n, kv, "v", dev)
     qp, ldq, n_q, op, ldo = 0, 0, 0, 0, 0
     if q is not None:
-        n_q = q.shape[1] // c.head_dim
-        if q.shape[1] != n_q * c.head_dim:
+        width = _wide(q, "q")
+        n_q = width // c.head_dim
+        if width != n_q * c.head_dim:
             raise ValueError("q must have whole heads of %d elements" % c.head_dim)
-        ldq, qp = _rows(q, n, q.shape[1], "q"), q.data_ptr()
+        ldq, qp = _rows(q, n, width, "q", dev), q.data_ptr()
         if q_out is None:
-            q_out = _empty(k_cache, (n, q.shape[1]), k_cache.dtype, stream)
+            q_out = _empty(k_cache, (n, width), k_cache.dtype, stream)
         elif q_out.dtype != k_cache.dtype:
             raise ValueError("q_out must have the cache's dtype")
-        ldo, op = _rows(q_out, n, q.shape[1], "q_out"), q_out.data_ptr()
+        ldo, op = _rows(q_out, n, width, "q_out", dev), q_out.data_ptr()
     rp, n_pos, rot = 0, 0, 0
     if rope is not None:
-        if rope.dtype != torch.float32 or not rope.is_cuda or rope.dim() != 2 or not rope.is_contiguous():
-            raise ValueError("rope must be a contiguous 2-D float32 CUDA tensor")
+        if rope.dtype != torch.float32 or rope.get_device() != dev or rope.dim() != 2 or not rope.is_contiguous():
+            raise ValueError("rope must be a contiguous 2-D float32 tensor on the current CUDA device")
         n_pos, rot = rope.shape
         rp = rope.data_ptr()
-    _check(kv_append_raw(c, tp, n_seqs, cols, ldt, _int32(seq, (n,), "seq"), _int32(pos, (n,), "pos"), n, qp, ldq, n_q,
-                         k.data_ptr(), ldk, v.data_ptr(), ldv, xt, rp, n_pos, rot, style, op, ldo, _stream(stream)),
-           "q2_0_kv_append")
+    _check(kv_append_raw(c, tp, n_seqs, cols, ldt, _dense(seq, torch.int32, (n,), "seq", dev),
+                         _dense(pos, torch.int32, (n,), "pos", dev), n, qp, ldq, n_q, k.data_ptr(), ldk, v.data_ptr(), ldv, xt,
+                         rp, n_pos, rot, style, op, ldo, _stream(stream, dev)), "q2_0_kv_append")
     return q_out
 
 
@@ -600,27 +625,26 @@ def q2_0_attn_shared(q, k_cache, v_cache, table, lens, scale: float, prefix_len:
     each sequence with the prefix and its query tokens; max_len bounds lens (default: what the table holds).  Returns
     out like q."""
     import torch
-    c = _cache(k_cache, v_cache)
-    tp, n_seqs, cols, ldt = _table(table)
-    width = q.shape[1]
+    dev = torch.cuda.current_device()
+    c = _cache(k_cache, v_cache, dev)
+    tp, n_seqs, cols, ldt = _table(table, dev)
+    width = _wide(q, "q")
     n_q = width // c.head_dim
     if q.dtype != k_cache.dtype or width != n_q * c.head_dim:
         raise ValueError("q must have the cache's dtype and whole heads of %d elements" % c.head_dim)
-    ldq = _rows(q, n_seqs * n_qt, width, "q")
+    ldq = _rows(q, n_seqs * n_qt, width, "q", dev)
     if out is None:
         out = _empty(q, (n_seqs * n_qt, width), q.dtype, stream)
     elif out.dtype != q.dtype:
         raise ValueError("out must have the cache's dtype")
-    ldo = _rows(out, n_seqs * n_qt, width, "out")
+    ldo = _rows(out, n_seqs * n_qt, width, "out", dev)
     if max_len is None:
         max_len = cols * c.page_size
     need = attn_shared_workspace_bytes(n_seqs, n_q, c.n_kv, c.head_dim, n_qt, prefix_len, max_len)
-    if workspace is None and need:
-        workspace = _empty(q, need, torch.uint8, stream, result=False)
-    wsp = workspace.data_ptr() if workspace is not None else 0
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(attn_shared_raw(c, tp, n_seqs, cols, ldt, _int32(lens, (n_seqs,), "lens"), prefix_len, max_len, q.data_ptr(),
-                           ldq, n_q, n_qt, scale, out.data_ptr(), ldo, wsp, wsb, _stream(stream)), "q2_0_attn_shared")
+    workspace, wsp, wsb = _work(workspace, need, q, stream, dev)
+    _check(attn_shared_raw(c, tp, n_seqs, cols, ldt, _dense(lens, torch.int32, (n_seqs,), "lens", dev), prefix_len, max_len,
+                           q.data_ptr(), ldq, n_q, n_qt, scale, out.data_ptr(), ldo, wsp, wsb, _stream(stream, dev)),
+           "q2_0_attn_shared")
     return out
 
 
@@ -629,20 +653,20 @@ def q2_0_moe_route(logits, n_used: int, normalise: bool = True, ids=None, weight
     (n_tokens, n_expert) float32, float16 or bfloat16, largest first and the lower index first among equals, and their
     softmax weights over the chosen (normalise) or over all experts."""
     import torch
-    n, n_expert = logits.shape
+    dev = torch.cuda.current_device()
+    n_expert = _wide(logits, "logits")
+    n = logits.shape[0]
     xt = _act_types().get(logits.dtype)
     if xt is None:
         raise ValueError("logits must be float32, float16 or bfloat16")
-    ld = _rows(logits, n, n_expert, "logits")
+    ld = _rows(logits, n, n_expert, "logits", dev)
     if ids is None:
         ids = _empty(logits, (n, n_used), torch.int32, stream)
     if weights is None:
         weights = _empty(logits, (n, n_used), torch.float32, stream)
-    if weights.dtype != torch.float32 or weights.shape != (n, n_used) or not weights.is_cuda or \
-            not weights.is_contiguous():
-        raise ValueError("weights must be a contiguous float32 CUDA tensor (n_tokens, n_used)")
     _check(moe_route_raw(logits.data_ptr(), xt, ld, n, n_expert, n_used, int(bool(normalise)),
-                         _int32(ids, (n, n_used), "ids"), weights.data_ptr(), _stream(stream)), "q2_0_moe_route")
+                         _dense(ids, torch.int32, (n, n_used), "ids", dev),
+                         _dense(weights, torch.float32, (n, n_used), "weights", dev), _stream(stream, dev)), "q2_0_moe_route")
     return ids, weights
 
 
@@ -653,26 +677,24 @@ def q2_0_moe_layer(w_gate, w_up, w_down, n_expert: int, n_ff: int, K: int, x, id
     w_gate and w_up hold n_expert (n_ff, K) Q2_0 matrices back to back, w_down n_expert (K, n_ff) ones; x (n_tokens, >=K)
     float32, float16 or bfloat16, at most MOE_LAYER_MAX_TOKENS rows; ids int32 and weights float32 (n_tokens, n_used)."""
     import torch
+    dev = torch.cuda.current_device()
     xp, n, ldx, xt = _xcols(x, K, "x")
-    n_used = ids.shape[1]
-    if weights.dtype != torch.float32 or weights.shape != (n, n_used) or not weights.is_cuda or \
-            not weights.is_contiguous():
-        raise ValueError("weights must be a contiguous float32 CUDA tensor (n_tokens, n_used)")
+    n_used = _wide(ids, "ids")
     for w, name in ((w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down")):
-        if not w.is_cuda or not w.is_contiguous() or \
+        if w.get_device() != dev or not w.is_contiguous() or \
                 w.numel() * w.element_size() < n_expert * n_ff * K // BLOCK_WEIGHTS * BLOCK_BYTES:
-            raise ValueError("%s must be a contiguous CUDA tensor that holds n_expert matrices" % name)
+            raise ValueError("%s must be a contiguous tensor on the current CUDA device that holds n_expert matrices" % name)
     if y is None:
         y = _empty(x, (n, K), torch.float32, stream)
     yp, yn, ldy = _cols(y, K, "y")
     if yn != n:
         raise ValueError("y must have n_tokens rows")
+    if x.get_device() != dev or y.get_device() != dev:
+        raise ValueError("x and y must be on the current CUDA device")
     need = moe_layer_workspace_bytes(n_ff, K, n_used, n)
-    if workspace is None and need:
-        workspace = _empty(x, need, torch.uint8, stream, result=False)
-    wsp = workspace.data_ptr() if workspace is not None else 0
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    workspace, wsp, wsb = _work(workspace, need, x, stream, dev)
     _check(moe_layer_raw(w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), n_expert, n_ff, K, xp, xt, ldx,
-                         _int32(ids, (n, n_used), "ids"), weights.data_ptr(), n_used, n, yp, ldy, wsp, wsb,
-                         _stream(stream)), "q2_0_moe_layer")
+                         _dense(ids, torch.int32, (n, n_used), "ids", dev),
+                         _dense(weights, torch.float32, (n, n_used), "weights", dev), n_used, n, yp, ldy, wsp, wsb,
+                         _stream(stream, dev)), "q2_0_moe_layer")
     return y
