@@ -407,7 +407,8 @@ typedef enum {
  * seq is outside [0, n_seqs), whose position is negative or beyond its table row, or whose
  * page is outside [0, n_pages) is not stored (its q row is still written): mark padding
  * with seq = -1.  Two tokens of one call must not share a cache row.
- * Errors: SHAPE (also n_pos beyond 2^31 - 1 and rot_dim odd, negative or > head_dim), the
+ * Errors: SHAPE (also n_pos beyond 2^31 - 1, rot_dim odd, negative or > head_dim, and a call
+ * of 2^24 workgroups, over a million tokens of 48 heads of 128), the
  * n_tokens == 0 no-op, NULL, LAYOUT, UNSUPPORTED (x_type, cache type, head_dim, style),
  * ALIGN.
  */
@@ -446,7 +447,7 @@ int q2_0_kv_append(const q2_0_kv_cache *cache, const int32_t *table, int64_t n_s
  *   workspace / ws_bytes: at least q2_0_attn_shared_workspace_bytes() bytes, 16-byte aligned
  *            (may be 0): partial results of the splits of the key axis.  Overwritten.
  * Errors: SHAPE (also n_q not a multiple of n_kv, n_qt outside [1, 16], a bad max_len or
- * prefix_len, scale), the no-op for n_seqs == 0 or n_q == 0, NULL, LAYOUT, UNSUPPORTED,
+ * prefix_len, scale, and 2^24 rows of heads to join), the no-op for n_seqs == 0 or n_q == 0, NULL, LAYOUT, UNSUPPORTED,
  * ALIGN (q, out and the cache 16-byte aligned, strides multiples of 8: LAYOUT),
  * WORKSPACE.
  */
@@ -468,7 +469,7 @@ size_t q2_0_attn_shared_workspace_bytes(int64_t n_seqs, int64_t n_q, int64_t n_k
  *   weights: f32 [n_tokens][n_used]: exp(logit - max) over its sum, the sum taken over the
  *            chosen (normalise != 0) or over all experts (0); f32 throughout.  A token whose
  *            logits are all -inf gets weights 0.
- * 1 <= n_used <= min(n_expert, 64), n_expert <= 8192: SHAPE otherwise.  Errors: SHAPE, the
+ * 1 <= n_used <= min(n_expert, 64), n_expert <= 8192, n_tokens < 2^26 - 3: SHAPE otherwise.  Errors: SHAPE, the
  * n_tokens == 0 no-op, NULL, LAYOUT (ld < n_expert), UNSUPPORTED (x_type), ALIGN.
  */
 int q2_0_moe_route(const void *logits, int x_type, int64_t ld, int64_t n_tokens, int64_t n_expert, int64_t n_used,

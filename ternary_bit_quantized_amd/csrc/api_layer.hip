@@ -12,6 +12,7 @@ constexpr int64_t kMaxInt = ((int64_t)1 << 31) - 1;
 constexpr int64_t kMaxStride = (int64_t)1 << 40;     // elements; byte offsets stay far inside 63 bits
 constexpr int64_t kMaxQueryRows = (int64_t)1 << 28;
 constexpr int64_t kMaxTokenStride = (int64_t)1 << 24;
+constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;   // workgroups of 256 threads: a launch counts threads in 32 bits
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -93,6 +94,8 @@ int q2_0_kv_append(const q2_0_kv_cache *cache, const int32_t *table, int64_t n_s
     a.n_q = (int)n_q, a.n_kv = (int)c.n_kv, a.dim = (int)c.head_dim, a.rot = (int)rot_dim;
     a.half_style = style == Q2_0_ROPE_HALF;
     a.head_blocks = 0;
+    // (a SHAPE error too, but of the variant that alignment decides)
+    if (q2_0::kv_append_groups(a, (q2_0::Act)x_type, n_tokens) > kMaxGroups) return Q2_0_ERR_SHAPE;
     return q2_0::record_hip_error(q2_0::launch_kv_append(a, (q2_0::Act)x_type, (q2_0::Act)c.type, n_tokens,
                                                          static_cast<hipStream_t>(stream)));
 }
@@ -115,6 +118,8 @@ int q2_0_attn_shared(const q2_0_kv_cache *cache, const int32_t *table, int64_t n
         (max_len > 0 && c.n_pages == 0) || !std::isfinite(scale) || !(scale > 0.f))
         return Q2_0_ERR_SHAPE;
     if (n_seqs == 0 || n_q == 0) return Q2_0_OK;
+    const q2_0::AttnPlan p = q2_0::attn_plan(n_seqs, n_q, c.n_kv, c.head_dim, n_qt, prefix_len, max_len);
+    if (p.groups > kMaxGroups) return Q2_0_ERR_SHAPE;
     if (!lens || !q || !out || (max_len > 0 && !table)) return Q2_0_ERR_NULL;
     int st = check_cache(c);
     if (st) return st;
@@ -124,7 +129,6 @@ int q2_0_attn_shared(const q2_0_kv_cache *cache, const int32_t *table, int64_t n
     if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(q, 16) || !aligned(out, 16) || !aligned(table, 4) ||
         !aligned(lens, 4))
         return Q2_0_ERR_ALIGN;
-    const q2_0::AttnPlan p = q2_0::attn_plan(n_seqs, n_q, c.n_kv, c.head_dim, n_qt, prefix_len, max_len);
     if (p.ws_bytes && (ws_bytes < p.ws_bytes || !workspace || !aligned(workspace, 16))) return Q2_0_ERR_WORKSPACE;
     q2_0::AttnShared a{};
     a.q = q, a.ldq = ldq;
@@ -145,7 +149,7 @@ int q2_0_attn_shared(const q2_0_kv_cache *cache, const int32_t *table, int64_t n
 
 int q2_0_moe_route(const void *logits, int x_type, int64_t ld, int64_t n_tokens, int64_t n_expert, int64_t n_used,
                    int normalise, int32_t *ids, float *weights, void *stream) {
-    if (!in(n_tokens, 0, kMaxInt) || !in(n_expert, 1, 8192) || !in(n_used, 1, 64) || n_used > n_expert)
+    if (!in(n_tokens, 0, 4 * kMaxGroups) || !in(n_expert, 1, 8192) || !in(n_used, 1, 64) || n_used > n_expert)
         return Q2_0_ERR_SHAPE;
     if (n_tokens == 0) return Q2_0_OK;
     if (!logits || !ids || !weights) return Q2_0_ERR_NULL;

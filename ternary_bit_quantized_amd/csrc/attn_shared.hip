@@ -911,6 +911,8 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t n_q, int64_t n_kv, int64_t dim, int64
     if (!shared || max_len > prefix_len)
         p.splits_o = own <= few ? 1 : splits(div_up(512, wgs), own / (2 * kAttnWaves));
     const int64_t n = p.splits_p + p.splits_o;
+    const int64_t rows_wgs = n_kv * (p.groups_p * p.splits_p + p.groups_o * p.splits_o * n_seqs), out_rows = rows_p * n_kv;
+    p.groups = n > 1 && out_rows > rows_wgs ? out_rows : rows_wgs;      // (attn_rows, attn_join)
     p.ws_bytes = n <= 1 ? 0 : (size_t)(n * rows_p * n_kv) * (size_t)(dim + 2) * 4;
     return p;
 }

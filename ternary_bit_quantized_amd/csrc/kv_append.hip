@@ -144,13 +144,25 @@ __global__ __launch_bounds__(256) void kv_append_any(KvAppend a) {
     dst[ib] = to_elem<CT>(y);
 }
 
-hipError_t launch_kv_append(KvAppend a, Act xt, Act ct, int64_t n_tokens, hipStream_t s) {
+static bool vector_form(const KvAppend &a, Act xt) {
     const int eb = act_bytes(xt);
     const auto fits = [&](const void *p, int64_t ld) { return (uintptr_t)p % (4 * eb) == 0 && ld % 4 == 0; };
-    const bool vec = a.rot % 8 == 0 && (a.n_q == 0 || (fits(a.q, a.ldq) && (uintptr_t)a.q_out % 16 == 0 && a.ldqo % 8 == 0)) &&
-                     fits(a.k, a.ldk) && fits(a.v, a.ldv) && (uintptr_t)a.rope % 16 == 0;
+    return a.rot % 8 == 0 && (a.n_q == 0 || (fits(a.q, a.ldq) && (uintptr_t)a.q_out % 16 == 0 && a.ldqo % 8 == 0)) &&
+           fits(a.k, a.ldk) && fits(a.v, a.ldv) && (uintptr_t)a.rope % 16 == 0;
+}
+
+static int head_blocks(const KvAppend &a, bool vec) {
     const int per = vec ? 256 / (a.dim / 8) : 256 / (a.dim / 2);    // heads per workgroup
-    a.head_blocks = (a.n_q + 2 * a.n_kv + per - 1) / per;
+    return (a.n_q + 2 * a.n_kv + per - 1) / per;
+}
+
+int64_t kv_append_groups(const KvAppend &a, Act xt, int64_t n_tokens) {
+    return n_tokens * head_blocks(a, vector_form(a, xt));
+}
+
+hipError_t launch_kv_append(KvAppend a, Act xt, Act ct, int64_t n_tokens, hipStream_t s) {
+    const bool vec = vector_form(a, xt);
+    a.head_blocks = head_blocks(a, vec);
     const dim3 grid((unsigned)(n_tokens * a.head_blocks));
     return with_act(xt, [&](auto xtag) -> hipError_t {
         using XT = decltype(xtag);

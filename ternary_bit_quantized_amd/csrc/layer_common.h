@@ -75,6 +75,7 @@ struct KvAppend {
     int n_q, n_kv, dim, rot, half_style;
     int head_blocks;      // workgroups per token
 };
+int64_t kv_append_groups(const KvAppend &a, Act xt, int64_t n_tokens);   // workgroups of the launch
 hipError_t launch_kv_append(KvAppend a, Act xt, Act ct, int64_t n_tokens, hipStream_t s);
 
 hipError_t launch_moe_choose(const void *logits, Act xt, int64_t ld, int64_t n_tokens, int n_expert, int n_used,
@@ -108,6 +109,7 @@ struct AttnPlan {
     int row_tiles;                         // 16-row tiles of a wave in the prefix part; 0: no such part
     bool joint;                            // the own part takes the prefix too
     int64_t groups_p, splits_p, groups_o, splits_o;
+    int64_t groups;                        // workgroups of the larger launch
     size_t ws_bytes;
 };
 AttnPlan attn_plan(int64_t n_seqs, int64_t n_q, int64_t n_kv, int64_t dim, int64_t n_qt, int64_t prefix_len,
