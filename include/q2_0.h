@@ -429,8 +429,8 @@ int q2_0_kv_append(const q2_0_kv_cache *cache, const int32_t *table, int64_t n_s
  *            through their sequence's row.
  *   lens   : DEVICE int32 [n_seqs]: tokens of each sequence, the prefix and its own query
  *            tokens included, so query j of sequence s sees keys i < lens[s] - n_qt + 1 + j.
- *            A sequence may end inside the prefix; it then costs the sequences that share its
- *            workgroup about twice the time for the rest of the prefix (length 0 costs nothing).
+ *            Sequences may end inside the prefix; one or many, they cost the sequences that share
+ *            their workgroup about twice the time for the rest of the prefix (length 0 costs nothing).
  *   max_len: bound on lens (host), prefix_len <= max_len <= table_len*page_size; it only
  *            sets how the work is split.
  *   scale  : finite and positive; scores are scale * (q . k).

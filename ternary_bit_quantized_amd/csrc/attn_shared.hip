@@ -303,8 +303,9 @@ struct Rows {
                         float4_t{o[t][e][i], o[t][e + 1][i], o[t][e + 2][i], o[t][e + 3][i]};
         }
     }
-    // A tile whose keys only some rows see (its keys in k): its values are multiplied once per distinct limit,
-    // lowest first, with value rows at or past it zeroed, and only the rows of that limit take the product
+    // A tile whose keys only some rows see (its keys in k): its values are multiplied once per distinct limit
+    // inside it, and once for all rows that see it whole, lowest first, with value rows at or past the limit zeroed,
+    // and only the rows of that limit take the product
     // (a zeroed P would not do: 0 * NaN reaches the others).  Nothing in the loop branches by lane: a
     // branch on lim == cur was carried into the next pass by the compiler, whose minimum over the rows
     // then missed lanes and never came to an end.
@@ -318,13 +319,14 @@ struct Rows {
         const Weights p = weights(s, t, scale2);
         sums(p, t);
         int done = max(key0, k_lo);             // (rows of limits up to here see nothing in this tile)
+        const int mylim = min(lim[t], key0 + kAttnTile);
 #pragma unroll 1
         for (int pass = 0; pass < 16; ++pass) { // (16 rows: no more limits)
-            const int cur = __builtin_amdgcn_readfirstlane(row_min(lim[t] > done ? lim[t] : 0x7fffffff));
+            const int cur = __builtin_amdgcn_readfirstlane(row_min(mylim > done ? mylim : 0x7fffffff));
             if (cur == 0x7fffffff) break;
             done = cur;
             const u32x4_t keep = keys_kept(key0, k_lo, cur, g);
-            const bool mine = lim[t] == cur;
+            const bool mine = mylim == cur;
 #pragma unroll
             for (int e = 0; e < DPL; ++e) {
                 u32x4_t va = operand(e);
