@@ -9,7 +9,7 @@
 //
 // Routing.  In moe_up_few workgroup (rows, p) serves the expert of pair p if p is the first pair that
 // chose it, for all pairs that did (or row y of the grid is an expert, where the pairs are the more
-// numerous), and finds them with one compare and ballot a wave.  (moe_down_few reads an expert's
+// numerous), and finds them with one compare and ballot.  (moe_down_few reads an expert's
 // weights once per pair: its workgroup is a token's.)  Beyond few pairs moe_prepare lists every chosen
 // expert's pairs once, the experts with the most pairs first, so that no late workgroup has two
 // passes and none is empty between: with every workgroup of moe_stream finding its own pairs (2.5 of its
@@ -32,7 +32,7 @@
 // row's 144 bytes are read as 16-byte pieces from its own start, and where fewer are left
 // the last piece ends with the row, so nothing outside the row is touched.
 //
-// What bounds it, for 128 experts of 768 x 2048 with 8 used, in a graph.  One token 14.9 us (10.6 MB of weights,
+// What bounds it, for 128 experts of 768 x 2048 with 8 used, in a graph.  One token 13.9 us (10.6 MB of weights,
 // 1.7 us of HBM time): the latency of its dependent steps, ids, weights, products, twice.  Every
 // instruction line met first costs a trip to the L2, so loops are kept rolled: unrolled
 // (12 KB of code instead of 5) the same launches took 19 us.  16 tokens 44.8 us (110 MB, 18 us): gate and up
@@ -48,8 +48,11 @@ namespace q2_0 {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
+// Pairs up to which the two launches for few pairs run.  128 experts of 768 x 2048, 8 used, in us, two launches
+// against four: 2 tokens 18.8 / 23.8, 4 tokens 26.2 / 25.7, 6 tokens 35.2 / 31.7, 8 tokens 38.8 / 35.9.
+constexpr int kFewPairs = 24;
+
 constexpr int kMlWaves = 8;
-constexpr int kMlMaxPairs = Q2_0_MOE_LAYER_MAX_TOKENS * Q2_0_MOE_LAYER_MAX_USED;
 constexpr int kMlSB = 8;                                  // blocks of a stage
 constexpr int kMlRow = kMlSB * kBlockBytes;               // LDS bytes per row (36 dwords: 16 rows on distinct banks)
 constexpr int kMlTileBytes = kMvTile * kMlRow;
@@ -233,9 +236,9 @@ __device__ __forceinline__ float silu(float v) {
     return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(t) * __builtin_fmaf(lo, ln2, 1.f));
 }
 
-// ---- routing.  grid.y counts experts (by_expert) or pairs.  The pairs that chose this workgroup's
+// ---- routing of few pairs.  grid.y counts experts (by_expert) or pairs.  The pairs that chose this workgroup's
 // expert, in order, into list; returns their number, 0 where there is nothing to do (no such
-// expert, nobody chose it, an earlier pair's workgroup serves it).  hit: 8 words of LDS.
+// expert, nobody chose it, an earlier pair's workgroup serves it).
 struct Choice {
     const int32_t *ids;
     int n_expert, n_pairs;
@@ -243,30 +246,17 @@ struct Choice {
     FastDiv used;               // a pair's token: pair / slots per token
 };
 
-__device__ __forceinline__ int chosen(const Choice &a, int &e, uint64_t *hit, uint16_t *list, int tid) {
-    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int p = a.by_expert ? 0x7fffffff : (int)blockIdx.y;
-    e = a.by_expert ? (int)blockIdx.y : a.ids[p];
+__device__ __forceinline__ int chosen(const Choice &a, int &e, uint8_t *list, int tid) {
+    static_assert(kFewPairs <= 64, "a pair a lane");
+    e = a.by_expert ? (int)blockIdx.y : a.ids[blockIdx.y];
     if (e < 0 || e >= a.n_expert) return 0;
-    int n = 0;
-    for (int b = 0; b < a.n_pairs; b += 64 * kMlWaves) {
-        const uint64_t mine = __ballot(b + tid < a.n_pairs && a.ids[min(b + tid, a.n_pairs - 1)] == e);
-        if (b) __syncthreads();
-        if (lane == 0) hit[wave] = mine;
-        __syncthreads();
-        int before = n;
-#pragma unroll 1
-        for (int w = 0; w < kMlWaves; ++w) {
-            const uint64_t m = hit[w];
-            if (n == 0 && m && b + 64 * w + (int)__ffsll((unsigned long long)m) - 1 < p && !a.by_expert) return 0;
-            const int c = (int)__popcll(m);
-            n += c;
-            if (w < wave) before += c;
-        }
-        if ((mine >> lane) & 1) list[before + (int)__popcll(mine & (((uint64_t)1 << lane) - 1))] = (uint16_t)(b + tid);
-    }
+    const int lane = tid & 63;
+    const bool mine = lane < a.n_pairs && a.ids[min(lane, a.n_pairs - 1)] == e;
+    const uint64_t hit = __ballot(mine);
+    if (hit == 0 || (!a.by_expert && (int)__ffsll((unsigned long long)hit) - 1 < (int)blockIdx.y)) return 0;
+    if (tid < 64 && mine) list[__popcll(hit & (((uint64_t)1 << lane) - 1))] = (uint8_t)lane;
     __syncthreads();
-    return n;
+    return (int)__popcll(hit);
 }
 
 // ---- gate and up of few pairs.  KS: K slices, one wave each, so that 8/KS waves own a tile of gate
@@ -294,13 +284,12 @@ __global__ __launch_bounds__(64 * kMlWaves, 4) void moe_up_few(MoeUp a) {
     __shared__ i32x4_t lds_c[XB * NC];                    // [block][column] minus the digits' sums
     __shared__ float lds_s[XB / 2][NC];                   // scales of a column's block pairs
     __shared__ float lds_red[KS > 1 ? kMlWaves * 2 * 64 : 1];
-    __shared__ uint64_t lds_hit[kMlWaves];
-    __shared__ uint16_t lds_list[kMlMaxPairs];
+    __shared__ uint8_t lds_list[kFewPairs];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15, g = lane >> 4;
     int e;
-    const int n = chosen(a.c, e, lds_hit, lds_list, tid);
+    const int n = chosen(a.c, e, lds_list, tid);
     if (n == 0) return;
 
     const int ks = wave % KS;
@@ -768,10 +757,6 @@ size_t moe_layer_ws_bytes(int64_t n_ff, int64_t K, int64_t n_used, int64_t n_tok
     // (and the experts' entries and pairs, with room for a read of 8 pairs at the last)
     return pairs * ((size_t)records((int)n_ff) + (size_t)K * 4 + sizeof(Entry) + 4) + (size_t)n_tokens * records((int)K) + 32;
 }
-
-// Pairs up to which the two launches for few pairs run.  128 experts of 768 x 2048, 8 used, in us, two launches
-// against four: 2 tokens 18.8 / 23.8, 4 tokens 26.2 / 25.7, 6 tokens 35.2 / 31.7, 8 tokens 38.8 / 35.9.
-constexpr int kFewPairs = 24;
 
 template <typename XT>
 static hipError_t launch_few(const uint8_t *wg, const uint8_t *wu, const uint8_t *wd, const Choice &c, int n_ff, int K,
