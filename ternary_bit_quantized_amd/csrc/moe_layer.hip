@@ -13,8 +13,10 @@
 // weights once per pair: its workgroup is a token's.)  Beyond few pairs moe_prepare lists every chosen
 // expert's pairs once, the experts with the most pairs first, so that no late workgroup has two
 // passes and none is empty between: with every workgroup of moe_stream finding its own pairs (2.5 of its
-// 17 us) in the experts' order 16 tokens took 54.5 us and 64 took 83.  An expert's weights are read once,
-// whatever number of tokens chose it.
+// 17 us) in the experts' order 16 tokens took 54.5 us and 64 took 83.  An expert's weights are loaded once
+// a pass, of 4 or 8 of its pairs.  Its passes follow one another in a workgroup, so few experts with many pairs each
+// leave most of the chip idle and take what one expert's passes take: 64 tokens with 8 of 8 experts 151 us, with 2 of 8
+// 66, where 2 us would read the weights.
 //
 // Products, exact but for the activations' own rounding and the f32 sums over blocks.  An
 // activation is fixed point, 31 bits with its sign, below the largest of its 128 neighbours
@@ -48,8 +50,9 @@ namespace q2_0 {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
-// Pairs up to which the two launches for few pairs run.  128 experts of 768 x 2048, 8 used, in us, two launches
-// against four: 2 tokens 18.8 / 23.8, 4 tokens 26.2 / 25.7, 6 tokens 35.2 / 31.7, 8 tokens 38.8 / 35.9.
+// Pairs up to which the two launches for few pairs run.  Experts of 768 x 2048, in us, two launches against four: 8 of
+// 128 used by 2 tokens 17.8 / 23.3, 3 tokens 23.2 / 24.5, 4 tokens 24.8 / 25.2, 6 tokens 34.0 / 30.8; 4 of 16 by 6
+// tokens 20.6 / 23.3, by 12 32.7 / 28.2; 2 of 8 by 8 tokens 17.4 / 22.2, by 12 26.0 / 27.5.
 constexpr int kFewPairs = 24;
 
 constexpr int kMlWaves = 8;
