@@ -816,9 +816,13 @@ hipError_t launch_moe_layer(const uint8_t *wg, const uint8_t *wu, const uint8_t 
                                K / kBlockWeights, hrec, nullptr};
             const MoeStream down{wd, nullptr, (int64_t)K * (n_ff / kBlockWeights) * kBlockBytes, hrec, entry, list, c.used, K,
                                  n_ff / kBlockWeights, nullptr, z};
-            // 8 pairs a pass where many experts have more than 4: 128 experts of 768 x 2048, in us with
-            // 4 and 8: 16 tokens 45.7 / 47.7, 32 tokens 58.9 / 61.1, 48 tokens 70.9 / 69.2, 64 tokens 80.1 / 74.8
-            if (2 * n_pairs <= 5 * n_expert) launch_stream<1>(up, down, (unsigned)rows, s);
+            // 8 pairs a pass where many experts have more than 4.  While all of gate-and-up's workgroups are on the chip at
+            // once, two a CU, the call waits for the few experts that take a second pass, so there already at 1.5 pairs an
+            // expert on average.  Experts of 768 x 2048, in us with 4 and 8: 8 of 128 used, 16 tokens 44.5 / 45.5, 32 tokens
+            // 57.9 / 59.1, 48 tokens 70.2 / 66.3, 64 tokens 80.7 / 72.9; 4 of 60, 16 tokens 28.6 / 29.5, 32 tokens 42.3 /
+            // 36.2, 64 tokens 52.7 / 45.6; 4 of 16, 8 tokens 31.6 / 26.5, 64 tokens 90.8 / 71.8.
+            const bool at_once = (int64_t)rows * ((n_ff + 127) / 128) <= 512;
+            if (2 * n_pairs <= (at_once ? 3 : 5) * n_expert) launch_stream<1>(up, down, (unsigned)rows, s);
             else launch_stream<2>(up, down, (unsigned)rows, s);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
