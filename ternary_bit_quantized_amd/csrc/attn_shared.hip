@@ -40,11 +40,11 @@
 //    (Key operands straight from the cache touch 64 lines an instruction, 16 rows
 //    x 4 pieces: with every wave reading them so, the L1's tag rate held 64 sequences over
 //    32768 keys at 123 us.)  Of 32 keys x 32 rows ~120
-//    VALU and 52 matrix instructions: bound by issue with two workgroups on a CU, by the latency of a
-//    tile's steps with one.
+//    VALU and 52 matrix instructions: bound by issue with two workgroups on a CU (1.6 us a tile for both, 128
+//    dims and 128 rows), by the latency of a tile's steps with one (1.1).
 //    Few rows, or a short prefix of few sequences, go the own part's way instead.
 // Workgroups that read the same prefix keys for other rows get launch numbers 8 apart: the same XCD, whose
-// L2 then serves all but one of them (four row groups over 8192 keys: 56 us spread over the XCDs, 48 so).
+// L2 then serves all but one of them (64 sequences over 8192 keys, four row groups: 55 us spread over the XCDs, 50 so).
 // Splits of the key axis join in attn_join.
 //
 // Masks.  A row sees keys below its limit.  Scores past it become -inf before the maximum, value
@@ -122,8 +122,9 @@ __device__ __forceinline__ void load_dwords(const uint8_t *p, uint32_t *v) {
 }
 
 // Waves of a workgroup: 4, so that two workgroups share a CU and are not in step (one's softmax then runs
-// beside the other's matrix instructions), and a sequence's keys split finely.  With 8, 777 keys of one
-// sequence took 10.6 instead of 9.3 us, 2000 12.9 instead of 9.5, 16 sequences of 2000 36 instead of 31.
+// beside the other's matrix instructions), and a sequence's keys split finely.  In us with 4 and with 8 (8 key heads
+// of 128): 1200 keys of one sequence 9.7 and 12.0, 2000 9.9 and 13.0, 16 sequences of 2000 30.0 and 36.0; where keys
+// are not split 8 gain a little, 777 keys of one sequence 11.5 and 10.9, of 16 14.0 and 13.0.
 constexpr int kAttnWaves = 4;
 
 // The page table through the scalar cache (uniform index).
@@ -797,10 +798,10 @@ __device__ __forceinline__ void prefix_part(const AttnShared &a, AttnLds<D, true
 }
 
 // RTP: 16-row tiles of a wave in the prefix part; 0: there is none.
-// Measured with 32 query and 8 key heads of 128, bfloat16, in a graph: one sequence of 777 keys 11.0 us (3.2 MB:
-// latency of seven dependent tiles); of 100000 75.7 us (410 MB, 5.4 TB/s); 16 sequences over 4096 shared keys
-// and up to 513 own 15.9 us with the join (36 MB); 64 over 32768 and up to 1025 77 us (270 MB, 3.5 TB/s: a
-// prefix tile takes 0.75 us where HBM would need 0.35, and the splits' results are written and read back,
+// Measured with 32 query and 8 key heads of 128, bfloat16, in a graph: one sequence of 777 keys 11.5 us (3.2 MB:
+// latency of seven dependent tiles); of 100000 76.5 us (410 MB, 5.4 TB/s); 16 sequences over 4096 shared keys
+// and up to 513 own 16.5 us with the join (36 MB); 64 over 32768 and up to 1025 87 us (270 MB, 3.1 TB/s: a
+// prefix tile takes 1.1 us where HBM would need 0.35, and the splits' results are written and read back,
 // 2 x 17 MB).
 template <typename CT, int D, int RTP, bool P16>
 __global__ __launch_bounds__(64 * kAttnWaves, D == 256 ? 1 : 2) void attn_rows(AttnShared a) {
@@ -881,18 +882,21 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t n_q, int64_t n_kv, int64_t dim, int64
     // The prefix has a part of its own unless it is of one sequence with one tile of rows, or all is
     // short and few: then a sequence's workgroups take all of its keys, prefix included (read once per
     // sequence, from the L2).  In us, so and with a part of its own: 8 sequences of 4 query tokens and 2 key
-    // heads with 1300 keys 9.3 and 10.1, with 1750 9.9 and 10.3; 8 sequences of 8 key heads with 1000 keys
-    // 9.4 and 9.5, with 1300 11.6 and 11.4, with 1600 12.7 and 11.3; 16 of them with 1200 keys 14.7 and 13.8.
+    // heads with 1300 keys 9.5 and 10.4, with 1750 10.3 and 10.9; 8 sequences of 8 key heads with 1000 keys
+    // 9.7 and 10.8, with 1300 12.5 and 11.0, with 1600 12.8 and 11.0; 16 of them with 1200 keys 15.7 and 12.4.
     const int64_t wgs = n_seqs * n_kv * p.groups_o;
     p.joint = prefix_len > 0 && ((n_seqs == 1 && rows_p <= 16) || (tiles(max_len) <= 56 && tiles(max_len) * wgs <= 2304));
     const bool shared = prefix_len > 0 && !p.joint;
     if (shared) {
         // Row tiles of a wave (2 read the tiles from LDS half as often, 1 gives twice the workgroups; 256 dims
-        // have registers for 1) and the number of splits weigh the tiles of a split, in us of a workgroup
-        // alone on its CU or beside another, against the splits' results (0.75 MB a us, written and read
-        // back).  64 sequences of 32 heads, 33 MB of results for 32 splits: over 32768 keys 16 splits took
-        // 77 us and 32 took 88, over 131072 220 and 198; 2 row tiles against 1 79 and 95 us over 32768
-        // keys, 50 and 48 over 8192.  At least four tiles each.
+        // have registers for 1) and the number of splits weigh the tiles of a split, by a workgroup alone on its CU or
+        // beside another, against the splits' results, written and read back.  The weights are not times: they were
+        // fitted, at 128 dims, and the choice they make is what was measured.  With 8 key heads of 32 query heads, in us,
+        // row tiles / splits: 64 sequences of 128 dims over 32768 keys choose 2/16, 90 (2/24 85, 2/32 97, 1/12 95), over
+        // 8192 1/8, 50 (2/12 49, 2/16 50), over 131072 2/32, 235 (2/24 246, 1/16 280); 16 over 4096 1/16, 17.3 (1/8 22,
+        // 1/32 19); of 64 dims over 32768 2/32, 53 (1/24 55), over 8192 29 (2/16 27).  256 dims, of which a CU
+        // holds one workgroup, fit less well: 64 sequences over 8192 keys 114 (1/4 102), over 32768 231 (1/12 226), 16 over
+        // 4096 30 (1/16 26).  At least four tiles each.
         constexpr double alone[2] = {0.55, 0.75}, beside[2] = {0.98, 1.15};
         const int64_t t = tiles(prefix_len), part = rows_p * n_kv * dim * 4;
         double best = 0;
@@ -906,9 +910,13 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t n_q, int64_t n_kv, int64_t dim, int64
         }
     }
     const int64_t own = shared ? tiles(max_len) - prefix_len / kAttnTile : tiles(max_len);
-    // own keys: a few tiles a wave are taken at once (777 keys of one sequence: 11.0 us so, 9.2 in 3 splits and
-    // a join, whose launch costs the caller more than that; 1200 keys: 14.4 and 9.4; 1000 keys of 16: 14.7
-    // and 16.6); beyond, enough workgroups for the chip, two tiles a wave at least
+    // own keys: a few tiles a wave are taken at once; beyond, enough workgroups for the chip, two tiles a wave at
+    // least.  A split saves the GPU's time and costs a caller that is not captured in a graph a second launch, some 4 us
+    // of its own.  With 8 key heads of 128, in us, GPU / back to back from Python: one sequence of 640 keys in one split
+    // 9.3 / 11.2, in 3 8.5 / 15.6; 777 11.5 / 11.8 and 9.6 / 15.7; 896 11.4 / 11.8 and 9.7 / 15.7; 1000 12.7 / 13.0
+    // and in 4 8.9 / 15.7; 1200 14.9 / 15.1 and 9.7 / 15.4.  At 28 tiles the one form stops costing the GPU less than
+    // the other costs the caller.  16 sequences: 1000 keys 15.8 / 15.6 in one, 16.5 / 16.6 in 4; 1280 20.4 / 20.2 and
+    // 19.5 / 19.4.
     const int64_t few = shared ? 20 : wgs >= 128 ? 40 : 28;
     if (!shared || max_len > prefix_len)
         p.splits_o = own <= few ? 1 : splits(div_up(512, wgs), own / (2 * kAttnWaves));
