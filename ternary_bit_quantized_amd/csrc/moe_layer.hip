@@ -26,7 +26,10 @@
 // instruction gives sum (q - 1) digit of a 64-weight block, in integers, for 4 columns x 4
 // digits and 16 rows.  Digits join in 32-bit integers and one f32 rounding, times d, and add up in
 // f32.  Unpacking 16 codes takes 7 instructions (one AND, three shifts and ANDs), where their
-// fp16 form (q - 1 exact in fp16, x as a hi/lo pair) takes 17.
+// fp16 form (q - 1 exact in fp16, x as a hi/lo pair) takes 17.  The fixed point costs no accuracy where a sum of
+// f32 products would keep it: an element errs by 2^-31 of its largest neighbour, a running f32 sum that holds that neighbour
+// by 2^-24 of it a step (against 64 bits the layer errs 1.7e-7, products and sums in f32 1.1e-6).  Only a row whose
+// weights skip the neighbour, by many zeros in a row, would keep more of the small ones in f32; the bound is the header's.
 //
 // Weights.  A wave takes two tiles of 16 rows at a time (gate and up of the same rows, or two
 // tiles of down), so that one read of the digits serves both; stages of 8 blocks pass through
@@ -812,6 +815,9 @@ hipError_t launch_moe_layer(const uint8_t *wg, const uint8_t *wu, const uint8_t 
             const MoePrepare prep{x, ldx, K / kBlockWeights, xrec, ids, n_expert, n_pairs, rows, entry, list, (rows + 3) / 4, tb,
                                   FastDiv::make((uint32_t)tb)};
             moe_prepare<XT><<<prep.entry_blocks + n_tokens * tb, 256, (size_t)n_expert * 4, s>>>(prep);
+            // (what follows reads experts and pairs from the workspace, so it must not run without them)
+            hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
             const MoeStream up{wg, wu, (int64_t)n_ff * (K / kBlockWeights) * kBlockBytes, xrec, entry, list, c.used, n_ff,
                                K / kBlockWeights, hrec, nullptr};
             const MoeStream down{wd, nullptr, (int64_t)K * (n_ff / kBlockWeights) * kBlockBytes, hrec, entry, list, c.used, K,
@@ -824,7 +830,7 @@ hipError_t launch_moe_layer(const uint8_t *wg, const uint8_t *wu, const uint8_t 
             const bool at_once = (int64_t)rows * ((n_ff + 127) / 128) <= 512;
             if (2 * n_pairs <= (at_once ? 3 : 5) * n_expert) launch_stream<1>(up, down, (unsigned)rows, s);
             else launch_stream<2>(up, down, (unsigned)rows, s);
-            const hipError_t e = hipGetLastError();
+            e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
         moe_sum<<<dim3((unsigned)((K + 255) / 256), (unsigned)n_tokens), 256, 0, s>>>(z, ids, weights, n_used, n_expert, K, y,
