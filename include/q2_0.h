@@ -436,7 +436,7 @@ int q2_0_kv_append(const q2_0_kv_cache *cache, const int32_t *table, int64_t n_s
  *   scale  : finite and positive; scores are scale * (q . k).
  *   out    : rows as q's, element type of the cache, at out + row*ldo.
  * The result is sum_i softmax_i(score) v_i, softmax statistics and sums in f32; a softmax weight enters the matrix
- * cores as its value in the cache's type and what that left (relative 2^-18 for BF16, 2^-24 for F16; in F16 also
+ * cores as its value in the cache's type and what that left (relative 2^-17 for BF16, 2^-23 for F16; in F16 also
  * 2^-36 of the row's largest weight, which only keys below 2^-12 of it feel), in its sum as in the values', and the
  * result is rounded once.  Scores beyond 2^20 either way are past what f32 exponents
  * resolve; their weights may come out as NaN.  A query that sees no key (or only

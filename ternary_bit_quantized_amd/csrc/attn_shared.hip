@@ -66,6 +66,7 @@ template <>
 struct Mma<_Float16> {
     static constexpr uint32_t kOnes = 0x3c003c00u;
     static constexpr float kHead = 4.f, kBias = 11.f;     // of the weights, as powers of two; together at most 15
+    static constexpr float kOver = 1.f + 0x1p-11f;
     static __device__ __forceinline__ float4_t mul(u32x4_t a, u32x4_t b, float4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c,
                                                       0, 0, 0);
@@ -75,6 +76,7 @@ template <>
 struct Mma<bf16_t> {
     static constexpr uint32_t kOnes = 0x3f803f80u;
     static constexpr float kHead = 8.f, kBias = 0.f;
+    static constexpr float kOver = 1.f + 0x1p-8f;
     static __device__ __forceinline__ float4_t mul(u32x4_t a, u32x4_t b, float4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8_t, a), __builtin_bit_cast(bf8_t, b), c, 0,
                                                        0, 0);
@@ -134,7 +136,8 @@ __device__ __forceinline__ int table_at(const int32_t *t, int i) {
 }
 
 // Softmax weights of 8 keys for a row, as the second product takes them: the weight in the cache's type and what
-// that rounding left, again in that type.
+// that rounding left, again in that type.  All weights are carried kOver times as large, in the second operand, so that
+// this one is above 0 where the first is: with both signs, or 0, an infinite value would come out as NaN.
 struct Weights {
     u32x4_t hi, lo;
 };
@@ -248,7 +251,7 @@ struct Rows {
             const uint32_t hi = pack2<CT>(w[0], w[1]);
             const float2_t r = unpack2<CT>(hi);
             p.hi[i] = hi;
-            p.lo[i] = pack2<CT>(w[0] - r.x, w[1] - r.y);
+            p.lo[i] = pack2<CT>(__builtin_fmaf(w[0], Mma<CT>::kOver, -r.x), __builtin_fmaf(w[1], Mma<CT>::kOver, -r.y));
         }
         return p;
     }
