@@ -441,7 +441,8 @@ int q2_0_kv_append(const q2_0_kv_cache *cache, const int32_t *table, int64_t n_s
  * result is rounded once.  Scores beyond 2^20 either way are past what f32 exponents
  * resolve; their weights may come out as NaN.  A query that sees no key (or only
  * scores of -inf) gives zeros.  Keys and values that a query does not see are never part
- * of its result, whatever they hold (NaN and inf included).  lens[s] outside
+ * of its result, whatever they hold (NaN and inf included); an infinite value that it does see makes
+ * its element infinite (or NaN, where the weight is below 2^-24 of the row's largest).  lens[s] outside
  * [0, max_len], or a page outside [0, n_pages) among the keys a query sees, gives NaN
  * and reads nothing out of bounds.  Results are deterministic run to run.
  *   workspace / ws_bytes: at least q2_0_attn_shared_workspace_bytes() bytes, 16-byte aligned
