@@ -509,6 +509,175 @@ int q2_0_moe_layer(const void *w_gate, const void *w_up, const void *w_down, int
 /* Workspace bytes q2_0_moe_layer needs (0 for invalid sizes). */
 size_t q2_0_moe_layer_workspace_bytes(int64_t n_ff, int64_t K, int64_t n_used, int64_t n_tokens);
 
+/*
+ * ---- Between two decoder steps: expert choice in groups, drafted tokens, pages of the cache.
+ */
+
+/* How a router's logits become scores (see q2_0_moe_route_groups). */
+typedef enum {
+    Q2_0_SCORE_SOFTMAX = 0,   /* exp(logit - max) over the sum of a token's */
+    Q2_0_SCORE_SIGMOID = 1    /* 1 / (1 + exp(-logit)), each by itself */
+} q2_0_score;
+
+/*
+ * moe_route_groups: choose experts by score plus bias, inside the best groups of experts.
+ *   logits : n_tokens rows of n_expert values of element type x_type at logits + t*ld.
+ *   score  : a q2_0_score.
+ *   bias   : DEVICE f32 [n_expert], added to the scores for the choice alone (balance between
+ *            experts), or NULL.  A bias of -inf masks its expert: it is chosen only where nothing else
+ *            is left, with weight 0.
+ *   n_group: the experts stand in n_group groups of n_expert/n_group, one after the other; a group's value is
+ *            the sum of its group_top (1 or 2) largest biased scores, and experts come from the
+ *            n_group_used groups of the largest values.  n_group = n_group_used = 1: no groups.
+ *   ids    : int32 [n_tokens][n_used]: the n_used largest biased scores of those groups, largest first.
+ *            Among equals the lower index is first, of groups too; NaN comes after -inf.
+ *   weights: f32 [n_tokens][n_used]: scale * score (without the bias) of the chosen, divided by their
+ *            sum with normalise != 0 (a sum of 0 gives weights 0).
+ * Scores, bias sums and group values are worked out and compared in 64 bits; a weight is rounded to f32 once.
+ * A softmax over -inf alone has scores 0; a NaN logit, or +inf under softmax, makes its token's scores (under
+ * sigmoid its own score) NaN.  ids are experts of the row whatever it holds.
+ * n_expert <= 1024, n_used <= 64, n_group <= 64, scale finite: SHAPE otherwise, as for groups that do not divide the
+ * experts or hold fewer than n_used or group_top.  n_tokens < 2^26 - 3.  Errors: SHAPE, the n_tokens == 0
+ * no-op, NULL, LAYOUT (ld < n_expert), UNSUPPORTED (x_type, score), ALIGN.
+ */
+int q2_0_moe_route_groups(const void *logits, int x_type, int64_t ld, int64_t n_tokens, int64_t n_expert, int64_t n_used,
+                          int score, const float *bias, int64_t n_group, int64_t n_group_used, int64_t group_top,
+                          int normalise, float scale, int32_t *ids, float *weights, void *stream);
+
+/* What the rows given to q2_0_draft_verify hold. */
+typedef enum {
+    Q2_0_DRAFT_LOGITS = 0,   /* logits: probabilities are their softmax over the temperature; -inf masks a token */
+    Q2_0_DRAFT_PROBS = 1     /* probabilities, taken as they are (values below 0 count as 0 where a token is drawn) */
+} q2_0_draft_form;
+
+/* Largest number of drafted tokens of a sequence in one call. */
+#define Q2_0_DRAFT_MAX 15
+
+/*
+ * draft_verify: how many of a sequence's drafted tokens the target model takes, and the token that follows them.
+ *   target : row s*(max_draft+1) + j of n_vocab elements of x_type at target + row*ld_target: the target model's
+ *            values at drafted place j of sequence s (the last: after all of them).
+ *   draft  : row s*max_draft + j at draft + row*ld_draft: the values the token of place j was drawn from.
+ *            NULL: the drafts were not drawn but found (in the text so far): probability 1 of the drafted token.
+ *   form   : a q2_0_draft_form, for both.
+ *   temperature : DEVICE f32 [n_seqs], for both models, or NULL (1).  0: the largest logit takes all (the
+ *            lowest index among equals).  Logits only (UNSUPPORTED with probabilities).
+ *   tokens : DEVICE int32 [n_seqs][max_draft].  One outside [0, n_vocab) is not taken.
+ *   n_draft: DEVICE int32 [n_seqs]: drafted tokens of the sequence, 0 .. max_draft.  Any other value leaves the
+ *            sequence out (mark padding with -1): n_accepted 0, its out all -1, nothing of its rows is read.
+ *   u      : DEVICE f32 [n_seqs][max_draft+1], uniform numbers of [0, 1): [s][j] decides on place j,
+ *            [s][max_draft] draws the token that follows.
+ *   out    : int32 [n_seqs][max_draft+1]: the tokens taken, the one that follows, then -1.
+ *   n_accepted : int32 [n_seqs]: tokens taken.
+ * Place j's token t is taken where u*q(t) < p(t), up to the first that is not.  There the token that follows is drawn
+ * from max(p - q, 0) (from p where that leaves less than 2^-32), after the last place from p: the lowest token at which
+ * the running sum passes u times the whole.  With max_draft = 0 the call draws a token from each row.
+ * A row that is needed and holds NaN or +inf, or nothing but -inf (probabilities: nothing above 0), or has a
+ * temperature that is negative or NaN, takes no token and gives -1.
+ * Exponentials and sums are in 64 bits, in a fixed order.  Deterministic run to run.
+ *   workspace / ws_bytes: at least q2_0_draft_verify_workspace_bytes() bytes, 16-byte aligned.  Overwritten.
+ * n_vocab <= 2^24, n_seqs <= 2^20, max_draft <= Q2_0_DRAFT_MAX.  Errors: SHAPE (also launches past 2^24
+ * workgroups), the n_seqs == 0 no-op, NULL, LAYOUT (ld below n_vocab), UNSUPPORTED (x_type, form), ALIGN, WORKSPACE.
+ */
+int q2_0_draft_verify(const void *target, int64_t ld_target, const void *draft, int64_t ld_draft, int x_type, int form,
+                      int64_t n_vocab, const float *temperature, const int32_t *tokens, const int32_t *n_draft, const float *u,
+                      int64_t n_seqs, int64_t max_draft, int32_t *out, int32_t *n_accepted, void *workspace, size_t ws_bytes,
+                      void *stream);
+
+/* Workspace bytes q2_0_draft_verify needs (0 for invalid sizes); has_draft: draft is not NULL. */
+size_t q2_0_draft_verify_workspace_bytes(int64_t n_seqs, int64_t max_draft, int64_t n_vocab, int x_type, int form,
+                                         int has_draft);
+
+/*
+ * The pages of a cache (q2_0_kv_cache, above), as the calls below keep them on the device:
+ *   ref    : int32 [n_pages]: how many table rows (or other owners, by the caller's own counting) hold a page.
+ *   free   : one bit a page, bit i % 32 of word i / 32: the page may be taken.  Bits past n_pages are ignored.
+ * A new pool has ref 0 and every bit set.  A page with ref 0 and its bit clear is the caller's.
+ * These calls change tables, lengths, counts and bits in place: those of one pool belong on one stream.  Results
+ * do not depend on timing.  n_pages and table_len <= 2^30, page_size and n_kv so that a page's 16-byte
+ * vectors stay below 2^31, launches below 2^24 workgroups: SHAPE otherwise.
+ */
+typedef struct {
+    int32_t *ref;
+    uint32_t *free;
+    int64_t n_pages;
+} q2_0_kv_pages;
+
+/*
+ * kv_copy: pages src[i] of `from` to pages dst[i] of `to`, keys and values (the same cache, or one of the same
+ * page_size, n_kv, head_dim and type with strides of its own: a sequence that is swapped out, a page that is
+ * to be written).  A pair with a page outside its pool is left out.  A page must not stand twice in dst, and in one
+ * cache not in src and dst both.
+ *   src, dst : DEVICE int32 [n], 4-byte aligned.
+ * Errors: NULL (to, from), SHAPE (also caches of different pages), the n == 0 no-op, NULL, LAYOUT, UNSUPPORTED, ALIGN.
+ */
+int q2_0_kv_copy(const q2_0_kv_cache *to, const q2_0_kv_cache *from, const int32_t *src, const int32_t *dst, int64_t n,
+                 void *stream);
+
+/*
+ * kv_fork: sequence dst[i] becomes a sequence of the same tokens as src[i], in the same pages (beams, several
+ * answers to one prompt): its table row up to the length, its length, and one holder more for each page.
+ * q2_0_kv_resize gives a sequence that grows from inside a shared page a copy of it.
+ *   lens   : DEVICE int32 [n_seqs].  dst[i] must be empty (length 0).
+ *   src, dst : DEVICE int32 [n].  A pair is left out (lens[dst[i]] tells) where either is outside [0, n_seqs) or both are
+ *            the same, where dst[i] is not empty, where lens[src[i]] is outside [0, table_len*page_size], and where
+ *            an earlier pair has the same dst.  Lengths are those before the call: a dst of one pair is empty as
+ *            src of another.
+ *   workspace / ws_bytes: at least q2_0_kv_fork_workspace_bytes() bytes, 16-byte aligned.  Overwritten.
+ * Errors: SHAPE, the no-op for n == 0 or n_seqs == 0, NULL, LAYOUT, ALIGN, WORKSPACE.
+ */
+int q2_0_kv_fork(int32_t *ref, int64_t n_pages, int32_t *table, int64_t n_seqs, int64_t table_len, int64_t ld_table,
+                 int64_t page_size, int32_t *lens, const int32_t *src, const int32_t *dst, int64_t n, void *workspace,
+                 size_t ws_bytes, void *stream);
+
+/* Workspace bytes q2_0_kv_fork needs (0 for invalid sizes). */
+size_t q2_0_kv_fork_workspace_bytes(int64_t n);
+
+/*
+ * kv_resize: every sequence gets the length new_lens[s].
+ *   A shorter one leaves the pages past its new length: its table entries become -1, the pages' counts go down, and
+ *   those at 0 are free (all of a sequence's with new_lens 0).
+ *   A longer one takes free pages for the rows up to its new length.  Where it grows from inside a page that others hold
+ *   too, it takes a page more, gets that page's rows so far, and leaves the shared one; where all holders of a
+ *   page do so in one call, the sequence with the lowest index keeps it.  So the rows between the old and the new length
+ *   are the sequence's own, to be written by q2_0_kv_append.
+ *   Pages left in the call are free for it.  Pages are taken in the order of their numbers, the lowest for
+ *   the first sequence, a copy before new rows.
+ *   lens   : DEVICE int32 [n_seqs], the lengths so far; set to new_lens.  A sequence with either length outside
+ *            [0, table_len*page_size] stays as it is (new_lens -1: leave it).
+ *   missing: DEVICE int32 [1]: 0, or how many pages more the growing sequences need than there are: then none of
+ *            them grows (their rows, lengths and pages stay), while the others have become shorter.
+ *   workspace / ws_bytes: at least q2_0_kv_resize_workspace_bytes() bytes, 16-byte aligned.  Overwritten.
+ * Table entries outside [0, n_pages) are no pages: nothing is counted or copied for them.  pages->n_pages is the cache's;
+ * n_seqs <= 8192.  Errors: NULL (cache, pages), SHAPE, the n_seqs == 0 no-op, NULL, LAYOUT, UNSUPPORTED, ALIGN, WORKSPACE.
+ */
+int q2_0_kv_resize(const q2_0_kv_cache *cache, const q2_0_kv_pages *pages, int32_t *table, int64_t n_seqs, int64_t table_len,
+                   int64_t ld_table, int32_t *lens, const int32_t *new_lens, int32_t *missing, void *workspace,
+                   size_t ws_bytes, void *stream);
+
+/* Workspace bytes q2_0_kv_resize needs (0 for invalid sizes). */
+size_t q2_0_kv_resize_workspace_bytes(int64_t n_seqs, int64_t n_pages);
+
+/*
+ * kv_compact: the pages of `from` that are not free become the first pages of `to`, in the order of their numbers (a
+ * pool that shrinks, or grows, while sequences live): their keys and values, their counts and
+ * bits, and to_table, the rows of `table` with the new numbers (entries past a sequence's length, of a length
+ * outside [0, table_len*page_size], and of free pages or none are -1).  Lengths stay.
+ *   to     : another cache of the same page_size, n_kv, head_dim and type, with strides of its own; to_pages and
+ *            to_table [n_seqs][ld_to_table] its own too (equal pointers are LAYOUT).  Free pages of `to` keep their rows.
+ *   n_used : DEVICE int32 [1]: pages that are not free.  Where that is more than to_pages->n_pages, nothing else
+ *            is written.
+ *   workspace / ws_bytes: at least q2_0_kv_compact_workspace_bytes(from_pages->n_pages) bytes, 16-byte aligned.
+ * Errors: NULL (caches, pages), SHAPE, NULL, LAYOUT, UNSUPPORTED, ALIGN, WORKSPACE.
+ */
+int q2_0_kv_compact(const q2_0_kv_cache *to, const q2_0_kv_pages *to_pages, const q2_0_kv_cache *from,
+                    const q2_0_kv_pages *from_pages, const int32_t *table, int64_t n_seqs, int64_t table_len, int64_t ld_table,
+                    const int32_t *lens, int32_t *to_table, int64_t ld_to_table, int32_t *n_used, void *workspace,
+                    size_t ws_bytes, void *stream);
+
+/* Workspace bytes q2_0_kv_compact needs (0 for invalid sizes). */
+size_t q2_0_kv_compact_workspace_bytes(int64_t n_pages);
+
 /* A static, human-readable name for a status code. */
 const char *q2_0_status_string(int status);
 

@@ -1,0 +1,478 @@
+// Verification of drafted tokens, and the token that follows the accepted ones.
+//
+// With p = softmax(target / T) and q = softmax(draft / T) of a drafted place, its token t is taken where
+// u q(t) < p(t); at the first that is not, the token comes from max(p - q, 0), and after the last from p
+// itself, both by the inverse of the running sum at a given number.  Every output is a whole number
+// that hangs on a comparison of sums over the vocabulary, so exponentials and sums are in 64 bits: in 32
+// a running sum over 10^5 tokens is off by some 10^-7 of the whole, which moves about one choice in a
+// thousand to the token beside it.
+//
+//   draft_stats  one pass over every row that may be needed: maximum and sum of exponentials of each chunk
+//                (a running maximum in registers, rescaled where a pass raises it)
+//   draft_sums   each workgroup joins its sequence's chunks, decides how many drafts are taken, and sums
+//                max(p - q, 0) of the deciding row over tiles of 1024 tokens
+//   draft_pick   one workgroup a sequence: the tile, then the token, at which the running sum passes the number
+//
+// Given probabilities need no statistics.  Fixed order of all sums: results are the same in every run.
+#include "serve_common.h"
+
+namespace q2_0 {
+
+constexpr int kMaxRows = 2 * Q2_0_DRAFT_MAX + 1;
+constexpr int kTile = 1024;
+constexpr int kPassVecs = 1024;       // 16-byte vectors of a workgroup's pass: 4 a thread
+
+// 2^y for y <= 0 (0 below -1100 and for NaN): 2^n 2^r with n = rint(y) from the low bits of y + 1.5 2^52 and
+// r in [-1/2, 1/2] by the polynomial of degree 9 that meets 2^r at the Chebyshev points (relative error 2e-14).
+__device__ __forceinline__ double exp2_64(double y) {
+    y = fmax(y, -1100.0);
+    const double big = 6755399441055744.0;
+    const double t = y + big;
+    const double r = y - (t - big);
+    double e = 1.020590550210069e-07;
+    e = fma(e, r, 1.3259645241948732e-06);
+    e = fma(e, r, 1.5252672924257465e-05);
+    e = fma(e, r, 0.0001540343375126647);
+    e = fma(e, r, 0.0013333558200796013);
+    e = fma(e, r, 0.00961812919393429);
+    e = fma(e, r, 0.05550410866465166);
+    e = fma(e, r, 0.2402265069564034);
+    e = fma(e, r, 0.6931471805599462);
+    e = fma(e, r, 1.0000000000000135);
+    return __builtin_amdgcn_ldexp(e, (int)(uint32_t)__builtin_bit_cast(uint64_t, t));
+}
+
+__device__ __forceinline__ double nan64() { return __builtin_nan(""); }
+
+// log2(e) / temperature; NaN for a temperature that is not positive
+__device__ __forceinline__ double scale_of(const DraftVerify &a, int s) {
+    if (!a.temperature) return 1.4426950408889634074;
+    const float t = a.temperature[s];
+    return t > 0.f ? 1.4426950408889634074 / (double)t : nan64();
+}
+
+__device__ __forceinline__ bool greedy_of(const DraftVerify &a, int s) { return a.temperature && a.temperature[s] == 0.f; }
+
+template <typename XT>
+struct Vec {                          // 16 bytes of a row
+    static constexpr int n = 16 / sizeof(XT);
+    float x[n];
+};
+
+__device__ __forceinline__ void unpack(u32x4_t v, Vec<float> &o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t b = v[i];      // (a cast of the element itself would read the vector's first)
+        o.x[i] = __builtin_bit_cast(float, b);
+    }
+}
+__device__ __forceinline__ void unpack(u32x4_t v, Vec<_Float16> &o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t b = v[i];
+        const half2_t h = __builtin_bit_cast(half2_t, b);
+        o.x[2 * i] = (float)h.x, o.x[2 * i + 1] = (float)h.y;
+    }
+}
+__device__ __forceinline__ void unpack(u32x4_t v, Vec<bf16_t> &o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        o.x[2 * i] = __builtin_bit_cast(float, v[i] << 16);
+        o.x[2 * i + 1] = __builtin_bit_cast(float, v[i] & 0xffff0000u);
+    }
+}
+
+// Vector w of a row whose first element is `shift` elements past a 16-byte boundary; what is outside
+// the row (or at w >= end) is -inf and not read.
+template <typename XT>
+__device__ __forceinline__ Vec<XT> load_vec(const XT *row, int shift, int n_vocab, int w, int end) {
+    constexpr int VE = Vec<XT>::n;
+    Vec<XT> o;
+    const int e = w * VE - shift;
+    if (w < end && e >= 0 && e + VE <= n_vocab) {
+        unpack(*reinterpret_cast<const u32x4_t *>(row + e), o);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+            o.x[i] = w < end && e + i >= 0 && e + i < n_vocab ? act_to_f32(row[e + i]) : -__builtin_inff();
+    }
+    return o;
+}
+
+template <typename XT>
+__global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
+    const int b = (int)(blockIdx.x / (unsigned)p.chunks), c = (int)(blockIdx.x % (unsigned)p.chunks);
+    const int per = a.max_draft + 1, n_target = a.n_seqs * per;
+    const bool is_draft = b >= n_target;
+    const int s = is_draft ? (b - n_target) / a.max_draft : b / per;
+    const int j = is_draft ? (b - n_target) % a.max_draft : b % per;
+    const int nd = a.n_draft[s];
+    if (nd < 0 || nd > a.max_draft || j >= nd + (is_draft ? 0 : 1)) return;
+    const bool greedy = greedy_of(a, s);
+    if (greedy && is_draft) return;
+    const XT *row = is_draft ? static_cast<const XT *>(a.draft) + (int64_t)(b - n_target) * a.ld_draft
+                             : static_cast<const XT *>(a.target) + (int64_t)b * a.ld_target;
+    constexpr int VE = Vec<XT>::n;
+    const int shift = (int)(((uintptr_t)row & 15) / sizeof(XT));
+    const int nv = (a.n_vocab + shift + VE - 1) / VE;
+    const int v0 = c * p.chunk_vecs, v1 = nv < v0 + p.chunk_vecs ? nv : v0 + p.chunk_vecs;
+    const double k = scale_of(a, s);
+    float m = -__builtin_inff();
+    double z = 0.0;
+    int arg = 0x7fffffff;
+    bool bad = false;
+    for (int v = v0; v < v1; v += kPassVecs) {
+        Vec<XT> x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = load_vec(row, shift, a.n_vocab, v + i * 256 + (int)threadIdx.x, v1);
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                top = fmaxf(top, x[i].x[e]);
+                bad |= x[i].x[e] != x[i].x[e];
+            }
+        if (greedy) {
+            if (top > m) {
+                m = top;
+#pragma unroll
+                for (int i = 3; i >= 0; --i)
+#pragma unroll
+                    for (int e = VE - 1; e >= 0; --e)
+                        if (x[i].x[e] == top) arg = (v + i * 256 + (int)threadIdx.x) * VE - shift + e;
+            }
+        } else {
+            if (top > m) {
+                z *= exp2_64(((double)m - (double)top) * k);
+                m = top;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < VE; ++e) z += exp2_64(((double)x[i].x[e] - (double)m) * k);
+        }
+    }
+    __shared__ float wm[4];
+    __shared__ double wz[4];
+    __shared__ int warg[4], wbad[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    float top = m;
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    if (lane == 0) wm[wave] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(wm[0], wm[1]), fmaxf(wm[2], wm[3]));
+    if (greedy) {
+        int at = m == top ? arg : 0x7fffffff;
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) {
+            const int o = __shfl_xor(at, off);
+            at = o < at ? o : at;
+        }
+        if (lane == 0) warg[wave] = at;
+    } else {
+        z *= exp2_64(((double)m - (double)top) * k);
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) z += __shfl_xor(z, off);
+    }
+    const bool any = __ballot(bad) != 0;
+    if (lane == 0) wz[wave] = z, wbad[wave] = any;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const bool none = wbad[0] | wbad[1] | wbad[2] | wbad[3] || top == __builtin_inff();
+        reinterpret_cast<double *>(a.ws + p.off_z)[blockIdx.x] =
+            none ? nan64() : greedy ? 1.0 : ((wz[0] + wz[1]) + wz[2]) + wz[3];
+        reinterpret_cast<float *>(a.ws + p.off_max)[blockIdx.x] = top;
+        if (greedy) {
+            int at = 0x7fffffff;
+            for (int w = 0; w < 4; ++w) at = warg[w] < at ? warg[w] : at;
+            reinterpret_cast<int *>(a.ws + p.off_arg)[blockIdx.x] = at;
+        }
+    }
+}
+
+// What decides a sequence's next token.
+struct Pick {
+    double k, m_p, inv_p, m_q, inv_q;     // p(x) = 2^(k (x - m)) inv
+    int64_t row_p, row_q;                 // rows of target and draft
+    int taken;                            // drafts taken; < 0: the sequence is left out
+    int kind;                             // kFixed: `token`; else what is taken from p
+    int token;                            // the next token (kFixed), the token to leave out (kOneHot)
+};
+enum { kFixed = 0, kPlain = 1, kOneHot = 2, kMinus = 3 };
+
+template <bool PROBS>
+__device__ __forceinline__ double prob(float x, double k, double m, double inv) {
+    return PROBS ? (double)x : exp2_64(((double)x - m) * k) * inv;
+}
+
+// All threads of the workgroup; the result is in `pick` after a barrier.
+template <typename XT, bool PROBS>
+__device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pick) {
+    __shared__ double most[kMaxRows], inv[kMaxRows];
+    __shared__ int arg[kMaxRows];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int nd = a.n_draft[s], per = a.max_draft + 1;
+    if (nd < 0 || nd > a.max_draft) {
+        if (threadIdx.x == 0) pick.taken = -1, pick.kind = kFixed, pick.token = -1;
+        return;
+    }
+    const bool greedy = !PROBS && greedy_of(a, s);
+    const double k = PROBS ? 0.0 : scale_of(a, s);
+    if (!PROBS) {
+        const int rows = nd + 1 + (a.draft && !greedy ? nd : 0);
+        for (int r = wave; r < rows; r += 4) {
+            const int64_t b = r <= nd ? (int64_t)s * per + r : (int64_t)a.n_seqs * per + (int64_t)s * a.max_draft + (r - nd - 1);
+            const double *z = reinterpret_cast<const double *>(a.ws + p.off_z) + b * p.chunks;
+            const float *m = reinterpret_cast<const float *>(a.ws + p.off_max) + b * p.chunks;
+            const int *at = reinterpret_cast<const int *>(a.ws + p.off_arg) + b * p.chunks;
+            float top = -__builtin_inff();
+            for (int c = lane; c < p.chunks; c += 64) top = fmaxf(top, m[c]);
+#pragma unroll
+            for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+            double sum = 0.0;
+            int best = 0x7fffffff;
+            for (int c = lane; c < p.chunks; c += 64) {
+                // (a chunk of NaN: its sum is NaN and stays so)
+                sum += greedy ? z[c] : z[c] * exp2_64(((double)m[c] - (double)top) * k);
+                if (greedy && m[c] == top) best = at[c] < best ? at[c] : best;
+            }
+#pragma unroll
+            for (int off = 32; off >= 1; off >>= 1) {
+                sum += __shfl_xor(sum, off);
+                const int o = __shfl_xor(best, off);
+                best = o < best ? o : best;
+            }
+            if (lane == 0) {
+                most[r] = top;
+                inv[r] = sum > 0.0 && sum < __builtin_inf() ? 1.0 / sum : nan64();
+                arg[r] = sum == sum && top > -__builtin_inff() ? best : -1;
+            }
+        }
+        __syncthreads();
+    }
+    if (wave != 0) return;
+    bool yes = false;
+    int tok = -1;
+    const int64_t row_p = (int64_t)s * per + lane, row_q = (int64_t)s * a.max_draft + lane;
+    if (lane < nd) {
+        tok = a.tokens[row_q];
+        if (tok >= 0 && tok < a.n_vocab) {
+            if (greedy) {
+                yes = arg[lane] == tok;
+            } else {
+                const double pt = prob<PROBS>(act_to_f32(static_cast<const XT *>(a.target)[row_p * a.ld_target + tok]), k,
+                                              PROBS ? 0.0 : most[lane], PROBS ? 0.0 : inv[lane]);
+                double qt = 1.0;
+                if (a.draft)
+                    qt = prob<PROBS>(act_to_f32(static_cast<const XT *>(a.draft)[row_q * a.ld_draft + tok]), k,
+                                     PROBS ? 0.0 : most[nd + 1 + lane], PROBS ? 0.0 : inv[nd + 1 + lane]);
+                yes = (double)a.u[row_p] * qt < pt;
+            }
+        }
+    }
+    const uint64_t no = __ballot(!yes);                  // (lanes from nd on: not taken)
+    const int j = (int)__ffsll((unsigned long long)no) - 1;
+    const int t = __builtin_amdgcn_readlane(tok, j);
+    if (lane == 0) {
+        pick.taken = j;
+        pick.k = k;
+        pick.row_p = (int64_t)s * per + j;
+        pick.row_q = (int64_t)s * a.max_draft + j;
+        if (!PROBS) {
+            pick.m_p = most[j], pick.inv_p = inv[j];
+            if (j < nd && a.draft && !greedy) pick.m_q = most[nd + 1 + j], pick.inv_q = inv[nd + 1 + j];
+        }
+        if (greedy) pick.kind = kFixed, pick.token = arg[j];
+        else if (j == nd) pick.kind = kPlain, pick.token = -1;
+        else if (!a.draft) pick.kind = kOneHot, pick.token = t;
+        else pick.kind = kMinus, pick.token = -1;
+    }
+}
+
+// What is left for token e: not below zero, NaN where either is.
+template <typename XT, bool PROBS>
+__device__ __forceinline__ double weight(const DraftVerify &a, const Pick &pick, int kind, int e) {
+    if (e >= a.n_vocab) return 0.0;
+    double w = prob<PROBS>(act_to_f32(static_cast<const XT *>(a.target)[pick.row_p * a.ld_target + e]), pick.k, pick.m_p,
+                           pick.inv_p);
+    if (kind == kMinus)
+        w -= prob<PROBS>(act_to_f32(static_cast<const XT *>(a.draft)[pick.row_q * a.ld_draft + e]), pick.k, pick.m_q,
+                         pick.inv_q);
+    if (kind == kOneHot && e == pick.token) w = 0.0;
+    return w <= 0.0 ? 0.0 : w;
+}
+
+// Lane l holds tokens tile * 1024 + 64 i + l.
+template <typename XT, bool PROBS>
+__device__ __forceinline__ double tile_sum(const DraftVerify &a, const Pick &pick, int kind, int tile) {
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kTile / 64; ++i)
+        sum += weight<XT, PROBS>(a, pick, kind, tile * kTile + 64 * i + (int)(threadIdx.x & 63));
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
+    return sum;
+}
+
+template <typename XT, bool PROBS>
+__global__ __launch_bounds__(256) void draft_sums(DraftVerify a, DraftPlan p) {
+    const int per = (p.tiles + 3) / 4;                   // workgroups of a sequence
+    const int s = (int)(blockIdx.x / (unsigned)per), g = (int)(blockIdx.x % (unsigned)per);
+    __shared__ Pick pick;
+    decide<XT, PROBS>(a, p, s, pick);
+    __syncthreads();
+    if (g == 0 && threadIdx.x == 0) reinterpret_cast<Pick *>(a.ws + p.off_pick)[s] = pick;
+    const int tile = g * 4 + (int)(threadIdx.x >> 6);
+    if (pick.kind == kFixed || tile >= p.tiles) return;
+    const double sum = tile_sum<XT, PROBS>(a, pick, pick.kind, tile);
+    if ((threadIdx.x & 63) == 0) reinterpret_cast<double *>(a.ws + p.off_tiles)[(int64_t)s * p.tiles + tile] = sum;
+}
+
+template <typename XT, bool PROBS>
+__global__ __launch_bounds__(256) void draft_pick(DraftVerify a, DraftPlan p) {
+    const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    __shared__ Pick pick;
+    __shared__ double inc[256], before;
+    __shared__ int first, last, found, result;
+    double *tiles = reinterpret_cast<double *>(a.ws + p.off_tiles) + (int64_t)s * p.tiles;
+    if (tid == 0) {
+        pick = reinterpret_cast<const Pick *>(a.ws + p.off_pick)[s];
+        result = pick.token;
+    }
+    __syncthreads();
+    int kind = pick.kind;
+    const int each = (p.tiles + 255) / 256, t0 = tid * each, t1 = t0 + each < p.tiles ? t0 + each : p.tiles;
+    for (int turn = 0; kind != kFixed && turn < 2; ++turn) {
+        double sum = 0.0;
+        for (int t = t0; t < t1; ++t) sum += tiles[t];
+        // running sums over the threads
+        double run = sum;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const double o = __shfl_up(run, off);
+            if (lane >= off) run += o;
+        }
+        inc[tid] = run;
+        if (tid == 0) first = 256, last = -1;
+        __syncthreads();
+        double base = 0.0;
+        for (int w = 0; w < wave; ++w) base += inc[64 * w + 63];
+        const double total = ((inc[63] + inc[127]) + inc[191]) + inc[255];
+        run += base;
+        __syncthreads();
+        inc[tid] = run;
+        // Next to nothing is left of p - q (uniform): p itself.  A token that was drawn from q is refused as often as p - q
+        // leaves, so this is not met in earnest; what is left then is the rounding of p and q (some 2^-50).
+        if (total < 0x1p-32 && kind != kPlain && turn == 0) {
+            kind = kPlain;
+            for (int t = wave; t < p.tiles; t += 4) {
+                const double again = tile_sum<XT, PROBS>(a, pick, kind, t);
+                if (lane == 0) tiles[t] = again;
+            }
+            __syncthreads();
+            continue;
+        }
+        if (!(total > 0.0 && total < __builtin_inf())) {
+            if (tid == 0) result = -1;
+            break;
+        }
+        const float u = a.u[(int64_t)s * (a.max_draft + 1) + a.max_draft];
+        const double r = (u > 0.f ? (double)u : 0.0) * total;
+        if (run > r && sum > 0.0) atomicMin(&first, tid);
+        if (sum > 0.0) atomicMax(&last, tid);
+        __syncthreads();
+        const int who = first < 256 ? first : last;
+        if (tid == who) {
+            double at = tid ? inc[tid - 1] : 0.0, from = at;
+            int hit = -1;
+            for (int t = t0; t < t1; ++t) {
+                const double v = tiles[t];
+                if (v > 0.0) hit = t, from = at;
+                at += v;
+                if (v > 0.0 && at > r) break;
+            }
+            found = hit, before = from;
+        }
+        __syncthreads();
+        if (wave == 0) {
+            const int tile = found;
+            double w[kTile / 64], at = before;
+#pragma unroll
+            for (int i = 0; i < kTile / 64; ++i) w[i] = weight<XT, PROBS>(a, pick, kind, tile * kTile + 64 * i + lane);
+            int hit = -1;
+            bool passed = false;
+#pragma unroll
+            for (int i = 0; i < kTile / 64; ++i) {
+                double sc = w[i];
+#pragma unroll
+                for (int off = 1; off < 64; off <<= 1) {
+                    const double o = __shfl_up(sc, off);
+                    if (lane >= off) sc += o;
+                }
+                const uint64_t some = __ballot(w[i] > 0.0), over = __ballot(w[i] > 0.0 && at + sc > r);
+                if (!passed && some) {
+                    passed = over != 0;
+                    const int l = passed ? (int)__ffsll((unsigned long long)over) - 1 : 63 - (int)__clzll((long long)some);
+                    hit = tile * kTile + 64 * i + l;
+                }
+                at += __shfl(sc, 63);
+            }
+            if (lane == 0) result = hit;
+        }
+        break;
+    }
+    __syncthreads();
+    if (tid <= a.max_draft) {
+        const int64_t at = (int64_t)s * (a.max_draft + 1) + tid;
+        const int taken = pick.taken;
+        a.out[at] = tid < taken ? a.tokens[(int64_t)s * a.max_draft + tid] : tid == taken ? result : -1;
+        if (tid == 0) a.n_accepted[s] = taken < 0 ? 0 : taken;
+    }
+}
+
+DraftPlan draft_plan(int64_t n_seqs, int64_t max_draft, int64_t n_vocab, bool has_draft, int elem_bytes, bool probs) {
+    DraftPlan p{};
+    const int64_t rows = probs ? 0 : n_seqs * (max_draft + 1 + (has_draft ? max_draft : 0));
+    const int64_t ve = 16 / elem_bytes, vecs = (n_vocab + 2 * ve - 2) / ve;      // of the worst alignment
+    // one pass a workgroup until there are some 16 workgroups for each of the 256 CUs, then longer chunks
+    int64_t passes = (vecs + kPassVecs - 1) / kPassVecs, per = 1;
+    while (per < 8 && rows * ((passes + per - 1) / per) > 4096) per *= 2;
+    p.chunk_vecs = (int)(per * kPassVecs);
+    p.chunks = (int)((passes + per - 1) / per);
+    p.tiles = (int)((n_vocab + kTile - 1) / kTile);
+    p.stat_groups = rows * p.chunks;
+    p.sum_groups = n_seqs * ((p.tiles + 3) / 4);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t from = at;
+        at += (bytes + 15) / 16 * 16;
+        return from;
+    };
+    p.off_z = take((size_t)p.stat_groups * 8);
+    p.off_max = take((size_t)p.stat_groups * 4);
+    p.off_arg = take((size_t)p.stat_groups * 4);
+    p.off_tiles = take((size_t)n_seqs * p.tiles * 8);
+    p.off_pick = take((size_t)n_seqs * sizeof(Pick));
+    p.ws_bytes = at;
+    return p;
+}
+
+hipError_t launch_draft_verify(const DraftVerify &a, const DraftPlan &p, Act xt, bool probs, hipStream_t s) {
+    return with_act(xt, [&](auto tag) -> hipError_t {
+        using XT = decltype(tag);
+        const unsigned sums = (unsigned)p.sum_groups, seqs = (unsigned)a.n_seqs;
+        if (probs) {
+            draft_sums<XT, true><<<sums, 256, 0, s>>>(a, p);
+            draft_pick<XT, true><<<seqs, 256, 0, s>>>(a, p);
+        } else {
+            draft_stats<XT><<<(unsigned)p.stat_groups, 256, 0, s>>>(a, p);
+            draft_sums<XT, false><<<sums, 256, 0, s>>>(a, p);
+            draft_pick<XT, false><<<seqs, 256, 0, s>>>(a, p);
+        }
+        return hipGetLastError();
+    });
+}
+
+}  // namespace q2_0

@@ -1,0 +1,178 @@
+// Expert choice from scores in 64 bits: sigmoid or softmax of the logits, a bias for balance, the best
+// groups, the n_used best experts in them and their weights.
+//
+// One wave per token.  Lane l holds PL consecutive experts (l*PL ..) as unsigned 64-bit keys that
+// order as the biased scores do (sign-folded bits of the double, NaN below -inf, 0 for "not to be
+// chosen").  Scores are worked out in 64 bits because they decide: two f32 sigmoids of different
+// logits, or a score and its bias added in f32, fall on the same or on swapped values some
+// once in 10^5 choices, and an expert chosen otherwise is another result.  A round takes the
+// wave's largest key as moe_choose does, upper halves first and lower halves only where these are
+// equal, and the lowest lane and place among equals is the lowest index.
+//
+// Groups: the keys go through LDS, lane g looks through group g for its one or two best; a group's
+// rank is the number of groups before it, counted with a lane read of each.
+#include <type_traits>
+
+#include "serve_common.h"
+
+namespace q2_0 {
+
+__device__ __forceinline__ uint64_t order_key64(double v) {
+    if (v != v) return 1u;
+    const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);    // -0 + 0 = +0
+    return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+}
+
+__device__ __forceinline__ double key_value64(uint64_t k) {
+    if (k <= 1u) return __builtin_nan("");
+    return __builtin_bit_cast(double, (k >> 63) ? (k & 0x7fffffffffffffffull) : ~k);
+}
+
+__device__ __forceinline__ uint64_t read_lane64(uint64_t v, int lane) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
+    return (uint64_t)hi << 32 | lo;
+}
+
+__device__ __forceinline__ double wave_sum_f64(double v) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+    return v;
+}
+
+template <int PL, typename XT, bool SIGMOID>
+__global__ __launch_bounds__(256) void moe_choose_groups(ChooseGroups a) {
+    extern __shared__ uint64_t key_lds[];                        // 4 waves x 64 * PL keys, with groups only
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+    if (t >= a.n_tokens) return;                                 // (no barrier below)
+    const XT *row = static_cast<const XT *>(a.logits) + t * a.ld;
+    float v[PL];
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+        const int e = lane * PL + i;
+        v[i] = e < a.n_expert ? act_to_f32(row[e]) : -__builtin_inff();
+    }
+    // softmax about the largest logit; a row of -inf alone has scores 0
+    double m = 0.0, inv = 0.0;
+    if (!SIGMOID) {
+        float top = v[0];
+#pragma unroll
+        for (int i = 1; i < PL; ++i) top = fmaxf(top, v[i]);
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+        m = top == -__builtin_inff() ? 0.0 : (double)top;
+    }
+    double s[PL];
+    if (SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < PL; ++i) s[i] = 1.0 / (1.0 + exp(-(double)v[i]));
+    } else {
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            s[i] = exp((double)v[i] - m);
+            sum += s[i];
+        }
+        sum = wave_sum_f64(sum);
+        inv = sum == 0.0 ? 0.0 : 1.0 / sum;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) s[i] *= inv;
+    }
+    uint64_t key[PL];
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+        const int e = lane * PL + i;
+        key[i] = e < a.n_expert ? order_key64(s[i] + (a.bias ? (double)a.bias[e] : 0.0)) : 0u;
+    }
+    if (a.n_group > 1) {
+        uint64_t *mine = key_lds + wave * 64 * PL;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) mine[lane * PL + i] = key[i];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        uint64_t g = 0u;
+        if (lane < a.n_group) {
+            const int n = (int)a.size.d;
+            uint64_t b1 = 0u, b2 = 0u;
+            for (int i = 0; i < n; ++i) {
+                const uint64_t k = mine[lane * n + i];
+                b2 = k > b1 ? b1 : (k > b2 ? k : b2);
+                b1 = k > b1 ? k : b1;
+            }
+            g = order_key64(a.group_top == 2 ? key_value64(b1) + key_value64(b2) : key_value64(b1));
+        }
+        int rank = 0;
+        for (int h = 0; h < a.n_group; ++h) {
+            const uint64_t k = read_lane64(g, h);
+            rank += k > g || (k == g && h < lane);
+        }
+        const uint64_t open = __ballot(lane < a.n_group && rank < a.n_group_used);
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            const int e = lane * PL + i;
+            if (e < a.n_expert && !((open >> a.size.div((uint32_t)e)) & 1)) key[i] = 0u;
+        }
+    }
+    int my_id = 0;         // lane u < n_used: the u-th choice
+    for (int u = 0; u < a.n_used; ++u) {
+        uint64_t best = key[0];
+        int at = 0;
+#pragma unroll
+        for (int i = 1; i < PL; ++i) {
+            const bool more = key[i] > best;
+            best = more ? key[i] : best;
+            at = more ? i : at;
+        }
+        const uint32_t hi = (uint32_t)(best >> 32), lo = (uint32_t)best;
+        const uint32_t top = wave_max_u32(hi);
+        uint64_t held = __ballot(hi == top);
+        if (held & (held - 1)) {                                 // (uniform) equal upper halves: the lower ones decide
+            const uint32_t low = wave_max_u32(hi == top ? lo : 0u);
+            held = __ballot(hi == top && lo == low);
+        }
+        const int win = (int)__ffsll((unsigned long long)held) - 1;
+        const int id = win * PL + __builtin_amdgcn_readlane(at, win);
+        my_id = lane == u ? id : my_id;
+#pragma unroll
+        for (int i = 0; i < PL; ++i)
+            if (lane == win && i == at) key[i] = 0u;
+    }
+    // the chosen experts' scores without the bias; one that the bias masks (-inf) weighs nothing
+    double w = 0.0;
+    if (lane < a.n_used) {
+        const double x = (double)act_to_f32(row[my_id]);
+        w = SIGMOID ? 1.0 / (1.0 + exp(-x)) : exp(x - m) * inv;
+        if (a.bias && a.bias[my_id] == -__builtin_inff()) w = 0.0;
+    }
+    if (a.normalise) {
+        const double sum = wave_sum_f64(w);
+        w = sum == 0.0 ? 0.0 : w / sum;
+    }
+    if (lane < a.n_used) {
+        a.ids[t * a.n_used + lane] = my_id;
+        a.weights[t * a.n_used + lane] = (float)(w * (double)a.scale);   // rounded to f32 once
+    }
+}
+
+hipError_t launch_moe_choose_groups(const ChooseGroups &a, Act xt, bool sigmoid, hipStream_t s) {
+    return with_act(xt, [&](auto tag) -> hipError_t {
+        using XT = decltype(tag);
+        const dim3 grid((unsigned)((a.n_tokens + 3) / 4));
+        auto go = [&](auto pl) {
+            constexpr int PL = decltype(pl)::value;
+            const size_t lds = a.n_group > 1 ? 4 * 64 * PL * sizeof(uint64_t) : 0;
+            if (sigmoid) moe_choose_groups<PL, XT, true><<<grid, 256, lds, s>>>(a);
+            else moe_choose_groups<PL, XT, false><<<grid, 256, lds, s>>>(a);
+        };
+        // the smallest register tile that holds a row
+        if (a.n_expert <= 64) go(std::integral_constant<int, 1>{});
+        else if (a.n_expert <= 128) go(std::integral_constant<int, 2>{});
+        else if (a.n_expert <= 256) go(std::integral_constant<int, 4>{});
+        else if (a.n_expert <= 512) go(std::integral_constant<int, 8>{});
+        else go(std::integral_constant<int, 16>{});
+        return hipGetLastError();
+    });
+}
+
+}  // namespace q2_0

@@ -1,0 +1,115 @@
+// Shared by the operators between two decoder steps: grouped expert choice, verification of
+// drafted tokens, pages of the cache.
+#pragma once
+
+#include "layer_common.h"
+
+namespace q2_0 {
+
+// ---- expert choice in groups
+struct ChooseGroups {
+    const void *logits;
+    int64_t ld, n_tokens;
+    const float *bias;
+    FastDiv size;          // experts of a group
+    int n_expert, n_used, n_group, n_group_used, group_top;
+    int normalise;
+    float scale;
+    int32_t *ids;
+    float *weights;
+};
+hipError_t launch_moe_choose_groups(const ChooseGroups &a, Act xt, bool sigmoid, hipStream_t s);
+
+// ---- verification of drafted tokens
+struct DraftPlan {
+    int64_t stat_groups;   // workgroups of the statistics (0: probabilities are given)
+    int64_t sum_groups;    // of the tile sums
+    int chunks;            // of a row in the statistics
+    int chunk_vecs;        // 16-byte vectors of a chunk
+    int tiles;             // of a row in the tile sums
+    size_t off_z, off_max, off_arg, off_tiles, off_pick;
+    size_t ws_bytes;
+};
+struct DraftVerify {
+    const void *target, *draft;
+    int64_t ld_target, ld_draft;
+    int n_vocab, n_seqs, max_draft;
+    const float *temperature;
+    const int32_t *tokens, *n_draft;
+    const float *u;
+    int32_t *out, *n_accepted;
+    char *ws;
+};
+DraftPlan draft_plan(int64_t n_seqs, int64_t max_draft, int64_t n_vocab, bool has_draft, int elem_bytes, bool probs);
+hipError_t launch_draft_verify(const DraftVerify &a, const DraftPlan &p, Act xt, bool probs, hipStream_t s);
+
+// ---- pages of a cache
+struct PageRows {          // where the rows of a page are in the two pools
+    char *k, *v;
+    int64_t page_stride, head_stride, token_stride;   // bytes
+};
+struct PageShape {
+    FastDiv page;          // token rows of a page
+    int heads;             // key heads
+    int vec_shift;         // log2 of the 16-byte vectors of a row
+    int vecs;              // of a page: both pools, all heads and rows
+};
+struct PageTable {
+    int32_t *table;
+    int64_t ld;
+    int n_seqs, cols;
+    int32_t *lens;
+};
+struct KvCopy {
+    PageRows to, from;
+    PageShape shape;
+    int to_pages, from_pages;
+    const int32_t *src, *dst;
+    int n;
+};
+hipError_t launch_kv_copy(const KvCopy &a, hipStream_t s);
+int64_t kv_copy_groups(const PageShape &p, int64_t n);
+
+struct KvFork {
+    PageTable t;
+    FastDiv page;
+    int32_t *ref;
+    int n_pages, n;
+    const int32_t *src, *dst;
+    int32_t *plan;         // length that pair i copies, -1: none
+};
+hipError_t launch_kv_fork(const KvFork &a, hipStream_t s);
+int64_t kv_table_groups(int64_t n_rows, int64_t cols);
+
+constexpr int kResizeMaxSeqs = 8192;
+struct KvResize {
+    PageTable t;
+    PageRows rows;
+    PageShape shape;
+    int32_t *ref;
+    uint32_t *free;
+    int n_pages;
+    const int32_t *new_lens;
+    int32_t *missing;
+    int32_t *plan;         // 8 numbers a sequence
+    int32_t *fresh;        // the pages that the call takes
+};
+hipError_t launch_kv_resize(const KvResize &a, hipStream_t s);
+
+struct KvCompact {
+    PageTable t;
+    PageRows to, from;
+    PageShape shape;
+    const int32_t *ref;
+    const uint32_t *free;
+    int from_pages, to_pages;
+    int32_t *to_ref;
+    uint32_t *to_free;
+    int32_t *to_table;
+    int64_t ld_to;
+    int32_t *n_used;
+    int32_t *before;       // pages in use before each word of `free`
+};
+hipError_t launch_kv_compact(const KvCompact &a, hipStream_t s);
+
+}  // namespace q2_0

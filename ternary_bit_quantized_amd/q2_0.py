@@ -34,6 +34,10 @@ Q2_0_ACT_F16 = 1
 Q2_0_ACT_BF16 = 2
 Q2_0_ROPE_HALF = 0
 Q2_0_ROPE_PAIRS = 1
+Q2_0_SCORE_SOFTMAX = 0
+Q2_0_SCORE_SIGMOID = 1
+Q2_0_DRAFT_LOGITS = 0
+Q2_0_DRAFT_PROBS = 1
 BLOCK_WEIGHTS = 64
 BLOCK_BYTES = 18
 MAT_VEC_MAX_N = 8
@@ -41,6 +45,7 @@ NOALLOC_SCRATCH_BYTES = 64 << 20
 ATTN_MAX_QT = 16
 MOE_LAYER_MAX_TOKENS = 64
 MOE_LAYER_MAX_USED = 32
+DRAFT_MAX = 15
 
 EXPORTS = ("q2_0_get_rows", "q2_0_mul_mat_vec", "q2_0_mul_mat_vec_group", "q2_0_mul_mat",
            "q2_0_mul_mat_workspace_bytes", "q2_0_mul_mat_group", "q2_0_mul_mat_group_workspace_bytes",
@@ -48,6 +53,9 @@ EXPORTS = ("q2_0_get_rows", "q2_0_mul_mat_vec", "q2_0_mul_mat_vec_group", "q2_0_
            "q2_0_quantize", "q2_0_repack_g128", "q2_0_mul_mat_id", "q2_0_mul_mat_id_workspace_bytes",
            "q2_0_mul_mat_noalloc", "q2_0_mul_mat_vec_batch", "q2_0_kv_append", "q2_0_attn_shared",
            "q2_0_attn_shared_workspace_bytes", "q2_0_moe_route", "q2_0_moe_layer", "q2_0_moe_layer_workspace_bytes",
+           "q2_0_moe_route_groups", "q2_0_draft_verify", "q2_0_draft_verify_workspace_bytes", "q2_0_kv_copy",
+           "q2_0_kv_fork", "q2_0_kv_fork_workspace_bytes", "q2_0_kv_resize", "q2_0_kv_resize_workspace_bytes",
+           "q2_0_kv_compact", "q2_0_kv_compact_workspace_bytes",
            "q2_0_status_string", "q2_0_last_hip_error", "q2_0_version")
 
 
@@ -68,6 +76,11 @@ class KvCache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("type", ctypes.c_int), ("n_pages", ctypes.c_int64),
                 ("page_size", ctypes.c_int64), ("n_kv", ctypes.c_int64), ("head_dim", ctypes.c_int64),
                 ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+
+
+class KvPages(ctypes.Structure):
+    """q2_0_kv_pages: counts and free bits of a cache's pages."""
+    _fields_ = [("ref", ctypes.c_void_p), ("free", ctypes.c_void_p), ("n_pages", ctypes.c_int64)]
 
 
 def make_batch_items(entries):
@@ -148,6 +161,23 @@ def lib() -> ctypes.CDLL:
         L.q2_0_moe_layer.restype = C
         L.q2_0_moe_layer_workspace_bytes.argtypes = [I64] * 4
         L.q2_0_moe_layer_workspace_bytes.restype = ctypes.c_size_t
+        S = ctypes.c_size_t
+        L.q2_0_moe_route_groups.argtypes = [P, C, I64, I64, I64, I64, C, P, I64, I64, I64, C, ctypes.c_float, P, P, P]
+        L.q2_0_draft_verify.argtypes = [P, I64, P, I64, C, C, I64, P, P, P, P, I64, I64, P, P, P, S, P]
+        L.q2_0_draft_verify_workspace_bytes.argtypes = [I64, I64, I64, C, C, C]
+        L.q2_0_kv_copy.argtypes = [P, P, P, P, I64, P]
+        L.q2_0_kv_fork.argtypes = [P, I64, P, I64, I64, I64, I64, P, P, P, I64, P, S, P]
+        L.q2_0_kv_fork_workspace_bytes.argtypes = [I64]
+        L.q2_0_kv_resize.argtypes = [P, P, P, I64, I64, I64, P, P, P, P, S, P]
+        L.q2_0_kv_resize_workspace_bytes.argtypes = [I64, I64]
+        L.q2_0_kv_compact.argtypes = [P, P, P, P, P, I64, I64, I64, P, P, I64, P, P, S, P]
+        L.q2_0_kv_compact_workspace_bytes.argtypes = [I64]
+        for f in (L.q2_0_moe_route_groups, L.q2_0_draft_verify, L.q2_0_kv_copy, L.q2_0_kv_fork, L.q2_0_kv_resize,
+                  L.q2_0_kv_compact):
+            f.restype = C
+        for f in (L.q2_0_draft_verify_workspace_bytes, L.q2_0_kv_fork_workspace_bytes, L.q2_0_kv_resize_workspace_bytes,
+                  L.q2_0_kv_compact_workspace_bytes):
+            f.restype = S
         for f in (L.q2_0_mul_mat_vec_act, L.q2_0_mul_mat_vec_group_act, L.q2_0_mul_mat_act,
                   L.q2_0_mul_mat_group_act, L.q2_0_quantize, L.q2_0_repack_g128, L.q2_0_mul_mat_id):
             f.restype = ctypes.c_int
@@ -295,6 +325,67 @@ def moe_layer_raw(w_gate: int, w_up: int, w_down: int, n_expert: int, n_ff: int,
 @functools.lru_cache(maxsize=1024)      # (a function of the sizes alone)
 def moe_layer_workspace_bytes(n_ff: int, K: int, n_used: int, n_tokens: int) -> int:
     return lib().q2_0_moe_layer_workspace_bytes(n_ff, K, n_used, n_tokens)
+
+
+def moe_route_groups_raw(logits: int, x_type: int, ld: int, n_tokens: int, n_expert: int, n_used: int, score: int, bias: int,
+                         n_group: int, n_group_used: int, group_top: int, normalise: int, scale: float, ids: int,
+                         weights: int, stream: int = 0) -> int:
+    return lib().q2_0_moe_route_groups(logits, x_type, ld, n_tokens, n_expert, n_used, score, bias, n_group, n_group_used,
+                                       group_top, normalise, scale, ids, weights, stream)
+
+
+def draft_verify_raw(target: int, ld_target: int, draft: int, ld_draft: int, x_type: int, form: int, n_vocab: int,
+                     temperature: int, tokens: int, n_draft: int, u: int, n_seqs: int, max_draft: int, out: int,
+                     n_accepted: int, workspace: int, ws_bytes: int, stream: int = 0) -> int:
+    return lib().q2_0_draft_verify(target, ld_target, draft, ld_draft, x_type, form, n_vocab, temperature, tokens, n_draft, u,
+                                   n_seqs, max_draft, out, n_accepted, workspace, ws_bytes, stream)
+
+
+@functools.lru_cache(maxsize=1024)      # (a function of the sizes alone)
+def draft_verify_workspace_bytes(n_seqs: int, max_draft: int, n_vocab: int, x_type: int, form: int, has_draft: int) -> int:
+    return lib().q2_0_draft_verify_workspace_bytes(n_seqs, max_draft, n_vocab, x_type, form, has_draft)
+
+
+def _ref(struct):
+    return ctypes.byref(struct) if struct is not None else None
+
+
+def kv_copy_raw(to: KvCache, frm: KvCache, src: int, dst: int, n: int, stream: int = 0) -> int:
+    return lib().q2_0_kv_copy(_ref(to), _ref(frm), src, dst, n, stream)
+
+
+def kv_fork_raw(ref: int, n_pages: int, table: int, n_seqs: int, table_len: int, ld_table: int, page_size: int, lens: int,
+                src: int, dst: int, n: int, workspace: int, ws_bytes: int, stream: int = 0) -> int:
+    return lib().q2_0_kv_fork(ref, n_pages, table, n_seqs, table_len, ld_table, page_size, lens, src, dst, n, workspace,
+                              ws_bytes, stream)
+
+
+@functools.lru_cache(maxsize=1024)      # (a function of the sizes alone)
+def kv_fork_workspace_bytes(n: int) -> int:
+    return lib().q2_0_kv_fork_workspace_bytes(n)
+
+
+def kv_resize_raw(cache: KvCache, pages: KvPages, table: int, n_seqs: int, table_len: int, ld_table: int, lens: int,
+                  new_lens: int, missing: int, workspace: int, ws_bytes: int, stream: int = 0) -> int:
+    return lib().q2_0_kv_resize(_ref(cache), _ref(pages), table, n_seqs, table_len, ld_table, lens, new_lens, missing,
+                                workspace, ws_bytes, stream)
+
+
+@functools.lru_cache(maxsize=1024)      # (a function of the sizes alone)
+def kv_resize_workspace_bytes(n_seqs: int, n_pages: int) -> int:
+    return lib().q2_0_kv_resize_workspace_bytes(n_seqs, n_pages)
+
+
+def kv_compact_raw(to: KvCache, to_pages: KvPages, frm: KvCache, from_pages: KvPages, table: int, n_seqs: int, table_len: int,
+                   ld_table: int, lens: int, to_table: int, ld_to_table: int, n_used: int, workspace: int, ws_bytes: int,
+                   stream: int = 0) -> int:
+    return lib().q2_0_kv_compact(_ref(to), _ref(to_pages), _ref(frm), _ref(from_pages), table, n_seqs, table_len, ld_table,
+                                 lens, to_table, ld_to_table, n_used, workspace, ws_bytes, stream)
+
+
+@functools.lru_cache(maxsize=1024)      # (a function of the sizes alone)
+def kv_compact_workspace_bytes(n_pages: int) -> int:
+    return lib().q2_0_kv_compact_workspace_bytes(n_pages)
 
 
 def version() -> str:
@@ -698,3 +789,160 @@ def q2_0_moe_layer(w_gate, w_up, w_down, n_expert: int, n_ff: int, K: int, x, id
                          _dense(weights, torch.float32, (n, n_used), "weights", dev), n_used, n, yp, ldy, wsp, wsb,
                          _stream(stream, dev)), "q2_0_moe_layer")
     return y
+
+
+# ------------------------------------------------------------- between two decoder steps (torch)
+
+def _ints(t, name, dev):
+    """A contiguous 1-D int32 tensor -> (address, length)."""
+    import torch
+    if t.dtype != torch.int32 or t.get_device() != dev or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous 1-D int32 tensor on the current CUDA device" % name)
+    return t.data_ptr(), t.shape[0]
+
+
+def _pages(ref, free, n_pages, dev):
+    """Counts and free bits (int32, 32 pages a word) of n_pages pages -> KvPages."""
+    import torch
+    return KvPages(_dense(ref, torch.int32, (n_pages,), "ref", dev),
+                   _dense(free, torch.int32, ((n_pages + 31) // 32,), "free", dev), n_pages)
+
+
+def q2_0_kv_pages(n_pages: int, device="cuda"):
+    """(ref, free) of a new pool of n_pages pages, all free: int32 counts, and int32 words of 32 pages' bits."""
+    import torch
+    return torch.zeros(n_pages, dtype=torch.int32, device=device), \
+        torch.full(((n_pages + 31) // 32,), -1, dtype=torch.int32, device=device)
+
+
+def q2_0_moe_route_groups(logits, n_used: int, score: int = Q2_0_SCORE_SIGMOID, bias=None, n_group: int = 1,
+                          n_group_used: int = 1, group_top: int = 1, normalise: bool = True, scale: float = 1.0, ids=None,
+                          weights=None, stream=None):
+    """(ids, weights), each (n_tokens, n_used): the n_used experts of the largest score + bias in the n_group_used best of
+    n_group groups (by the sum of a group's group_top largest), largest first and the lower index first among equals, and
+    scale * score, over the chosen scores' sum with normalise.  logits (n_tokens, n_expert) float32, float16 or bfloat16;
+    score Q2_0_SCORE_SIGMOID or Q2_0_SCORE_SOFTMAX; bias (n_expert) float32 or None, for the choice alone."""
+    import torch
+    dev = torch.cuda.current_device()
+    n_expert = _wide(logits, "logits")
+    n = logits.shape[0]
+    xt = _act_types().get(logits.dtype)
+    if xt is None:
+        raise ValueError("logits must be float32, float16 or bfloat16")
+    ld = _rows(logits, n, n_expert, "logits", dev)
+    bp = 0 if bias is None else _dense(bias, torch.float32, (n_expert,), "bias", dev)
+    if ids is None:
+        ids = _empty(logits, (n, n_used), torch.int32, stream)
+    if weights is None:
+        weights = _empty(logits, (n, n_used), torch.float32, stream)
+    _check(moe_route_groups_raw(logits.data_ptr(), xt, ld, n, n_expert, n_used, score, bp, n_group, n_group_used, group_top,
+                                int(bool(normalise)), scale, _dense(ids, torch.int32, (n, n_used), "ids", dev),
+                                _dense(weights, torch.float32, (n, n_used), "weights", dev), _stream(stream, dev)),
+           "q2_0_moe_route_groups")
+    return ids, weights
+
+
+def q2_0_draft_verify(target, draft, tokens, n_draft, u, form: int = Q2_0_DRAFT_LOGITS, temperature=None, out=None,
+                      n_accepted=None, workspace=None, stream=None):
+    """(out (n_seqs, max_draft + 1), n_accepted (n_seqs)), int32: the drafted tokens that the target takes, the token that
+    follows them, then -1; and how many are taken.
+
+    target (n_seqs*(max_draft+1), n_vocab) and draft (n_seqs*max_draft, n_vocab; None: drafts that were found, not drawn)
+    float32, float16 or bfloat16, both logits or both probabilities (form); tokens (n_seqs, max_draft) and n_draft (n_seqs)
+    int32; u (n_seqs, max_draft + 1) float32 of [0, 1); temperature (n_seqs) float32, 0 for the largest logit."""
+    import torch
+    dev = torch.cuda.current_device()
+    n, most = n_draft.shape[0] if n_draft.dim() == 1 else -1, _wide(tokens, "tokens")
+    vocab = _wide(target, "target")
+    xt = _act_types().get(target.dtype)
+    if xt is None or (draft is not None and draft.dtype != target.dtype):
+        raise ValueError("target and draft must be float32, float16 or bfloat16, both of one dtype")
+    ldt = _rows(target, n * (most + 1), vocab, "target", dev)
+    dp, ldd = 0, 0
+    if draft is not None:
+        if _wide(draft, "draft") != vocab:
+            raise ValueError("draft must have as many columns as target")
+        dp, ldd = draft.data_ptr(), _rows(draft, n * most, vocab, "draft", dev)
+    tp = 0 if temperature is None else _dense(temperature, torch.float32, (n,), "temperature", dev)
+    if out is None:
+        out = _empty(target, (n, most + 1), torch.int32, stream)
+    if n_accepted is None:
+        n_accepted = _empty(target, (n,), torch.int32, stream)
+    need = draft_verify_workspace_bytes(n, most, vocab, xt, form, int(draft is not None))
+    workspace, wsp, wsb = _work(workspace, need, target, stream, dev)
+    _check(draft_verify_raw(target.data_ptr(), ldt, dp, ldd, xt, form, vocab, tp,
+                            _dense(tokens, torch.int32, (n, most), "tokens", dev),
+                            _dense(n_draft, torch.int32, (n,), "n_draft", dev),
+                            _dense(u, torch.float32, (n, most + 1), "u", dev), n, most,
+                            _dense(out, torch.int32, (n, most + 1), "out", dev),
+                            _dense(n_accepted, torch.int32, (n,), "n_accepted", dev), wsp, wsb, _stream(stream, dev)),
+           "q2_0_draft_verify")
+    return out, n_accepted
+
+
+def q2_0_kv_copy(k_to, v_to, k_from, v_from, src, dst, stream=None):
+    """Copies pages src[i] of the pools k_from, v_from to pages dst[i] of k_to, v_to (the same pools, or others of the same
+    page): src, dst int32, pairs outside the pools are left out."""
+    import torch
+    dev = torch.cuda.current_device()
+    to, frm = _cache(k_to, v_to, dev), _cache(k_from, v_from, dev)
+    sp, n = _ints(src, "src", dev)
+    _check(kv_copy_raw(to, frm, sp, _dense(dst, torch.int32, (n,), "dst", dev), n, _stream(stream, dev)), "q2_0_kv_copy")
+
+
+def q2_0_kv_fork(ref, table, page_size: int, lens, src, dst, workspace=None, stream=None):
+    """Sequence dst[i] (empty) becomes one of the same tokens as src[i], in the same pages: table, lens and ref change.
+
+    ref (n_pages), lens (n_seqs), src and dst (n) int32; table (n_seqs, pages) int32."""
+    import torch
+    dev = torch.cuda.current_device()
+    tp, n_seqs, cols, ldt = _table(table, dev)
+    rp, n_pages = _ints(ref, "ref", dev)
+    sp, n = _ints(src, "src", dev)
+    workspace, wsp, wsb = _work(workspace, kv_fork_workspace_bytes(n), ref, stream, dev)
+    _check(kv_fork_raw(rp, n_pages, tp, n_seqs, cols, ldt, page_size, _dense(lens, torch.int32, (n_seqs,), "lens", dev), sp,
+                       _dense(dst, torch.int32, (n,), "dst", dev), n, wsp, wsb, _stream(stream, dev)), "q2_0_kv_fork")
+
+
+def q2_0_kv_resize(k_cache, v_cache, ref, free, table, lens, new_lens, missing=None, workspace=None, stream=None):
+    """Every sequence gets the length new_lens[s] (-1: as it is): the pages that it leaves go back, those that it needs are
+    taken, and a shared page that it would write in becomes a copy of its own.  table, lens, ref, free and the pools change.
+    Returns missing (1) int32: 0, or how many free pages too few there are (then no sequence has grown).
+
+    ref (n_pages) and free ((n_pages + 31) // 32) as q2_0_kv_pages gives them; table (n_seqs, pages), lens and new_lens
+    (n_seqs) int32."""
+    import torch
+    dev = torch.cuda.current_device()
+    c = _cache(k_cache, v_cache, dev)
+    tp, n_seqs, cols, ldt = _table(table, dev)
+    if missing is None:
+        missing = _empty(lens, (1,), torch.int32, stream)
+    if n_seqs == 0:
+        return missing.zero_()
+    workspace, wsp, wsb = _work(workspace, kv_resize_workspace_bytes(n_seqs, c.n_pages), lens, stream, dev)
+    _check(kv_resize_raw(c, _pages(ref, free, c.n_pages, dev), tp, n_seqs, cols, ldt,
+                         _dense(lens, torch.int32, (n_seqs,), "lens", dev),
+                         _dense(new_lens, torch.int32, (n_seqs,), "new_lens", dev),
+                         _dense(missing, torch.int32, (1,), "missing", dev), wsp, wsb, _stream(stream, dev)), "q2_0_kv_resize")
+    return missing
+
+
+def q2_0_kv_compact(k_to, v_to, ref_to, free_to, table_to, k_from, v_from, ref, free, table, lens, n_used=None,
+                    workspace=None, stream=None):
+    """Moves the pages that are not free from the pools k_from, v_from to the first pages of k_to, v_to, in order, and writes
+    their counts, bits and table rows there.  Returns n_used (1) int32: how many there are; more than the new pools
+    hold: nothing else is written.  table_to like table (n_seqs, pages) int32; lens (n_seqs) int32."""
+    import torch
+    dev = torch.cuda.current_device()
+    to, frm = _cache(k_to, v_to, dev), _cache(k_from, v_from, dev)
+    tp, n_seqs, cols, ldt = _table(table, dev)
+    np_, n_to, cols_to, ldn = _table(table_to, dev)
+    if n_to != n_seqs or cols_to != cols:
+        raise ValueError("table_to must have the shape of table")
+    if n_used is None:
+        n_used = _empty(lens, (1,), torch.int32, stream)
+    workspace, wsp, wsb = _work(workspace, kv_compact_workspace_bytes(frm.n_pages), lens, stream, dev)
+    _check(kv_compact_raw(to, _pages(ref_to, free_to, to.n_pages, dev), frm, _pages(ref, free, frm.n_pages, dev), tp, n_seqs,
+                          cols, ldt, _dense(lens, torch.int32, (n_seqs,), "lens", dev), np_, ldn,
+                          _dense(n_used, torch.int32, (1,), "n_used", dev), wsp, wsb, _stream(stream, dev)), "q2_0_kv_compact")
+    return n_used
