@@ -207,6 +207,12 @@ __device__ __forceinline__ double prob(float x, double k, double m, double inv) 
     return PROBS ? (double)x : exp2_64(((double)x - m) * k) * inv;
 }
 
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+    return v;
+}
+
 // All threads of the workgroup; the result is in `pick` after a barrier.
 template <typename XT, bool PROBS>
 __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pick) {
@@ -220,6 +226,20 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
     }
     const bool greedy = !PROBS && greedy_of(a, s);
     const double k = PROBS ? 0.0 : scale_of(a, s);
+    // the drafted tokens' values are asked for first: they arrive while the rows are joined
+    int tok = -1;
+    bool known = false;
+    float xt = 0.f, xd = 0.f, u = 0.f;
+    const int64_t row_p = (int64_t)s * per + lane, row_q = (int64_t)s * a.max_draft + lane;
+    if (wave == 0 && lane < nd) {
+        tok = a.tokens[row_q];
+        u = a.u[row_p];
+        known = tok >= 0 && tok < a.n_vocab;
+        if (known && !greedy) {
+            xt = act_to_f32(static_cast<const XT *>(a.target)[row_p * a.ld_target + tok]);
+            if (a.draft) xd = act_to_f32(static_cast<const XT *>(a.draft)[row_q * a.ld_draft + tok]);
+        }
+    }
     if (!PROBS) {
         const int rows = nd + 1 + (a.draft && !greedy ? nd : 0);
         for (int r = wave; r < rows; r += 4) {
@@ -238,11 +258,13 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
                 sum += greedy ? z[c] : z[c] * exp2_64(((double)m[c] - (double)top) * k);
                 if (greedy && m[c] == top) best = at[c] < best ? at[c] : best;
             }
+            sum = wave_sum(sum);
+            if (greedy) {
 #pragma unroll
-            for (int off = 32; off >= 1; off >>= 1) {
-                sum += __shfl_xor(sum, off);
-                const int o = __shfl_xor(best, off);
-                best = o < best ? o : best;
+                for (int off = 32; off >= 1; off >>= 1) {
+                    const int o = __shfl_xor(best, off);
+                    best = o < best ? o : best;
+                }
             }
             if (lane == 0) {
                 most[r] = top;
@@ -254,22 +276,13 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
     }
     if (wave != 0) return;
     bool yes = false;
-    int tok = -1;
-    const int64_t row_p = (int64_t)s * per + lane, row_q = (int64_t)s * a.max_draft + lane;
-    if (lane < nd) {
-        tok = a.tokens[row_q];
-        if (tok >= 0 && tok < a.n_vocab) {
-            if (greedy) {
-                yes = arg[lane] == tok;
-            } else {
-                const double pt = prob<PROBS>(act_to_f32(static_cast<const XT *>(a.target)[row_p * a.ld_target + tok]), k,
-                                              PROBS ? 0.0 : most[lane], PROBS ? 0.0 : inv[lane]);
-                double qt = 1.0;
-                if (a.draft)
-                    qt = prob<PROBS>(act_to_f32(static_cast<const XT *>(a.draft)[row_q * a.ld_draft + tok]), k,
-                                     PROBS ? 0.0 : most[nd + 1 + lane], PROBS ? 0.0 : inv[nd + 1 + lane]);
-                yes = (double)a.u[row_p] * qt < pt;
-            }
+    if (known) {
+        if (greedy) {
+            yes = arg[lane] == tok;
+        } else {
+            const double pt = prob<PROBS>(xt, k, PROBS ? 0.0 : most[lane], PROBS ? 0.0 : inv[lane]);
+            const double qt = !a.draft ? 1.0 : prob<PROBS>(xd, k, PROBS ? 0.0 : most[nd + 1 + lane], PROBS ? 0.0 : inv[nd + 1 + lane]);
+            yes = (double)u * qt < pt;
         }
     }
     const uint64_t no = __ballot(!yes);                  // (lanes from nd on: not taken)
@@ -291,139 +304,158 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
     }
 }
 
-// What is left for token e: not below zero, NaN where either is.
-template <typename XT, bool PROBS>
-__device__ __forceinline__ double weight(const DraftVerify &a, const Pick &pick, int kind, int e) {
-    if (e >= a.n_vocab) return 0.0;
-    double w = prob<PROBS>(act_to_f32(static_cast<const XT *>(a.target)[pick.row_p * a.ld_target + e]), pick.k, pick.m_p,
-                           pick.inv_p);
-    if (kind == kMinus)
-        w -= prob<PROBS>(act_to_f32(static_cast<const XT *>(a.draft)[pick.row_q * a.ld_draft + e]), pick.k, pick.m_q,
-                         pick.inv_q);
-    if (kind == kOneHot && e == pick.token) w = 0.0;
-    return w <= 0.0 ? 0.0 : w;
+// What is left for N tokens from e on, `step` apart: not below zero, NaN where either is.  Loads first and without
+// branches (a place past the row reads its last token and counts nothing): with a branch around each they wait for one another.
+template <int N, typename XT, bool PROBS>
+__device__ __forceinline__ void weights(const DraftVerify &a, const Pick &pick, int kind, int e, int step, double (&w)[N]) {
+    const XT *t = static_cast<const XT *>(a.target) + pick.row_p * a.ld_target;
+    float x[N], y[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int at = e + i * step;
+        x[i] = act_to_f32(t[at < a.n_vocab ? at : a.n_vocab - 1]);
+    }
+    if (kind == kMinus) {
+        const XT *d = static_cast<const XT *>(a.draft) + pick.row_q * a.ld_draft;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = e + i * step;
+            y[i] = act_to_f32(d[at < a.n_vocab ? at : a.n_vocab - 1]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int at = e + i * step;
+        double v = prob<PROBS>(x[i], pick.k, pick.m_p, pick.inv_p);
+        if (kind == kMinus) v -= prob<PROBS>(y[i], pick.k, pick.m_q, pick.inv_q);
+        const bool out = at >= a.n_vocab || (kind == kOneHot && at == pick.token);
+        w[i] = out || v <= 0.0 ? 0.0 : v;
+    }
 }
 
-// Lane l holds tokens tile * 1024 + 64 i + l.
 template <typename XT, bool PROBS>
 __device__ __forceinline__ double tile_sum(const DraftVerify &a, const Pick &pick, int kind, int tile) {
-    double sum = 0.0;
+    double w[kTile / 64], sum = 0.0;
+    weights<kTile / 64, XT, PROBS>(a, pick, kind, tile * kTile + (int)(threadIdx.x & 63), 64, w);
 #pragma unroll
-    for (int i = 0; i < kTile / 64; ++i)
-        sum += weight<XT, PROBS>(a, pick, kind, tile * kTile + 64 * i + (int)(threadIdx.x & 63));
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
-    return sum;
+    for (int i = 0; i < kTile / 64; ++i) sum += w[i];
+    return wave_sum(sum);
 }
 
 template <typename XT, bool PROBS>
 __global__ __launch_bounds__(256) void draft_sums(DraftVerify a, DraftPlan p) {
-    const int per = (p.tiles + 3) / 4;                   // workgroups of a sequence
-    const int s = (int)(blockIdx.x / (unsigned)per), g = (int)(blockIdx.x % (unsigned)per);
+    const int s = (int)(blockIdx.x / (unsigned)p.sum_parts), g = (int)(blockIdx.x % (unsigned)p.sum_parts);
     __shared__ Pick pick;
     decide<XT, PROBS>(a, p, s, pick);
     __syncthreads();
     if (g == 0 && threadIdx.x == 0) reinterpret_cast<Pick *>(a.ws + p.off_pick)[s] = pick;
-    const int tile = g * 4 + (int)(threadIdx.x >> 6);
-    if (pick.kind == kFixed || tile >= p.tiles) return;
-    const double sum = tile_sum<XT, PROBS>(a, pick, pick.kind, tile);
-    if ((threadIdx.x & 63) == 0) reinterpret_cast<double *>(a.ws + p.off_tiles)[(int64_t)s * p.tiles + tile] = sum;
+    if (pick.kind == kFixed) return;
+    const Pick mine = pick;
+    for (int tile = g * 4 + (int)(threadIdx.x >> 6); tile < p.tiles; tile += p.sum_parts * 4) {
+        const double sum = tile_sum<XT, PROBS>(a, mine, mine.kind, tile);
+        if ((threadIdx.x & 63) == 0) reinterpret_cast<double *>(a.ws + p.off_tiles)[(int64_t)s * p.tiles + tile] = sum;
+    }
+}
+
+// Running sums over the 256 threads in their order: the sum up to the thread itself; `total`: all.
+__device__ __forceinline__ double run_256(double v, double *wave_sums, double &total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const double o = __shfl_up(v, off);
+        if (lane >= off) v += o;
+    }
+    __syncthreads();                                     // (wave_sums may be read still)
+    if (lane == 63) wave_sums[wave] = v;
+    __syncthreads();
+    const double s0 = wave_sums[0], s1 = wave_sums[1], s2 = wave_sums[2], s3 = wave_sums[3];
+    total = ((s0 + s1) + s2) + s3;
+    return v + (wave == 0 ? 0.0 : wave == 1 ? s0 : wave == 2 ? s0 + s1 : (s0 + s1) + s2);
+}
+
+// The first thread whose running sum is above r and that holds anything, else the last that does.
+__device__ __forceinline__ int thread_at(double run, double own, double r, int *hits) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint64_t over = __ballot(own > 0.0 && run > r), some = __ballot(own > 0.0);
+    if (lane == 0) {
+        hits[wave] = over ? 64 * wave + (int)__ffsll((unsigned long long)over) - 1 : -1;
+        hits[4 + wave] = some ? 64 * wave + 63 - (int)__clzll((long long)some) : -1;
+    }
+    __syncthreads();
+    int who = -1;
+#pragma unroll
+    for (int w = 3; w >= 0; --w) who = hits[w] >= 0 ? hits[w] : who;
+    if (who < 0)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) who = hits[4 + w] >= 0 ? hits[4 + w] : who;
+    return who;
 }
 
 template <typename XT, bool PROBS>
 __global__ __launch_bounds__(256) void draft_pick(DraftVerify a, DraftPlan p) {
-    const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    __shared__ Pick pick;
-    __shared__ double inc[256], before;
-    __shared__ int first, last, found, result;
+    const int s = blockIdx.x, tid = threadIdx.x, wave = tid >> 6;
+    __shared__ double wave_sums[4], before;
+    __shared__ int hits[8], found;
     double *tiles = reinterpret_cast<double *>(a.ws + p.off_tiles) + (int64_t)s * p.tiles;
-    if (tid == 0) {
-        pick = reinterpret_cast<const Pick *>(a.ws + p.off_pick)[s];
-        result = pick.token;
-    }
-    __syncthreads();
-    int kind = pick.kind;
+    const Pick pick = reinterpret_cast<const Pick *>(a.ws + p.off_pick)[s];
+    const float u = a.u[(int64_t)s * (a.max_draft + 1) + a.max_draft];
+    int kind = pick.kind, result = pick.token;
     const int each = (p.tiles + 255) / 256, t0 = tid * each, t1 = t0 + each < p.tiles ? t0 + each : p.tiles;
-    for (int turn = 0; kind != kFixed && turn < 2; ++turn) {
-        double sum = 0.0;
-        for (int t = t0; t < t1; ++t) sum += tiles[t];
-        // running sums over the threads
-        double run = sum;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const double o = __shfl_up(run, off);
-            if (lane >= off) run += o;
-        }
-        inc[tid] = run;
-        if (tid == 0) first = 256, last = -1;
-        __syncthreads();
-        double base = 0.0;
-        for (int w = 0; w < wave; ++w) base += inc[64 * w + 63];
-        const double total = ((inc[63] + inc[127]) + inc[191]) + inc[255];
-        run += base;
-        __syncthreads();
-        inc[tid] = run;
+    if (kind != kFixed) {
+        double own, run, total;
+        auto sums = [&]() {
+            own = 0.0;
+            for (int t = t0; t < t1; ++t) own += tiles[t];
+            run = run_256(own, wave_sums, total);
+        };
+        sums();
         // Next to nothing is left of p - q (uniform): p itself.  A token that was drawn from q is refused as often as p - q
         // leaves, so this is not met in earnest; what is left then is the rounding of p and q (some 2^-50).
-        if (total < 0x1p-32 && kind != kPlain && turn == 0) {
+        if (total < 0x1p-32 && kind != kPlain) {
             kind = kPlain;
             for (int t = wave; t < p.tiles; t += 4) {
                 const double again = tile_sum<XT, PROBS>(a, pick, kind, t);
-                if (lane == 0) tiles[t] = again;
+                if ((tid & 63) == 0) tiles[t] = again;
             }
             __syncthreads();
-            continue;
+            sums();
         }
-        if (!(total > 0.0 && total < __builtin_inf())) {
-            if (tid == 0) result = -1;
-            break;
-        }
-        const float u = a.u[(int64_t)s * (a.max_draft + 1) + a.max_draft];
-        const double r = (u > 0.f ? (double)u : 0.0) * total;
-        if (run > r && sum > 0.0) atomicMin(&first, tid);
-        if (sum > 0.0) atomicMax(&last, tid);
-        __syncthreads();
-        const int who = first < 256 ? first : last;
-        if (tid == who) {
-            double at = tid ? inc[tid - 1] : 0.0, from = at;
-            int hit = -1;
-            for (int t = t0; t < t1; ++t) {
-                const double v = tiles[t];
-                if (v > 0.0) hit = t, from = at;
-                at += v;
-                if (v > 0.0 && at > r) break;
-            }
-            found = hit, before = from;
-        }
-        __syncthreads();
-        if (wave == 0) {
-            const int tile = found;
-            double w[kTile / 64], at = before;
-#pragma unroll
-            for (int i = 0; i < kTile / 64; ++i) w[i] = weight<XT, PROBS>(a, pick, kind, tile * kTile + 64 * i + lane);
-            int hit = -1;
-            bool passed = false;
-#pragma unroll
-            for (int i = 0; i < kTile / 64; ++i) {
-                double sc = w[i];
-#pragma unroll
-                for (int off = 1; off < 64; off <<= 1) {
-                    const double o = __shfl_up(sc, off);
-                    if (lane >= off) sc += o;
+        result = -1;
+        if (total > 0.0 && total < __builtin_inf()) {
+            const double r = (u > 0.f ? (double)u : 0.0) * total;
+            if (tid == thread_at(run, own, r, hits)) {
+                double at = run - own, from = at;
+                for (int t = t0; t < t1; ++t) {
+                    const double v = tiles[t];
+                    if (v > 0.0) found = t, before = from = at;
+                    at += v;
+                    if (v > 0.0 && at > r) break;
                 }
-                const uint64_t some = __ballot(w[i] > 0.0), over = __ballot(w[i] > 0.0 && at + sc > r);
-                if (!passed && some) {
-                    passed = over != 0;
-                    const int l = passed ? (int)__ffsll((unsigned long long)over) - 1 : 63 - (int)__clzll((long long)some);
-                    hit = tile * kTile + 64 * i + l;
-                }
-                at += __shfl(sc, 63);
             }
-            if (lane == 0) result = hit;
+            __syncthreads();
+            const int e = found * kTile + tid * 4;
+            const double base = before;
+            double w[4];
+            weights<4, XT, PROBS>(a, pick, kind, e, 1, w);
+            own = ((w[0] + w[1]) + w[2]) + w[3];
+            run = base + run_256(own, wave_sums, total);
+            if (tid == thread_at(run, own, r, hits)) {
+                double at = run - own;
+                int hit = 0;
+#pragma unroll
+                for (int i = 3; i >= 0; --i) hit = w[i] > 0.0 ? i : hit;      // (the first that holds anything)
+                bool passed = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    at += w[i];
+                    if (!passed && w[i] > 0.0) hit = i, passed = at > r;
+                }
+                found = e + hit;
+            }
+            __syncthreads();
+            result = found;
         }
-        break;
     }
-    __syncthreads();
     if (tid <= a.max_draft) {
         const int64_t at = (int64_t)s * (a.max_draft + 1) + tid;
         const int taken = pick.taken;
@@ -443,7 +475,10 @@ DraftPlan draft_plan(int64_t n_seqs, int64_t max_draft, int64_t n_vocab, bool ha
     p.chunks = (int)((passes + per - 1) / per);
     p.tiles = (int)((n_vocab + kTile - 1) / kTile);
     p.stat_groups = rows * p.chunks;
-    p.sum_groups = n_seqs * ((p.tiles + 3) / 4);
+    // four tiles a workgroup until they are more than the GPU holds at once (8 for each CU): each decides anew
+    const int64_t whole = (p.tiles + 3) / 4, fill = n_seqs > 0 ? (2048 + n_seqs - 1) / n_seqs : 1;
+    p.sum_parts = (int)(whole < fill ? whole : fill);
+    p.sum_groups = n_seqs * p.sum_parts;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t from = at;

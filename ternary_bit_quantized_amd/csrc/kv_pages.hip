@@ -18,9 +18,13 @@ namespace q2_0 {
 // Counts change within a launch: read and changed past the vector caches.
 __device__ __forceinline__ int peek(const int32_t *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 __device__ __forceinline__ void put(int32_t *p, int v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+// Between two steps of one workgroup that change and read counts with the calls above: every one of them has reached the
+// memory that all of them meet in.  (A fence for the whole device would write caches back, several us each.)
 __device__ __forceinline__ void all_done() {
-    __threadfence();
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+    __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
 }
 
 __device__ __forceinline__ bool bad_len(int v, int64_t most) { return v < 0 || v > most; }
@@ -30,30 +34,29 @@ __device__ __forceinline__ int pages_of(const FastDiv &page, int n) { return n =
 
 constexpr int kVecs = 8;              // 16-byte vectors of a thread in a copy
 
-// Vectors [part * 2048, ..) of a page, rows [0, rows) of each head; all loads first.
+// Vectors [part * 2048, ..) of a page, rows [0, rows) of each head, rows >= 1.  All loads first and without branches:
+// a place past the end reads the last one that counts and is not written.
 __device__ __forceinline__ void copy_part(const PageRows &to, const PageRows &from, const PageShape &sh, int64_t dst, int64_t src,
                                           int part, int rows) {
     u32x4_t x[kVecs];
-    int64_t at[kVecs];
-    uint32_t live = 0, second = 0;
+    char *at[kVecs];
+    const int64_t to_page = dst * to.page_stride, from_page = src * from.page_stride;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
         const int v = part * 256 * kVecs + i * 256 + (int)threadIdx.x;
-        const int row = v >> sh.vec_shift;
+        const int u = v < sh.vecs ? v : sh.vecs - 1;
+        const int row = u >> sh.vec_shift;
         const int head = sh.page.div((uint32_t)row), token = row - head * (int)sh.page.d;   // heads of k, then of v
-        if (v >= sh.vecs || token >= rows) continue;
+        const int tk = token < rows ? token : rows - 1;
         const bool is_v = head >= sh.heads;
-        const int h = is_v ? head - sh.heads : head;
-        const int64_t b = (int64_t)(v & ((1 << sh.vec_shift) - 1)) * 16;
-        x[i] = *reinterpret_cast<const u32x4_t *>((is_v ? from.v : from.k) + src * from.page_stride + h * from.head_stride +
-                                                  token * from.token_stride + b);
-        at[i] = dst * to.page_stride + h * to.head_stride + token * to.token_stride + b;
-        live |= 1u << i;
-        second |= (uint32_t)is_v << i;
+        const int64_t h = is_v ? head - sh.heads : head, b = (int64_t)(u & ((1 << sh.vec_shift) - 1)) * 16;
+        x[i] = *reinterpret_cast<const u32x4_t *>((is_v ? from.v : from.k) + (from_page + h * from.head_stride + tk * from.token_stride + b));
+        at[i] = (is_v ? to.v : to.k) + (to_page + h * to.head_stride + tk * to.token_stride + b);
+        if (v >= sh.vecs || token >= rows) at[i] = nullptr;
     }
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
-        if (live >> i & 1) *reinterpret_cast<u32x4_t *>(((second >> i & 1) ? to.v : to.k) + at[i]) = x[i];
+        if (at[i]) *reinterpret_cast<u32x4_t *>(at[i]) = x[i];
 }
 
 static int parts_of(const PageShape &p) { return (p.vecs + 256 * kVecs - 1) / (256 * kVecs); }
@@ -180,6 +183,14 @@ __global__ __launch_bounds__(1024) void kv_plan(KvResize a) {
     __shared__ int64_t tmp[16];
     const int64_t most = (int64_t)a.t.cols * a.shape.page.d;
     const int tid = threadIdx.x;
+    // free pages, asked for first
+    const int words = (a.n_pages + 31) / 32;
+    int64_t some = 0;
+    for (int w = tid; w < words; w += 1024) {
+        uint32_t bits = a.free[w];
+        if (w == words - 1 && a.n_pages % 32) bits &= (1u << (a.n_pages % 32)) - 1u;
+        some += __popc(bits);
+    }
     Planned pl[PT];
     int len[PT], now[PT], count[PT], left[PT];
     bool grows[PT], shared[PT], keeps[PT];
@@ -202,33 +213,32 @@ __global__ __launch_bounds__(1024) void kv_plan(KvResize a) {
         }
         shared[i] = count[i] > 1;
     }
-    all_done();
+    bool any = false;
 #pragma unroll
-    for (int i = 0; i < PT; ++i)
-        if (shared[i]) atomicSub(a.ref + pl[i].old, 1);
-    all_done();
+    for (int i = 0; i < PT; ++i) left[i] = 1, keeps[i] = false, any |= shared[i];
+    if (__syncthreads_or(any)) {                                 // (most calls: nothing is shared)
+        // (the counts are read, above)
 #pragma unroll
-    for (int i = 0; i < PT; ++i) left[i] = shared[i] ? peek(a.ref + pl[i].old) : 1;
-    all_done();
+        for (int i = 0; i < PT; ++i)
+            if (shared[i]) atomicSub(a.ref + pl[i].old, 1);
+        all_done();
 #pragma unroll
-    for (int i = 0; i < PT; ++i)
-        if (left[i] == 0) atomicMin(a.ref + pl[i].old, tid * PT + i - a.t.n_seqs);
-    all_done();
+        for (int i = 0; i < PT; ++i)
+            if (shared[i]) left[i] = peek(a.ref + pl[i].old);
+        all_done();
+#pragma unroll
+        for (int i = 0; i < PT; ++i)
+            if (left[i] == 0) atomicMin(a.ref + pl[i].old, tid * PT + i - a.t.n_seqs);
+        all_done();
+#pragma unroll
+        for (int i = 0; i < PT; ++i) keeps[i] = left[i] == 0 && peek(a.ref + pl[i].old) == tid * PT + i - a.t.n_seqs;
+    }
     int64_t need = 0;
 #pragma unroll
-    for (int i = 0; i < PT; ++i) {
-        keeps[i] = left[i] == 0 && peek(a.ref + pl[i].old) == tid * PT + i - a.t.n_seqs;
-        need += pl[i].want - pl[i].have + (shared[i] && !keeps[i]);
-    }
+    for (int i = 0; i < PT; ++i) need += pl[i].want - pl[i].have + (shared[i] && !keeps[i]);
     int64_t total;
     int64_t slot = scan_1024(need, tmp, total);
-    const int words = (a.n_pages + 31) / 32;
-    int64_t some = 0, avail;
-    for (int w = tid; w < words; w += 1024) {
-        uint32_t bits = a.free[w];
-        if (w == words - 1 && a.n_pages % 32) bits &= (1u << (a.n_pages % 32)) - 1u;
-        some += __popc(bits);
-    }
+    int64_t avail;
     scan_1024(some, tmp, avail);
     const bool enough = total <= avail;
     if (tid == 0) *a.missing = enough ? 0 : (int)(total - avail < 0x7fffffff ? total - avail : 0x7fffffff);

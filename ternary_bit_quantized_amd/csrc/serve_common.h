@@ -23,7 +23,8 @@ hipError_t launch_moe_choose_groups(const ChooseGroups &a, Act xt, bool sigmoid,
 // ---- verification of drafted tokens
 struct DraftPlan {
     int64_t stat_groups;   // workgroups of the statistics (0: probabilities are given)
-    int64_t sum_groups;    // of the tile sums
+    int64_t sum_groups;    // of the tile sums, sum_parts of a sequence
+    int sum_parts;
     int chunks;            // of a row in the statistics
     int chunk_vecs;        // 16-byte vectors of a chunk
     int tiles;             // of a row in the tile sums
