@@ -22,33 +22,68 @@ constexpr int kMaxRows = 2 * Q2_0_DRAFT_MAX + 1;
 constexpr int kTile = 1024;
 constexpr int kPassVecs = 1024;       // 16-byte vectors of a workgroup's pass: 4 a thread
 
-// 2^y for y <= 0 (0 below -1100 and for NaN): 2^n 2^r with n = rint(y) from the low bits of y + 1.5 2^52 and
-// r in [-1/2, 1/2] by the polynomial of degree 9 that meets 2^r at the Chebyshev points (relative error 2e-14).
+// 2^r for r in [-1/2, 1/2]: the polynomial of degree 8 that meets it at the Chebyshev points (relative error 1.1e-12).
+__device__ __forceinline__ double exp2_frac(double r) {
+    double e = 1.3255224884799127e-06;
+    e = fma(e, r, 1.5310079402383103e-05);
+    e = fma(e, r, 0.00015403455852419016);
+    e = fma(e, r, 0.0013333450568000008);
+    e = fma(e, r, 0.00961812915940262);
+    e = fma(e, r, 0.05550410941205934);
+    e = fma(e, r, 0.2402265069581299);
+    e = fma(e, r, 0.6931471805459335);
+    return fma(e, r, 1.0);
+}
+
+constexpr double kBig = 6755399441055744.0;      // 1.5 2^52: x + kBig is x rounded to a whole number, in the low bits
+
+// 2^y for y <= 0, 0 below -1100 and for NaN.
 __device__ __forceinline__ double exp2_64(double y) {
     y = fmax(y, -1100.0);
-    const double big = 6755399441055744.0;
-    const double t = y + big;
-    const double r = y - (t - big);
-    double e = 1.020590550210069e-07;
-    e = fma(e, r, 1.3259645241948732e-06);
-    e = fma(e, r, 1.5252672924257465e-05);
-    e = fma(e, r, 0.0001540343375126647);
-    e = fma(e, r, 0.0013333558200796013);
-    e = fma(e, r, 0.00961812919393429);
-    e = fma(e, r, 0.05550410866465166);
-    e = fma(e, r, 0.2402265069564034);
-    e = fma(e, r, 0.6931471805599462);
-    e = fma(e, r, 1.0000000000000135);
-    return __builtin_amdgcn_ldexp(e, (int)(uint32_t)__builtin_bit_cast(uint64_t, t));
+    const double t = y + kBig;
+    return __builtin_amdgcn_ldexp(exp2_frac(y - (t - kBig)), (int)(uint32_t)__builtin_bit_cast(uint64_t, t));
 }
+
+// The exponentials of a row (or a part of one) of largest value m: 2^(k x - ref) with ref the whole number next to k m.  ref goes
+// into the exponent: with t = k x + (kBig - ref), one rounding to a whole number, q = t - (kBig - ref) and r = k x - q, a value
+// takes 13 64-bit instructions, and k x is not rounded before its whole part is gone.
+// Where k m is 2^40 and more, one float32 step from m is 2^16 in the exponent: only m itself counts, and x - m takes
+// the place of x (`off`; else 0) with ref 0.
+struct Exps {
+    double k, d, big;      // d = 1000 / k; big = kBig - ref
+    float m, off, low;     // values below `low`, 2^-1000 of the largest, count nothing
+    __device__ __forceinline__ void scale(double by) { k = by, d = 1000.0 / by; }
+    __device__ __forceinline__ void about(float top) {
+        const double mk = (double)top * k;
+        const bool whole = fabs(mk) < 0x1p40;
+        m = top;
+        off = whole ? 0.f : top;
+        big = kBig - (whole ? rint(mk) : 0.0);
+        low = (float)((whole ? (double)top : 0.0) - d);
+    }
+    // 2^(this one's ref - that one's), of a part with values to the whole: at most 1
+    __device__ __forceinline__ double share_of(const Exps &all) const {
+        return exp2_64(off == 0.f && all.off == 0.f ? all.big - big : ((double)m - (double)all.m) * k);
+    }
+    // for sums: 2^-1000 and less count as that
+    __device__ __forceinline__ double of(float x) const {
+        const double v = (double)fmaxf(x - off, low);
+        const double t = fma(v, k, big);
+        u32x2_t e = __builtin_bit_cast(u32x2_t, exp2_frac(fma(v, k, -(t - big))));
+        e.y += (uint32_t)__builtin_bit_cast(uint64_t, t) << 20;
+        return __builtin_bit_cast(double, e);
+    }
+    __device__ __forceinline__ double exact(float x) const { return x - off < low ? 0.0 : of(x); }
+};
 
 __device__ __forceinline__ double nan64() { return __builtin_nan(""); }
 
-// log2(e) / temperature; NaN for a temperature that is not positive
+// log2(e) / temperature; NaN for a temperature that is not positive.  Past 2^100 all that is not masked is alike, and a
+// mask still is one.
 __device__ __forceinline__ double scale_of(const DraftVerify &a, int s) {
     if (!a.temperature) return 1.4426950408889634074;
     const float t = a.temperature[s];
-    return t > 0.f ? 1.4426950408889634074 / (double)t : nan64();
+    return t > 0.f ? 1.4426950408889634074 / (double)fminf(t, 0x1p100f) : nan64();
 }
 
 __device__ __forceinline__ bool greedy_of(const DraftVerify &a, int s) { return a.temperature && a.temperature[s] == 0.f; }
@@ -82,21 +117,29 @@ __device__ __forceinline__ void unpack(u32x4_t v, Vec<bf16_t> &o) {
     }
 }
 
-// Vector w of a row whose first element is `shift` elements past a 16-byte boundary; what is outside
-// the row (or at w >= end) is -inf and not read.
+// A thread's four vectors of the pass that begins at vector v of a row whose first element is `shift` elements past a 16-byte
+// boundary; what is outside the row (or at `end` and after it) is -inf and not read.
 template <typename XT>
-__device__ __forceinline__ Vec<XT> load_vec(const XT *row, int shift, int n_vocab, int w, int end) {
+__device__ __forceinline__ void load_pass(const XT *row, int shift, int n_vocab, int v, int end, Vec<XT> (&x)[4]) {
     constexpr int VE = Vec<XT>::n;
-    Vec<XT> o;
-    const int e = w * VE - shift;
-    if (w < end && e >= 0 && e + VE <= n_vocab) {
-        unpack(*reinterpret_cast<const u32x4_t *>(row + e), o);
-    } else {
+    const int first = v * VE - shift;
+    if (first >= 0 && v + kPassVecs <= end && first + kPassVecs * VE <= n_vocab) {
 #pragma unroll
-        for (int i = 0; i < VE; ++i)
-            o.x[i] = w < end && e + i >= 0 && e + i < n_vocab ? act_to_f32(row[e + i]) : -__builtin_inff();
+        for (int i = 0; i < 4; ++i)
+            unpack(__builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(row + first + (i * 256 + (int)threadIdx.x) * VE)), x[i]);
+        return;
     }
-    return o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int w = v + i * 256 + (int)threadIdx.x, e = w * VE - shift;
+        if (w < end && e >= 0 && e + VE <= n_vocab) {
+            unpack(*reinterpret_cast<const u32x4_t *>(row + e), x[i]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VE; ++j)
+                x[i].x[j] = w < end && e + j >= 0 && e + j < n_vocab ? act_to_f32(row[e + j]) : -__builtin_inff();
+        }
+    }
 }
 
 template <typename XT>
@@ -116,22 +159,22 @@ __global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
     const int shift = (int)(((uintptr_t)row & 15) / sizeof(XT));
     const int nv = (a.n_vocab + shift + VE - 1) / VE;
     const int v0 = c * p.chunk_vecs, v1 = nv < v0 + p.chunk_vecs ? nv : v0 + p.chunk_vecs;
-    const double k = scale_of(a, s);
     float m = -__builtin_inff();
     double z = 0.0;
     int arg = 0x7fffffff;
     bool bad = false;
+    Exps ex;
+    ex.scale(scale_of(a, s));
     for (int v = v0; v < v1; v += kPassVecs) {
         Vec<XT> x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = load_vec(row, shift, a.n_vocab, v + i * 256 + (int)threadIdx.x, v1);
+        load_pass(row, shift, a.n_vocab, v, v1, x);
         float top = m;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                top = fmaxf(top, x[i].x[e]);
-                bad |= x[i].x[e] != x[i].x[e];
+            for (int e = 0; e < VE; e += 2) {
+                top = fmaxf(fmaxf(x[i].x[e], x[i].x[e + 1]), top);
+                bad |= __builtin_isunordered(x[i].x[e], x[i].x[e + 1]);
             }
         if (greedy) {
             if (top > m) {
@@ -142,16 +185,19 @@ __global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
                     for (int e = VE - 1; e >= 0; --e)
                         if (x[i].x[e] == top) arg = (v + i * 256 + (int)threadIdx.x) * VE - shift + e;
             }
-        } else {
-            if (top > m) {
-                z *= exp2_64(((double)m - (double)top) * k);
-                m = top;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < VE; ++e) z += exp2_64(((double)x[i].x[e] - (double)m) * k);
+            continue;
         }
+        if (top > m) {
+            const Exps before = ex;
+            ex.about(top);
+            z = m == -__builtin_inff() ? 0.0 : z * before.share_of(ex);
+            m = top;
+        }
+        if (m == -__builtin_inff()) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) z += ex.of(x[i].x[e]);
     }
     __shared__ float wm[4];
     __shared__ double wz[4];
@@ -172,7 +218,9 @@ __global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
         }
         if (lane == 0) warg[wave] = at;
     } else {
-        z *= exp2_64(((double)m - (double)top) * k);
+        const Exps mine = ex;
+        ex.about(top);
+        z = m == -__builtin_inff() ? 0.0 : z * mine.share_of(ex);
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) z += __shfl_xor(z, off);
     }
@@ -181,8 +229,8 @@ __global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
     __syncthreads();
     if (threadIdx.x == 0) {
         const bool none = wbad[0] | wbad[1] | wbad[2] | wbad[3] || top == __builtin_inff();
-        reinterpret_cast<double *>(a.ws + p.off_z)[blockIdx.x] =
-            none ? nan64() : greedy ? 1.0 : ((wz[0] + wz[1]) + wz[2]) + wz[3];
+        const double sum = greedy ? 1.0 : ((wz[0] + wz[1]) + wz[2]) + wz[3];
+        reinterpret_cast<double *>(a.ws + p.off_z)[blockIdx.x] = none ? nan64() : top == -__builtin_inff() ? 0.0 : sum;
         reinterpret_cast<float *>(a.ws + p.off_max)[blockIdx.x] = top;
         if (greedy) {
             int at = 0x7fffffff;
@@ -194,7 +242,8 @@ __global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
 
 // What decides a sequence's next token.
 struct Pick {
-    double k, m_p, inv_p, m_q, inv_q;     // p(x) = 2^(k (x - m)) inv
+    Exps p, q;
+    double inv_p, inv_q;                  // p(x) = p.exact(x) inv_p
     int64_t row_p, row_q;                 // rows of target and draft
     int taken;                            // drafts taken; < 0: the sequence is left out
     int kind;                             // kFixed: `token`; else what is taken from p
@@ -203,8 +252,8 @@ struct Pick {
 enum { kFixed = 0, kPlain = 1, kOneHot = 2, kMinus = 3 };
 
 template <bool PROBS>
-__device__ __forceinline__ double prob(float x, double k, double m, double inv) {
-    return PROBS ? (double)x : exp2_64(((double)x - m) * k) * inv;
+__device__ __forceinline__ double prob(float x, const Exps &e, double inv) {
+    return PROBS ? (double)x : e.exact(x) * inv;
 }
 
 __device__ __forceinline__ double wave_sum(double v) {
@@ -216,7 +265,8 @@ __device__ __forceinline__ double wave_sum(double v) {
 // All threads of the workgroup; the result is in `pick` after a barrier.
 template <typename XT, bool PROBS>
 __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pick) {
-    __shared__ double most[kMaxRows], inv[kMaxRows];
+    __shared__ Exps most[kMaxRows];
+    __shared__ double inv[kMaxRows];
     __shared__ int arg[kMaxRows];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int nd = a.n_draft[s], per = a.max_draft + 1;
@@ -253,9 +303,13 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
             for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
             double sum = 0.0;
             int best = 0x7fffffff;
+            Exps all, part;
+            all.scale(k), part.scale(k);
+            all.about(top);
             for (int c = lane; c < p.chunks; c += 64) {
                 // (a chunk of NaN: its sum is NaN and stays so)
-                sum += greedy ? z[c] : z[c] * exp2_64(((double)m[c] - (double)top) * k);
+                part.about(m[c]);
+                sum += greedy || m[c] == -__builtin_inff() ? z[c] : z[c] * part.share_of(all);
                 if (greedy && m[c] == top) best = at[c] < best ? at[c] : best;
             }
             sum = wave_sum(sum);
@@ -267,7 +321,7 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
                 }
             }
             if (lane == 0) {
-                most[r] = top;
+                most[r] = all;
                 inv[r] = sum > 0.0 && sum < __builtin_inf() ? 1.0 / sum : nan64();
                 arg[r] = sum == sum && top > -__builtin_inff() ? best : -1;
             }
@@ -280,8 +334,8 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
         if (greedy) {
             yes = arg[lane] == tok;
         } else {
-            const double pt = prob<PROBS>(xt, k, PROBS ? 0.0 : most[lane], PROBS ? 0.0 : inv[lane]);
-            const double qt = !a.draft ? 1.0 : prob<PROBS>(xd, k, PROBS ? 0.0 : most[nd + 1 + lane], PROBS ? 0.0 : inv[nd + 1 + lane]);
+            const double pt = prob<PROBS>(xt, most[lane], inv[lane]);
+            const double qt = !a.draft ? 1.0 : prob<PROBS>(xd, most[nd + 1 + lane], inv[nd + 1 + lane]);
             yes = (double)u * qt < pt;
         }
     }
@@ -290,12 +344,11 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
     const int t = __builtin_amdgcn_readlane(tok, j);
     if (lane == 0) {
         pick.taken = j;
-        pick.k = k;
         pick.row_p = (int64_t)s * per + j;
         pick.row_q = (int64_t)s * a.max_draft + j;
         if (!PROBS) {
-            pick.m_p = most[j], pick.inv_p = inv[j];
-            if (j < nd && a.draft && !greedy) pick.m_q = most[nd + 1 + j], pick.inv_q = inv[nd + 1 + j];
+            pick.p = most[j], pick.inv_p = inv[j];
+            if (j < nd && a.draft && !greedy) pick.q = most[nd + 1 + j], pick.inv_q = inv[nd + 1 + j];
         }
         if (greedy) pick.kind = kFixed, pick.token = arg[j];
         else if (j == nd) pick.kind = kPlain, pick.token = -1;
@@ -326,8 +379,8 @@ __device__ __forceinline__ void weights(const DraftVerify &a, const Pick &pick, 
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int at = e + i * step;
-        double v = prob<PROBS>(x[i], pick.k, pick.m_p, pick.inv_p);
-        if (kind == kMinus) v -= prob<PROBS>(y[i], pick.k, pick.m_q, pick.inv_q);
+        double v = prob<PROBS>(x[i], pick.p, pick.inv_p);
+        if (kind == kMinus) v -= prob<PROBS>(y[i], pick.q, pick.inv_q);
         const bool out = at >= a.n_vocab || (kind == kOneHot && at == pick.token);
         w[i] = out || v <= 0.0 ? 0.0 : v;
     }
@@ -343,7 +396,7 @@ __device__ __forceinline__ double tile_sum(const DraftVerify &a, const Pick &pic
 }
 
 template <typename XT, bool PROBS>
-__global__ __launch_bounds__(256) void draft_sums(DraftVerify a, DraftPlan p) {
+__global__ __launch_bounds__(256, 5) void draft_sums(DraftVerify a, DraftPlan p) {
     const int s = (int)(blockIdx.x / (unsigned)p.sum_parts), g = (int)(blockIdx.x % (unsigned)p.sum_parts);
     __shared__ Pick pick;
     decide<XT, PROBS>(a, p, s, pick);
@@ -470,13 +523,13 @@ DraftPlan draft_plan(int64_t n_seqs, int64_t max_draft, int64_t n_vocab, bool ha
     const int64_t ve = 16 / elem_bytes, vecs = (n_vocab + 2 * ve - 2) / ve;      // of the worst alignment
     // one pass a workgroup until there are some 16 workgroups for each of the 256 CUs, then longer chunks
     int64_t passes = (vecs + kPassVecs - 1) / kPassVecs, per = 1;
-    while (per < 8 && rows * ((passes + per - 1) / per) > 4096) per *= 2;
+    while (per < 8 && rows * ((passes + per - 1) / per) > 6000) per *= 2;
     p.chunk_vecs = (int)(per * kPassVecs);
     p.chunks = (int)((passes + per - 1) / per);
     p.tiles = (int)((n_vocab + kTile - 1) / kTile);
     p.stat_groups = rows * p.chunks;
-    // four tiles a workgroup until they are more than the GPU holds at once (8 for each CU): each decides anew
-    const int64_t whole = (p.tiles + 3) / 4, fill = n_seqs > 0 ? (2048 + n_seqs - 1) / n_seqs : 1;
+    // four tiles a workgroup until they are more than the GPU holds at once (5 for each CU): each decides anew
+    const int64_t whole = (p.tiles + 3) / 4, fill = n_seqs > 0 ? (1280 + n_seqs - 1) / n_seqs : 1;
     p.sum_parts = (int)(whole < fill ? whole : fill);
     p.sum_groups = n_seqs * p.sum_parts;
     size_t at = 0;
