@@ -49,9 +49,25 @@ __device__ __forceinline__ double exp2_64(double y) {
 // takes 13 64-bit instructions, and k x is not rounded before its whole part is gone.
 // Where k m is 2^40 and more, one float32 step from m is 2^16 in the exponent: only m itself counts, and x - m takes
 // the place of x (`off`; else 0) with ref 0.
-struct Exps {
-    double k, d, big;      // d = 1000 / k; big = kBig - ref
-    float m, off, low;     // values below `low`, 2^-1000 of the largest, count nothing
+struct RowExps {
+    double big;            // kBig - ref
+    float off, low;        // values below `low`, 2^-1000 of the largest, count nothing
+    // for sums: 2^-1000 and less count as that
+    __device__ __forceinline__ double of(float x, double k) const {
+        const double v = (double)fmaxf(x - off, low);
+        const double t = fma(v, k, big);
+        u32x2_t e = __builtin_bit_cast(u32x2_t, exp2_frac(fma(v, k, -(t - big))));
+        e.y += (uint32_t)__builtin_bit_cast(uint64_t, t) << 20;
+        return __builtin_bit_cast(double, e);
+    }
+    __device__ __forceinline__ double exact(float x, double k) const {
+        const double v = of(x, k);
+        return x - off < low ? 0.0 : v;
+    }
+};
+struct Exps : RowExps {
+    double k, d;           // d = 1000 / k
+    float m;
     __device__ __forceinline__ void scale(double by) { k = by, d = 1000.0 / by; }
     __device__ __forceinline__ void about(float top) {
         const double mk = (double)top * k;
@@ -65,15 +81,6 @@ struct Exps {
     __device__ __forceinline__ double share_of(const Exps &all) const {
         return exp2_64(off == 0.f && all.off == 0.f ? all.big - big : ((double)m - (double)all.m) * k);
     }
-    // for sums: 2^-1000 and less count as that
-    __device__ __forceinline__ double of(float x) const {
-        const double v = (double)fmaxf(x - off, low);
-        const double t = fma(v, k, big);
-        u32x2_t e = __builtin_bit_cast(u32x2_t, exp2_frac(fma(v, k, -(t - big))));
-        e.y += (uint32_t)__builtin_bit_cast(uint64_t, t) << 20;
-        return __builtin_bit_cast(double, e);
-    }
-    __device__ __forceinline__ double exact(float x) const { return x - off < low ? 0.0 : of(x); }
 };
 
 __device__ __forceinline__ double nan64() { return __builtin_nan(""); }
@@ -197,7 +204,7 @@ __global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < VE; ++e) z += ex.of(x[i].x[e]);
+            for (int e = 0; e < VE; ++e) z += ex.of(x[i].x[e], ex.k);
     }
     __shared__ float wm[4];
     __shared__ double wz[4];
@@ -242,8 +249,8 @@ __global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
 
 // What decides a sequence's next token.
 struct Pick {
-    Exps p, q;
-    double inv_p, inv_q;                  // p(x) = p.exact(x) inv_p
+    RowExps p, q;
+    double k, inv_p, inv_q;               // p(x) = p.exact(x, k) inv_p
     int64_t row_p, row_q;                 // rows of target and draft
     int taken;                            // drafts taken; < 0: the sequence is left out
     int kind;                             // kFixed: `token`; else what is taken from p
@@ -252,8 +259,8 @@ struct Pick {
 enum { kFixed = 0, kPlain = 1, kOneHot = 2, kMinus = 3 };
 
 template <bool PROBS>
-__device__ __forceinline__ double prob(float x, const Exps &e, double inv) {
-    return PROBS ? (double)x : e.exact(x) * inv;
+__device__ __forceinline__ double prob(float x, const RowExps &e, double k, double inv) {
+    return PROBS ? (double)x : e.exact(x, k) * inv;
 }
 
 __device__ __forceinline__ double wave_sum(double v) {
@@ -265,7 +272,7 @@ __device__ __forceinline__ double wave_sum(double v) {
 // All threads of the workgroup; the result is in `pick` after a barrier.
 template <typename XT, bool PROBS>
 __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pick) {
-    __shared__ Exps most[kMaxRows];
+    __shared__ RowExps most[kMaxRows];
     __shared__ double inv[kMaxRows];
     __shared__ int arg[kMaxRows];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -334,8 +341,8 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
         if (greedy) {
             yes = arg[lane] == tok;
         } else {
-            const double pt = prob<PROBS>(xt, most[lane], inv[lane]);
-            const double qt = !a.draft ? 1.0 : prob<PROBS>(xd, most[nd + 1 + lane], inv[nd + 1 + lane]);
+            const double pt = prob<PROBS>(xt, most[lane], k, inv[lane]);
+            const double qt = !a.draft ? 1.0 : prob<PROBS>(xd, most[nd + 1 + lane], k, inv[nd + 1 + lane]);
             yes = (double)u * qt < pt;
         }
     }
@@ -344,6 +351,7 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
     const int t = __builtin_amdgcn_readlane(tok, j);
     if (lane == 0) {
         pick.taken = j;
+        pick.k = k;
         pick.row_p = (int64_t)s * per + j;
         pick.row_q = (int64_t)s * a.max_draft + j;
         if (!PROBS) {
@@ -357,41 +365,67 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
     }
 }
 
-// What is left for N tokens from e on, `step` apart: not below zero, NaN where either is.  Loads first and without
-// branches (a place past the row reads its last token and counts nothing): with a branch around each they wait for one another.
-template <int N, typename XT, bool PROBS>
-__device__ __forceinline__ void weights(const DraftVerify &a, const Pick &pick, int kind, int e, int step, double (&w)[N]) {
-    const XT *t = static_cast<const XT *>(a.target) + pick.row_p * a.ld_target;
+// The same values in scalar registers: a Pick comes from shared or global memory, the same for all lanes.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ float uniform(float v) { return __builtin_bit_cast(float, uniform(__builtin_bit_cast(int, v))); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
+__device__ __forceinline__ double uniform(double v) { return __builtin_bit_cast(double, uniform(__builtin_bit_cast(int64_t, v))); }
+__device__ __forceinline__ RowExps uniform(const RowExps &e) { return RowExps{uniform(e.big), uniform(e.off), uniform(e.low)}; }
+__device__ __forceinline__ Pick uniform(const Pick &v) {
+    return Pick{uniform(v.p), uniform(v.q), uniform(v.k), uniform(v.inv_p), uniform(v.inv_q), uniform(v.row_p), uniform(v.row_q),
+                uniform(v.taken), uniform(v.kind), uniform(v.token)};
+}
+
+// The values of N tokens from e on, `step` apart, for what is left of them.  Without branches (a place past the row
+// reads its last token): with a branch around each the loads wait for one another.
+template <int N, typename XT>
+struct Tokens {
     float x[N], y[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int at = e + i * step;
-        x[i] = act_to_f32(t[at < a.n_vocab ? at : a.n_vocab - 1]);
-    }
-    if (kind == kMinus) {
-        const XT *d = static_cast<const XT *>(a.draft) + pick.row_q * a.ld_draft;
+    __device__ __forceinline__ void load(const DraftVerify &a, const Pick &pick, int kind, int e, int step) {
+        const XT *t = static_cast<const XT *>(a.target) + pick.row_p * a.ld_target;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int at = e + i * step;
-            y[i] = act_to_f32(d[at < a.n_vocab ? at : a.n_vocab - 1]);
+            x[i] = act_to_f32(t[at < a.n_vocab ? at : a.n_vocab - 1]);
+        }
+        if (kind == kMinus) {
+            const XT *d = static_cast<const XT *>(a.draft) + pick.row_q * a.ld_draft;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int at = e + i * step;
+                y[i] = act_to_f32(d[at < a.n_vocab ? at : a.n_vocab - 1]);
+            }
         }
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int at = e + i * step;
-        double v = prob<PROBS>(x[i], pick.p, pick.inv_p);
-        if (kind == kMinus) v -= prob<PROBS>(y[i], pick.q, pick.inv_q);
+    // token `at`, the i-th: not below zero, NaN where either is
+    template <bool PROBS>
+    __device__ __forceinline__ double left(const DraftVerify &a, const Pick &pick, int kind, int i, int at) const {
+        double v = prob<PROBS>(x[i], pick.p, pick.k, pick.inv_p);
+        if (kind == kMinus) v -= prob<PROBS>(y[i], pick.q, pick.k, pick.inv_q);
         const bool out = at >= a.n_vocab || (kind == kOneHot && at == pick.token);
-        w[i] = out || v <= 0.0 ? 0.0 : v;
+        return out || v <= 0.0 ? 0.0 : v;
     }
-}
+};
 
 template <typename XT, bool PROBS>
 __device__ __forceinline__ double tile_sum(const DraftVerify &a, const Pick &pick, int kind, int tile) {
-    double w[kTile / 64], sum = 0.0;
-    weights<kTile / 64, XT, PROBS>(a, pick, kind, tile * kTile + (int)(threadIdx.x & 63), 64, w);
+    constexpr int N = kTile / 64;
+    const int e = tile * kTile + (int)(threadIdx.x & 63);
+    Tokens<N, XT> t;
+    t.load(a, pick, kind, e, 64);
+    double sum = 0.0;
+    if (kind == kMinus) {
 #pragma unroll
-    for (int i = 0; i < kTile / 64; ++i) sum += w[i];
+        for (int i = 0; i < N; ++i) {
+            sum += t.template left<PROBS>(a, pick, kMinus, i, e + 64 * i);
+            __builtin_amdgcn_sched_barrier(0);           // (side by side they take registers, and waves, away)
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) sum += t.template left<PROBS>(a, pick, kind == kOneHot ? kOneHot : kPlain, i, e + 64 * i);
+    }
     return wave_sum(sum);
 }
 
@@ -403,7 +437,7 @@ __global__ __launch_bounds__(256, 5) void draft_sums(DraftVerify a, DraftPlan p)
     __syncthreads();
     if (g == 0 && threadIdx.x == 0) reinterpret_cast<Pick *>(a.ws + p.off_pick)[s] = pick;
     if (pick.kind == kFixed) return;
-    const Pick mine = pick;
+    const Pick mine = uniform(pick);
     for (int tile = g * 4 + (int)(threadIdx.x >> 6); tile < p.tiles; tile += p.sum_parts * 4) {
         const double sum = tile_sum<XT, PROBS>(a, mine, mine.kind, tile);
         if ((threadIdx.x & 63) == 0) reinterpret_cast<double *>(a.ws + p.off_tiles)[(int64_t)s * p.tiles + tile] = sum;
@@ -450,7 +484,7 @@ __global__ __launch_bounds__(256) void draft_pick(DraftVerify a, DraftPlan p) {
     __shared__ double wave_sums[4], before;
     __shared__ int hits[8], found;
     double *tiles = reinterpret_cast<double *>(a.ws + p.off_tiles) + (int64_t)s * p.tiles;
-    const Pick pick = reinterpret_cast<const Pick *>(a.ws + p.off_pick)[s];
+    const Pick pick = uniform(reinterpret_cast<const Pick *>(a.ws + p.off_pick)[s]);
     const float u = a.u[(int64_t)s * (a.max_draft + 1) + a.max_draft];
     int kind = pick.kind, result = pick.token;
     const int each = (p.tiles + 255) / 256, t0 = tid * each, t1 = t0 + each < p.tiles ? t0 + each : p.tiles;
@@ -488,8 +522,11 @@ __global__ __launch_bounds__(256) void draft_pick(DraftVerify a, DraftPlan p) {
             __syncthreads();
             const int e = found * kTile + tid * 4;
             const double base = before;
+            Tokens<4, XT> t;
+            t.load(a, pick, kind, e, 1);
             double w[4];
-            weights<4, XT, PROBS>(a, pick, kind, e, 1, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = t.template left<PROBS>(a, pick, kind, i, e + i);
             own = ((w[0] + w[1]) + w[2]) + w[3];
             run = base + run_256(own, wave_sums, total);
             if (tid == thread_at(run, own, r, hits)) {
