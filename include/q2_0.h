@@ -561,7 +561,8 @@ typedef enum {
  *            NULL: the drafts were not drawn but found (in the text so far): probability 1 of the drafted token.
  *   form   : a q2_0_draft_form, for both.
  *   temperature : DEVICE f32 [n_seqs], for both models, or NULL (1).  0: the largest logit takes all (the
- *            lowest index among equals).  Logits only (UNSUPPORTED with probabilities).
+ *            lowest index among equals).  Others count as at least 2^-100 and at most 2^100.  Logits only
+ *            (UNSUPPORTED with probabilities).
  *   tokens : DEVICE int32 [n_seqs][max_draft].  One outside [0, n_vocab) is not taken.
  *   n_draft: DEVICE int32 [n_seqs]: drafted tokens of the sequence, 0 .. max_draft.  Any other value leaves the
  *            sequence out (mark padding with -1): n_accepted 0, its out all -1, nothing of its rows is read.

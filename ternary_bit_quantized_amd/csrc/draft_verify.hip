@@ -10,16 +10,16 @@
 //   draft_stats  one pass over every row that may be needed: maximum and sum of exponentials of each chunk
 //                (a running maximum in registers, rescaled where a pass raises it)
 //   draft_sums   each workgroup joins its sequence's chunks, decides how many drafts are taken, and sums
-//                max(p - q, 0) of the deciding row over tiles of 1024 tokens
-//   draft_pick   one workgroup a sequence: the tile, then the token, at which the running sum passes the number
+//                max(p - q, 0) of the deciding row over tiles of 512 tokens; the last workgroup of a sequence finds the tile, then the token, at which
+//                the running sum passes the number
 //
-// Given probabilities need no statistics.  Fixed order of all sums: results are the same in every run.
+// Given probabilities need no statistics, and find the token in a launch of its own (draft_pick).  Fixed order of all sums: results are the same in every run.
 #include "serve_common.h"
 
 namespace q2_0 {
 
 constexpr int kMaxRows = 2 * Q2_0_DRAFT_MAX + 1;
-constexpr int kTile = 1024;
+constexpr int kTile = 512;
 constexpr int kPassVecs = 1024;       // 16-byte vectors of a workgroup's pass: 4 a thread
 
 // 2^r for r in [-1/2, 1/2]: the polynomial of degree 8 that meets it at the Chebyshev points (relative error 1.1e-12).
@@ -47,8 +47,9 @@ __device__ __forceinline__ double exp2_64(double y) {
 // The exponentials of a row (or a part of one) of largest value m: 2^(k x - ref) with ref the whole number next to k m.  ref goes
 // into the exponent: with t = k x + (kBig - ref), one rounding to a whole number, q = t - (kBig - ref) and r = k x - q, a value
 // takes 13 64-bit instructions, and k x is not rounded before its whole part is gone.
-// Where k m is 2^40 and more, one float32 step from m is 2^16 in the exponent: only m itself counts, and x - m takes
-// the place of x (`off`; else 0) with ref 0.
+// Where k m is 2^28 and more, float32 has no value 1000 below m in the exponent to stop at (`low` is off by 16 there): x - m takes
+// the place of x (`off`; else 0) with ref 0.  The difference is exact in float32 for x within a factor of 2 of m, and the
+// others are 2^-2^27 and less.
 struct RowExps {
     double big;            // kBig - ref
     float off, low;        // values below `low`, 2^-1000 of the largest, count nothing
@@ -66,16 +67,16 @@ struct RowExps {
     }
 };
 struct Exps : RowExps {
-    double k, d;           // d = 1000 / k
-    float m;
-    __device__ __forceinline__ void scale(double by) { k = by, d = 1000.0 / by; }
+    double k;
+    float m, d;            // d: 1000 / k
+    __device__ __forceinline__ void scale(double by) { k = by, d = 1000.f / (float)by; }
     __device__ __forceinline__ void about(float top) {
         const double mk = (double)top * k;
-        const bool whole = fabs(mk) < 0x1p40;
+        const bool whole = fabs(mk) < 0x1p28;
         m = top;
         off = whole ? 0.f : top;
         big = kBig - (whole ? rint(mk) : 0.0);
-        low = (float)((whole ? (double)top : 0.0) - d);
+        low = (whole ? top : 0.f) - d;
     }
     // 2^(this one's ref - that one's), of a part with values to the whole: at most 1
     __device__ __forceinline__ double share_of(const Exps &all) const {
@@ -85,12 +86,12 @@ struct Exps : RowExps {
 
 __device__ __forceinline__ double nan64() { return __builtin_nan(""); }
 
-// log2(e) / temperature; NaN for a temperature that is not positive.  Past 2^100 all that is not masked is alike, and a
-// mask still is one.
+// log2(e) / temperature, which counts as at most 2^100 and at least 2^-100 (logits would be out of all proportion to it); NaN
+// for one that is not positive.
 __device__ __forceinline__ double scale_of(const DraftVerify &a, int s) {
     if (!a.temperature) return 1.4426950408889634074;
     const float t = a.temperature[s];
-    return t > 0.f ? 1.4426950408889634074 / (double)fminf(t, 0x1p100f) : nan64();
+    return t > 0.f ? 1.4426950408889634074 / (double)fmaxf(fminf(t, 0x1p100f), 0x1p-100f) : nan64();
 }
 
 __device__ __forceinline__ bool greedy_of(const DraftVerify &a, int s) { return a.temperature && a.temperature[s] == 0.f; }
@@ -156,6 +157,7 @@ __global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
     const bool is_draft = b >= n_target;
     const int s = is_draft ? (b - n_target) / a.max_draft : b / per;
     const int j = is_draft ? (b - n_target) % a.max_draft : b % per;
+    if (!is_draft && j == 0 && c == 0 && threadIdx.x == 0) reinterpret_cast<int *>(a.ws + p.off_done)[s] = 0;
     const int nd = a.n_draft[s];
     if (nd < 0 || nd > a.max_draft || j >= nd + (is_draft ? 0 : 1)) return;
     const bool greedy = greedy_of(a, s);
@@ -283,6 +285,9 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
     }
     const bool greedy = !PROBS && greedy_of(a, s);
     const double k = PROBS ? 0.0 : scale_of(a, s);
+    const double *all_z = reinterpret_cast<const double *>(a.ws + p.off_z);
+    const float *all_m = reinterpret_cast<const float *>(a.ws + p.off_max);
+    const int *all_at = reinterpret_cast<const int *>(a.ws + p.off_arg);
     // the drafted tokens' values are asked for first: they arrive while the rows are joined
     int tok = -1;
     bool known = false;
@@ -298,40 +303,77 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
         }
     }
     if (!PROBS) {
+        // four rows of a wave side by side: loads, maxima and sums of one wait for memory and for each other
         const int rows = nd + 1 + (a.draft && !greedy ? nd : 0);
-        for (int r = wave; r < rows; r += 4) {
-            const int64_t b = r <= nd ? (int64_t)s * per + r : (int64_t)a.n_seqs * per + (int64_t)s * a.max_draft + (r - nd - 1);
-            const double *z = reinterpret_cast<const double *>(a.ws + p.off_z) + b * p.chunks;
-            const float *m = reinterpret_cast<const float *>(a.ws + p.off_max) + b * p.chunks;
-            const int *at = reinterpret_cast<const int *>(a.ws + p.off_arg) + b * p.chunks;
-            float top = -__builtin_inff();
-            for (int c = lane; c < p.chunks; c += 64) top = fmaxf(top, m[c]);
+        for (int r0 = wave; r0 < rows; r0 += 16) {
+            int64_t b[4];
+            float m[4], top[4];
+            double z[4];
+            int at[4];
 #pragma unroll
-            for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-            double sum = 0.0;
-            int best = 0x7fffffff;
-            Exps all, part;
-            all.scale(k), part.scale(k);
-            all.about(top);
-            for (int c = lane; c < p.chunks; c += 64) {
-                // (a chunk of NaN: its sum is NaN and stays so)
-                part.about(m[c]);
-                sum += greedy || m[c] == -__builtin_inff() ? z[c] : z[c] * part.share_of(all);
-                if (greedy && m[c] == top) best = at[c] < best ? at[c] : best;
+            for (int i = 0; i < 4; ++i) {
+                const int r = r0 + 4 * i < rows ? r0 + 4 * i : r0;
+                b[i] = (r <= nd ? (int64_t)s * per + r : (int64_t)a.n_seqs * per + (int64_t)s * a.max_draft + (r - nd - 1)) * p.chunks;
+                const int64_t c = b[i] + (lane < p.chunks ? lane : 0);
+                m[i] = lane < p.chunks ? all_m[c] : -__builtin_inff();
+                z[i] = lane < p.chunks ? all_z[c] : 0.0;
+                at[i] = greedy && lane < p.chunks ? all_at[c] : 0x7fffffff;
             }
-            sum = wave_sum(sum);
-            if (greedy) {
+            Exps part, all;
+            part.scale(k), all.scale(k);
 #pragma unroll
-                for (int off = 32; off >= 1; off >>= 1) {
-                    const int o = __shfl_xor(best, off);
-                    best = o < best ? o : best;
+            for (int i = 0; i < 4; ++i) {
+                for (int c = lane + 64; c < p.chunks; c += 64) {         // (rows of over 64 chunks)
+                    const float om = all_m[b[i] + c];
+                    const double oz = all_z[b[i] + c];
+                    if (greedy) {
+                        z[i] += oz;
+                        if (om > m[i]) at[i] = all_at[b[i] + c];         // (chunks of a lane go up: the first of equals stays)
+                        m[i] = fmaxf(m[i], om);
+                    } else {
+                        const float most = fmaxf(m[i], om);
+                        all.about(most);
+                        part.about(m[i]);
+                        if (m[i] > -__builtin_inff()) z[i] *= part.share_of(all);
+                        part.about(om);
+                        z[i] += om > -__builtin_inff() ? oz * part.share_of(all) : oz;
+                        m[i] = most;
+                    }
                 }
+                top[i] = m[i];
             }
-            if (lane == 0) {
-                most[r] = all;
-                inv[r] = sum > 0.0 && sum < __builtin_inf() ? 1.0 / sum : nan64();
-                arg[r] = sum == sum && top > -__builtin_inff() ? best : -1;
+#pragma unroll
+            for (int off = 32; off >= 1; off >>= 1)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], __shfl_xor(top[i], off));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                all.about(top[i]);
+                part.about(m[i]);
+                // (a chunk of NaN: its sum is NaN and stays so)
+                if (!greedy && m[i] > -__builtin_inff()) z[i] *= part.share_of(all);
+                at[i] = m[i] == top[i] ? at[i] : 0x7fffffff;
             }
+#pragma unroll
+            for (int off = 32; off >= 1; off >>= 1)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] += __shfl_xor(z[i], off);
+            if (greedy)
+#pragma unroll
+                for (int off = 32; off >= 1; off >>= 1)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int o = __shfl_xor(at[i], off);
+                        at[i] = o < at[i] ? o : at[i];
+                    }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (lane == 0 && r0 + 4 * i < rows) {
+                    all.about(top[i]);
+                    most[r0 + 4 * i] = all;
+                    inv[r0 + 4 * i] = z[i] > 0.0 && z[i] < __builtin_inf() ? 1.0 / z[i] : nan64();
+                    arg[r0 + 4 * i] = z[i] == z[i] && top[i] > -__builtin_inff() ? at[i] : -1;
+                }
         }
         __syncthreads();
     }
@@ -429,19 +471,21 @@ __device__ __forceinline__ double tile_sum(const DraftVerify &a, const Pick &pic
     return wave_sum(sum);
 }
 
-template <typename XT, bool PROBS>
-__global__ __launch_bounds__(256, 5) void draft_sums(DraftVerify a, DraftPlan p) {
-    const int s = (int)(blockIdx.x / (unsigned)p.sum_parts), g = (int)(blockIdx.x % (unsigned)p.sum_parts);
-    __shared__ Pick pick;
-    decide<XT, PROBS>(a, p, s, pick);
+// Tile sums go from the workgroups that make them to the one that reads them by atomics of the whole device alone, which meet
+// in one memory whatever the dies' caches hold.  A fence for the device instead would write back and drop a cache for
+// every workgroup: 1280 of them took 155 us in place of 25.
+__device__ __forceinline__ void put_sum(double *p, double v) {
+    __hip_atomic_exchange(reinterpret_cast<uint64_t *>(p), __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ double sum_of(const double *p) {
+    return __builtin_bit_cast(double, __hip_atomic_load(reinterpret_cast<const uint64_t *>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+}
+// All threads: the workgroup's atomics have been performed.
+__device__ __forceinline__ void sums_done() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+    __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    if (g == 0 && threadIdx.x == 0) reinterpret_cast<Pick *>(a.ws + p.off_pick)[s] = pick;
-    if (pick.kind == kFixed) return;
-    const Pick mine = uniform(pick);
-    for (int tile = g * 4 + (int)(threadIdx.x >> 6); tile < p.tiles; tile += p.sum_parts * 4) {
-        const double sum = tile_sum<XT, PROBS>(a, mine, mine.kind, tile);
-        if ((threadIdx.x & 63) == 0) reinterpret_cast<double *>(a.ws + p.off_tiles)[(int64_t)s * p.tiles + tile] = sum;
-    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
 }
 
 // Running sums over the 256 threads in their order: the sum up to the thread itself; `total`: all.
@@ -478,13 +522,13 @@ __device__ __forceinline__ int thread_at(double run, double own, double r, int *
     return who;
 }
 
+// The token that follows, and all of a sequence's results: one workgroup, after all tile sums.
 template <typename XT, bool PROBS>
-__global__ __launch_bounds__(256) void draft_pick(DraftVerify a, DraftPlan p) {
-    const int s = blockIdx.x, tid = threadIdx.x, wave = tid >> 6;
+__device__ __forceinline__ void pick_token(const DraftVerify &a, const DraftPlan &p, int s, const Pick &pick) {
+    const int tid = threadIdx.x, wave = tid >> 6;
     __shared__ double wave_sums[4], before;
     __shared__ int hits[8], found;
     double *tiles = reinterpret_cast<double *>(a.ws + p.off_tiles) + (int64_t)s * p.tiles;
-    const Pick pick = uniform(reinterpret_cast<const Pick *>(a.ws + p.off_pick)[s]);
     const float u = a.u[(int64_t)s * (a.max_draft + 1) + a.max_draft];
     int kind = pick.kind, result = pick.token;
     const int each = (p.tiles + 255) / 256, t0 = tid * each, t1 = t0 + each < p.tiles ? t0 + each : p.tiles;
@@ -492,7 +536,7 @@ __global__ __launch_bounds__(256) void draft_pick(DraftVerify a, DraftPlan p) {
         double own, run, total;
         auto sums = [&]() {
             own = 0.0;
-            for (int t = t0; t < t1; ++t) own += tiles[t];
+            for (int t = t0; t < t1; ++t) own += sum_of(tiles + t);
             run = run_256(own, wave_sums, total);
         };
         sums();
@@ -502,9 +546,9 @@ __global__ __launch_bounds__(256) void draft_pick(DraftVerify a, DraftPlan p) {
             kind = kPlain;
             for (int t = wave; t < p.tiles; t += 4) {
                 const double again = tile_sum<XT, PROBS>(a, pick, kind, t);
-                if ((tid & 63) == 0) tiles[t] = again;
+                if ((tid & 63) == 0) put_sum(tiles + t, again);
             }
-            __syncthreads();
+            sums_done();
             sums();
         }
         result = -1;
@@ -513,30 +557,32 @@ __global__ __launch_bounds__(256) void draft_pick(DraftVerify a, DraftPlan p) {
             if (tid == thread_at(run, own, r, hits)) {
                 double at = run - own, from = at;
                 for (int t = t0; t < t1; ++t) {
-                    const double v = tiles[t];
+                    const double v = sum_of(tiles + t);
                     if (v > 0.0) found = t, before = from = at;
                     at += v;
                     if (v > 0.0 && at > r) break;
                 }
             }
             __syncthreads();
-            const int e = found * kTile + tid * 4;
+            constexpr int kEach = kTile / 256;
+            static_assert(kEach == 2, "two tokens a thread");
+            const int e = found * kTile + tid * kEach;
             const double base = before;
-            Tokens<4, XT> t;
+            Tokens<kEach, XT> t;
             t.load(a, pick, kind, e, 1);
-            double w[4];
+            double w[kEach];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = t.template left<PROBS>(a, pick, kind, i, e + i);
-            own = ((w[0] + w[1]) + w[2]) + w[3];
+            for (int i = 0; i < kEach; ++i) w[i] = t.template left<PROBS>(a, pick, kind, i, e + i);
+            own = w[0] + w[1];
             run = base + run_256(own, wave_sums, total);
             if (tid == thread_at(run, own, r, hits)) {
                 double at = run - own;
                 int hit = 0;
 #pragma unroll
-                for (int i = 3; i >= 0; --i) hit = w[i] > 0.0 ? i : hit;      // (the first that holds anything)
+                for (int i = kEach - 1; i >= 0; --i) hit = w[i] > 0.0 ? i : hit;      // (the first that holds anything)
                 bool passed = false;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < kEach; ++i) {
                     at += w[i];
                     if (!passed && w[i] > 0.0) hit = i, passed = at > r;
                 }
@@ -552,6 +598,40 @@ __global__ __launch_bounds__(256) void draft_pick(DraftVerify a, DraftPlan p) {
         a.out[at] = tid < taken ? a.tokens[(int64_t)s * a.max_draft + tid] : tid == taken ? result : -1;
         if (tid == 0) a.n_accepted[s] = taken < 0 ? 0 : taken;
     }
+}
+
+// The workgroup of a sequence that is done last takes the token (of logits: draft_stats has set its count to 0; given
+// probabilities have no launch before this one that could, and draft_pick follows).
+template <typename XT, bool PROBS>
+__global__ __launch_bounds__(256, 5) void draft_sums(DraftVerify a, DraftPlan p) {
+    const int s = (int)(blockIdx.x / (unsigned)p.sum_parts), g = (int)(blockIdx.x % (unsigned)p.sum_parts);
+    __shared__ Pick pick;
+    __shared__ bool last;
+    decide<XT, PROBS>(a, p, s, pick);
+    __syncthreads();
+    if (PROBS && g == 0 && threadIdx.x == 0) reinterpret_cast<Pick *>(a.ws + p.off_pick)[s] = pick;
+    const Pick mine = uniform(pick);
+    if (mine.kind == kFixed) {
+        if (!PROBS && g == 0) pick_token<XT, PROBS>(a, p, s, mine);
+        return;
+    }
+    for (int tile = g * 4 + (int)(threadIdx.x >> 6); tile < p.tiles; tile += p.sum_parts * 4) {
+        const double sum = tile_sum<XT, PROBS>(a, mine, mine.kind, tile);
+        if ((threadIdx.x & 63) == 0) put_sum(reinterpret_cast<double *>(a.ws + p.off_tiles) + (int64_t)s * p.tiles + tile, sum);
+    }
+    if (PROBS) return;
+    sums_done();
+    if (threadIdx.x == 0)
+        last = __hip_atomic_fetch_add(reinterpret_cast<int *>(a.ws + p.off_done) + s, 1, __ATOMIC_RELAXED,
+                                      __HIP_MEMORY_SCOPE_AGENT) == p.sum_parts - 1;
+    sums_done();
+    if (!last) return;
+    pick_token<XT, PROBS>(a, p, s, mine);
+}
+
+template <typename XT>
+__global__ __launch_bounds__(256) void draft_pick(DraftVerify a, DraftPlan p) {
+    pick_token<XT, true>(a, p, blockIdx.x, uniform(reinterpret_cast<const Pick *>(a.ws + p.off_pick)[blockIdx.x]));
 }
 
 DraftPlan draft_plan(int64_t n_seqs, int64_t max_draft, int64_t n_vocab, bool has_draft, int elem_bytes, bool probs) {
@@ -579,6 +659,7 @@ DraftPlan draft_plan(int64_t n_seqs, int64_t max_draft, int64_t n_vocab, bool ha
     p.off_max = take((size_t)p.stat_groups * 4);
     p.off_arg = take((size_t)p.stat_groups * 4);
     p.off_tiles = take((size_t)n_seqs * p.tiles * 8);
+    p.off_done = take((size_t)n_seqs * 4);
     p.off_pick = take((size_t)n_seqs * sizeof(Pick));
     p.ws_bytes = at;
     return p;
@@ -590,11 +671,10 @@ hipError_t launch_draft_verify(const DraftVerify &a, const DraftPlan &p, Act xt,
         const unsigned sums = (unsigned)p.sum_groups, seqs = (unsigned)a.n_seqs;
         if (probs) {
             draft_sums<XT, true><<<sums, 256, 0, s>>>(a, p);
-            draft_pick<XT, true><<<seqs, 256, 0, s>>>(a, p);
+            draft_pick<XT><<<seqs, 256, 0, s>>>(a, p);
         } else {
             draft_stats<XT><<<(unsigned)p.stat_groups, 256, 0, s>>>(a, p);
             draft_sums<XT, false><<<sums, 256, 0, s>>>(a, p);
-            draft_pick<XT, false><<<seqs, 256, 0, s>>>(a, p);
         }
         return hipGetLastError();
     });

@@ -28,7 +28,7 @@ struct DraftPlan {
     int chunks;            // of a row in the statistics
     int chunk_vecs;        // 16-byte vectors of a chunk
     int tiles;             // of a row in the tile sums
-    size_t off_z, off_max, off_arg, off_tiles, off_pick;
+    size_t off_z, off_max, off_arg, off_tiles, off_done, off_pick;
     size_t ws_bytes;
 };
 struct DraftVerify {

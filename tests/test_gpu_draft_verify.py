@@ -23,7 +23,7 @@ def probabilities(row, form, t):
     if t == 0:
         return np.eye(1, len(row), int(row.argmax()))[0]
     with np.errstate(all="ignore"):
-        e = np.exp((row - row.max()) / t)
+        e = np.exp((row - row.max()) / min(max(t, 2.0 ** -100), 2.0 ** 100))     # (the documented ends)
     return e / e.sum()
 
 
@@ -166,6 +166,33 @@ def test_temperatures(has_draft, x):
     assert int(out[7].max()) < 3001
     temp[3], temp[4] = -1.0, float("nan")
     check(target, draft, tokens, n_draft, u, temp=torch.where(torch.isinf(temp), 1.0, temp))
+
+
+@pytest.mark.parametrize("size,t", [(1.0, 1e-3), (1.0, 1e-6), (1.0, 1e-8), (1.0, 1e-10), (1.0, 1e-20), (1.0, 1e-30), (1e6, 1.0),
+                                    (1e6, 1e-4), (1e9, 300.0), (1e30, 1.0), (1e30, 1e27), (1e38, 1e37), (1e-30, 1e-30), (1e20, 1e25),
+                                    (1e-20, 1.0)])
+def test_logits_and_temperatures_out_of_proportion(size, t):
+    """Rows whose largest values are a few float32 steps apart, the others anywhere, masks among them; a temperature of the
+    size of a step tells the largest apart, others not."""
+    import torch
+    n, v = 24, 3000
+    g = torch.Generator(device="cuda").manual_seed(21)
+    target = size * torch.randn(n, v, generator=g, device="cuda")
+    target[:, ::7] = -float("inf")
+    top = torch.full((n,), min(5.3 * size, 3e38), device="cuda")      # (float32 ends at 3.4e38)
+    for i in range(40):
+        target[:, 50 * i + 1] = top
+        if i % 3 == 0:
+            top = torch.nextafter(top, torch.zeros_like(top))
+    target[1::2, 2:] = -target[1::2, 2:].abs()       # negative ones, the largest at the front
+    target[1::2, 7::7] = -float("inf")
+    u = torch.rand(n, 1, generator=g, device="cuda")
+    temp = torch.full((n,), t, device="cuda")
+    none = torch.zeros(n, 0, dtype=torch.int32, device="cuda")
+    check(target, None, none, torch.zeros(n, dtype=torch.int32, device="cuda"), u, temp=temp)
+    tokens = torch.full((n // 2, 1), 1, dtype=torch.int32, device="cuda")
+    draft = target[::2].roll(1, 0).contiguous()
+    check(target, draft, tokens, torch.ones(n // 2, dtype=torch.int32, device="cuda"), u.view(n // 2, 2), temp=temp[: n // 2])
 
 
 def test_draft_counts_and_tokens():
