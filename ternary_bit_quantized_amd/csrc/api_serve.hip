@@ -188,7 +188,9 @@ int q2_0_kv_fork(int32_t *ref, int64_t n_pages, int32_t *table, int64_t n_seqs, 
 }
 
 size_t q2_0_kv_resize_workspace_bytes(int64_t n_seqs, int64_t n_pages) {
-    return in(n_seqs, 1, q2_0::kResizeMaxSeqs) && in(n_pages, 0, kMaxPages) ? (size_t)n_seqs * 32 + (size_t)n_pages * 4 : 0;
+    return in(n_seqs, 1, q2_0::kResizeMaxSeqs) && in(n_pages, 0, kMaxPages)
+               ? (size_t)n_seqs * 32 + (size_t)n_pages * 4 + (size_t)((n_pages + 31) / 32 + 2) * 4
+               : 0;
 }
 
 int q2_0_kv_resize(const q2_0_kv_cache *cache, const q2_0_kv_pages *pages, int32_t *table, int64_t n_seqs, int64_t table_len,
@@ -219,6 +221,7 @@ int q2_0_kv_resize(const q2_0_kv_cache *cache, const q2_0_kv_pages *pages, int32
     a.new_lens = new_lens, a.missing = missing;
     a.plan = static_cast<int32_t *>(workspace);
     a.fresh = a.plan + n_seqs * 8;
+    a.before = a.fresh + c.n_pages;
     return q2_0::record_hip_error(q2_0::launch_kv_resize(a, static_cast<hipStream_t>(stream)));
 }
 

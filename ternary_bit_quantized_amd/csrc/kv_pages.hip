@@ -7,10 +7,11 @@
 //
 // resize  kv_drop   (a workgroup per 1024 columns of a row) the pages that shrinking sequences leave
 //         kv_plan   (one workgroup) which growing sequences need a copy of a shared last page, how many pages
-//                   that takes in all, whether there are as many, and the list of them
+//                   that takes in all, and whether there are as many; of small tables kv_drop's and kv_list's parts too
+//         kv_list   the pages that are taken
 //         kv_take   the new entries of the rows, and the copies
-// fork    kv_fork_plan (one workgroup) which pairs hold; kv_fork_rows the rows and counts
-// compact kv_count  (one workgroup) pages in use before each 32; kv_move everything else
+// fork    kv_fork_plan (one workgroup) which pairs hold, and of small tables the rows and counts; else kv_fork_rows
+// compact kv_count  (one workgroup, large pools) pages in use before each 32; kv_move everything else
 #include "serve_common.h"
 
 namespace q2_0 {
@@ -84,17 +85,18 @@ static int col_parts(int64_t cols) { return (int)((cols + kCols - 1) / kCols); }
 int64_t kv_table_groups(int64_t n_rows, int64_t cols) { return n_rows * col_parts(cols); }
 
 // Sum over the workgroup of 1024 of the values of lower threads; `total`: of all.
-__device__ __forceinline__ int64_t scan_1024(int64_t v, int64_t *tmp, int64_t &total) {
+template <typename T>
+__device__ __forceinline__ T scan_1024(T v, T *tmp, T &total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int64_t run = v;
+    T run = v;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-        const int64_t o = __shfl_up(run, off);
+        const T o = __shfl_up(run, off);
         if (lane >= off) run += o;
     }
     if (lane == 63) tmp[wave] = run;
     __syncthreads();
-    int64_t base = 0, all = 0;
+    T base = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < 16; ++w) {
         if (w == wave) base = all;
@@ -105,9 +107,40 @@ __device__ __forceinline__ int64_t scan_1024(int64_t v, int64_t *tmp, int64_t &t
     return base + run - v;
 }
 
+// One workgroup of 1024 goes through `count` things of each of up to 1024 * PT owners, thread t's being PT in a row from t * PT, as
+// one list: f(owner, i) for every i < count.  `ends` holds 1024 * PT numbers in shared memory.
+template <int PT, typename F>
+__device__ __forceinline__ void each_of(const int (&count)[PT], int *ends, int64_t *tmp, F &&f) {
+    int64_t sum = 0, total;
+#pragma unroll
+    for (int i = 0; i < PT; ++i) sum += count[i];
+    int64_t at = scan_1024(sum, tmp, total);
+    if (total == 0) return;                                      // (uniform)
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+        at += count[i];
+        ends[threadIdx.x * PT + i] = (int)at;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < (int)total; e += 1024) {
+        int lo = 0;                                              // owners that end at or before e
+#pragma unroll
+        for (int step = 512 * PT; step >= 1; step >>= 1)
+            if (ends[lo + step - 1] <= e) lo += step;
+        f(lo, e - (lo ? ends[lo - 1] : 0));
+    }
+}
+
+// Tables of up to this many entries are left to the one workgroup that plans, a launch less; a call that changes all
+// of them takes it some 30 us.  Measured: 7000 entries of which a few change 9.4 us as one, 12.5 as two.
+constexpr int64_t kOneGroup = 65536;
+
 // ---------------------------------------------------------------------------- fork
 
+template <bool ROWS>
 __global__ __launch_bounds__(1024) void kv_fork_plan(KvFork a) {
+    __shared__ int64_t tmp[16];
+    __shared__ int ends[1024];
     const int64_t most = (int64_t)a.t.cols * a.page.d;
     for (int i = threadIdx.x; i < a.n; i += 1024) {
         const int s = a.src[i], d = a.dst[i];
@@ -128,6 +161,15 @@ __global__ __launch_bounds__(1024) void kv_fork_plan(KvFork a) {
     all_done();
     for (int i = threadIdx.x; i < a.n; i += 1024)
         if (a.plan[i] >= 0) put(a.t.lens + a.dst[i], a.plan[i]);
+    if (!ROWS) return;
+    // (a thread has written what it reads here: n <= 1024)
+    const int len = (int)threadIdx.x < a.n ? a.plan[threadIdx.x] : 0;
+    const int count[1] = {len > 0 ? pages_of(a.page, len) : 0};
+    each_of<1>(count, ends, tmp, [&](int i, int c) {
+        const int page = a.t.table[a.src[i] * a.t.ld + c];
+        a.t.table[a.dst[i] * a.t.ld + c] = page;
+        if (page >= 0 && page < a.n_pages) atomicAdd(a.ref + page, 1);
+    });
 }
 
 __global__ __launch_bounds__(256) void kv_fork_rows(KvFork a, int parts) {
@@ -145,13 +187,23 @@ __global__ __launch_bounds__(256) void kv_fork_rows(KvFork a, int parts) {
 }
 
 hipError_t launch_kv_fork(const KvFork &a, hipStream_t s) {
-    kv_fork_plan<<<1, 1024, 0, s>>>(a);
+    if (a.n <= 1024 && (int64_t)a.n * a.t.cols <= kOneGroup) {
+        kv_fork_plan<true><<<1, 1024, 0, s>>>(a);
+        return hipGetLastError();
+    }
+    kv_fork_plan<false><<<1, 1024, 0, s>>>(a);
     if (a.t.cols > 0)
         kv_fork_rows<<<(unsigned)kv_table_groups(a.n, a.t.cols), 256, 0, s>>>(a, col_parts(a.t.cols));
     return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------- resize
+
+__device__ __forceinline__ void drop_page(const KvResize &a, int32_t *entry) {
+    const int page = *entry;
+    *entry = -1;
+    if (page >= 0 && page < a.n_pages && atomicSub(a.ref + page, 1) == 1) atomicOr(a.free + (page >> 5), 1u << (page & 31));
+}
 
 __global__ __launch_bounds__(256) void kv_drop(KvResize a, int parts) {
     const int s = (int)(blockIdx.x / (unsigned)parts), part = (int)(blockIdx.x % (unsigned)parts);
@@ -163,12 +215,41 @@ __global__ __launch_bounds__(256) void kv_drop(KvResize a, int parts) {
     const int c1 = have < (part + 1) * kCols ? have : (part + 1) * kCols;
     for (int c = part * kCols + (int)threadIdx.x; c < c1; c += 256) {
         if (c < want) continue;
-        const int page = row[c];
-        row[c] = -1;
-        if (page >= 0 && page < a.n_pages && atomicSub(a.ref + page, 1) == 1)
-            atomicOr(a.free + (page >> 5), 1u << (page & 31));
+        drop_page(a, row + c);
     }
 }
+
+__device__ __forceinline__ uint32_t free_bits(const KvResize &a, int w) {
+    const uint32_t bits = (uint32_t)peek(reinterpret_cast<const int32_t *>(a.free) + w);
+    return w == a.n_pages / 32 ? bits & ((1u << (a.n_pages % 32)) - 1u) : bits;   // (a last word that is not whole)
+}
+
+// A word's free pages from place `at` of the list on, as far as `take`; all lanes.  Two words at a time, a lane a bit, a wave
+// writes their pages next to each other (a thread a word wrote 64 lines at once: 68000 pages 41 us in one workgroup, 22 so).
+__device__ __forceinline__ void list_word(const KvResize &a, int w, uint32_t bits, int at, int take) {
+    const int lane = threadIdx.x & 63;
+    at = at < take ? at : take;
+    const uint64_t some = __ballot(bits && at < take);
+    if (!some) return;
+#pragma unroll 4
+    for (int j = 0; j < 64; j += 2) {
+        if (!(some >> j & 3)) continue;                          // (uniform)
+        const int from = j + (lane >> 5), bit = lane & 31;
+        const uint32_t theirs = (uint32_t)__shfl((int)bits, from);
+        const int place = __shfl(at, from) + __popc(theirs & ((1u << bit) - 1u));
+        if ((theirs >> bit & 1) && place < take) a.fresh[place] = (w - lane + from) * 32 + bit;
+    }
+    if (bits && at < take) {
+        uint32_t stay = 0;                                       // (without the lowest ones, as many as are taken)
+        if (__popc(bits) > take - at) {
+            stay = bits;
+            for (int n = take - at; n > 0; --n) stay &= stay - 1;
+        }
+        put(reinterpret_cast<int32_t *>(a.free) + w, (int)stay);
+    }
+}
+
+constexpr int kHeldWords = 6144;      // 196608 pages: 24 KB
 
 struct Planned {
     int slot, have, want, old, rows, pad[3];
@@ -178,19 +259,13 @@ static_assert(sizeof(Planned) == 32, "8 numbers a sequence");
 // A sequence that grows from inside a page that others hold too takes a copy of it -- unless all holders do so in this
 // call: then the lowest of them keeps the page.  Holders leave by counting down; where that ends at 0, the lowest
 // claim on the count is the one that stays.
-template <int PT>
+template <int PT, bool DROP>
 __global__ __launch_bounds__(1024) void kv_plan(KvResize a) {
     __shared__ int64_t tmp[16];
+    __shared__ int ends[DROP ? 1024 * PT : 1];
+    __shared__ uint32_t held[kHeldWords];
     const int64_t most = (int64_t)a.t.cols * a.shape.page.d;
     const int tid = threadIdx.x;
-    // free pages, asked for first
-    const int words = (a.n_pages + 31) / 32;
-    int64_t some = 0;
-    for (int w = tid; w < words; w += 1024) {
-        uint32_t bits = a.free[w];
-        if (w == words - 1 && a.n_pages % 32) bits &= (1u << (a.n_pages % 32)) - 1u;
-        some += __popc(bits);
-    }
     Planned pl[PT];
     int len[PT], now[PT], count[PT], left[PT];
     bool grows[PT], shared[PT], keeps[PT];
@@ -201,7 +276,31 @@ __global__ __launch_bounds__(1024) void kv_plan(KvResize a) {
         if (s < a.t.n_seqs) len[i] = a.t.lens[s], now[i] = a.new_lens[s];
         const bool ok = !bad_len(len[i], most) && !bad_len(now[i], most);
         if (!ok) now[i] = len[i];
-        grows[i] = ok && now[i] > len[i];
+    }
+    if (DROP) {
+        int count[PT];
+#pragma unroll
+        for (int i = 0; i < PT; ++i)
+            count[i] = now[i] < len[i] ? pages_of(a.shape.page, len[i]) - pages_of(a.shape.page, now[i]) : 0;
+        each_of<PT>(count, ends, tmp, [&](int s, int i) { drop_page(a, a.t.table + s * a.t.ld + pages_of(a.shape.page, a.new_lens[s]) + i); });
+        all_done();
+    }
+    // free pages; their bits stay in shared memory for the list, as far as that reaches
+    const int words = (a.n_pages + 31) / 32;
+    int64_t some = 0;
+#pragma unroll
+    for (int j = 0; j < kHeldWords / 1024; ++j) {
+        const int w = j * 1024 + tid;
+        const uint32_t bits = w < words ? free_bits(a, w) : 0u;
+        held[w] = bits;
+        some += __popc(bits);
+    }
+    for (int w = kHeldWords + tid; w < words; w += 1024) some += __popc(free_bits(a, w));
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+        const int s = tid * PT + i;
+        const bool ok = !bad_len(len[i], most);
+        grows[i] = now[i] > len[i];
         pl[i].have = ok ? pages_of(a.shape.page, len[i]) : 0;
         pl[i].want = grows[i] ? pages_of(a.shape.page, now[i]) : pl[i].have;
         pl[i].rows = ok && pl[i].have > 0 ? len[i] - (pl[i].have - 1) * (int)a.shape.page.d : 0;
@@ -257,22 +356,27 @@ __global__ __launch_bounds__(1024) void kv_plan(KvResize a) {
         reinterpret_cast<Planned *>(a.plan)[s] = pl[i];
     }
     // the free pages of the lowest numbers, `total` of them
-    for (int64_t w0 = 0, base = 0; enough && base < total && w0 < words; w0 += 1024) {
-        const int w = (int)w0 + tid;
-        uint32_t bits = w < words ? a.free[w] : 0u;
-        if (w == words - 1 && a.n_pages % 32) bits &= (1u << (a.n_pages % 32)) - 1u;
-        int64_t all;
-        int64_t at = base + scan_1024(__popc(bits), tmp, all);
-        uint32_t taken = 0;
-        while (bits && at < total) {
-            const int b = __ffs((int)bits) - 1;
-            bits &= bits - 1;
-            taken |= 1u << b;
-            a.fresh[at++] = w * 32 + b;
-        }
-        if (taken) a.free[w] &= ~taken;
+    const int take = enough ? (int)total : 0;                    // (at most n_pages)
+    if (!DROP && tid == 0) a.before[words] = take;
+    int base = 0, reached = 0;
+    for (int w0 = 0; base < take && w0 < words; w0 += 1024) {
+        const int w = w0 + tid;
+        const uint32_t bits = w0 < kHeldWords ? held[w] : w < words ? free_bits(a, w) : 0u;
+        int all;
+        const int at = base + scan_1024((int)__popc(bits), reinterpret_cast<int *>(tmp), all);
+        if (DROP) list_word(a, w, bits, at, take);
+        else if (w < words) a.before[w] = at;
         base += all;
+        reached = w0 + 1024;
     }
+    if (!DROP && tid == 0) a.before[words + 1] = reached;
+}
+
+// Large tables: the list by as many workgroups as the bits fill.
+__global__ __launch_bounds__(256) void kv_list(KvResize a) {
+    const int words = (a.n_pages + 31) / 32, w = (int)(blockIdx.x * 256 + threadIdx.x), take = a.before[words];
+    const bool in = w < words && w < a.before[words + 1];
+    list_word(a, w, in ? free_bits(a, w) : 0u, in ? a.before[w] : take, take);
 }
 
 __global__ __launch_bounds__(256) void kv_take(KvResize a, int parts, int copy_parts, unsigned row_groups) {
@@ -306,9 +410,14 @@ __global__ __launch_bounds__(256) void kv_take(KvResize a, int parts, int copy_p
 hipError_t launch_kv_resize(const KvResize &a, hipStream_t s) {
     const int parts = col_parts(a.t.cols), copy_parts = parts_of(a.shape);
     const unsigned rows = (unsigned)kv_table_groups(a.t.n_seqs, a.t.cols);
-    if (rows) kv_drop<<<rows, 256, 0, s>>>(a, parts);
-    if (a.t.n_seqs <= 1024) kv_plan<1><<<1, 1024, 0, s>>>(a);
-    else kv_plan<kResizeMaxSeqs / 1024><<<1, 1024, 0, s>>>(a);
+    const bool one = (int64_t)a.t.n_seqs * a.t.cols <= kOneGroup;
+    if (rows && !one) kv_drop<<<rows, 256, 0, s>>>(a, parts);
+    constexpr int kMany = kResizeMaxSeqs / 1024;
+    if (a.t.n_seqs <= 1024 && one) kv_plan<1, true><<<1, 1024, 0, s>>>(a);
+    else if (a.t.n_seqs <= 1024) kv_plan<1, false><<<1, 1024, 0, s>>>(a);
+    else if (one) kv_plan<kMany, true><<<1, 1024, 0, s>>>(a);
+    else kv_plan<kMany, false><<<1, 1024, 0, s>>>(a);
+    if (!one) kv_list<<<((unsigned)a.n_pages / 32u + 256u) / 256u, 256, 0, s>>>(a);
     if (rows) kv_take<<<rows + (unsigned)(a.t.n_seqs * copy_parts), 256, 0, s>>>(a, parts, copy_parts, rows);
     return hipGetLastError();
 }
@@ -327,59 +436,121 @@ __global__ __launch_bounds__(1024) void kv_count(KvCompact a) {
     for (int w0 = 0; w0 < words; w0 += 1024) {
         const int w = w0 + (int)threadIdx.x;
         int64_t all;
-        const int64_t at = scan_1024(w < words ? __popc(used_bits(a, w)) : 0, tmp, all);
+        const int64_t at = scan_1024((int64_t)(w < words ? __popc(used_bits(a, w)) : 0), tmp, all);
         if (w < words) a.before[w] = (int)(base + at);
         base += all;
     }
     if (threadIdx.x == 0) *a.n_used = (int)base;
 }
 
-// the new number of a page, -1 for one that is free or does not exist
-__device__ __forceinline__ int moved(const KvCompact &a, int page) {
-    if (page < 0 || page >= a.from_pages) return -1;
-    const uint32_t bits = used_bits(a, page >> 5);
-    if (!(bits >> (page & 31) & 1)) return -1;
-    return a.before[page >> 5] + __popc(bits & ((1u << (page & 31)) - 1u));
+// The new number of a page in use: pages in use before it.
+__device__ __forceinline__ bool in_use(const KvCompact &a, int page) {
+    return page >= 0 && page < a.from_pages && used_bits(a, page >> 5) >> (page & 31) & 1;
+}
+__device__ __forceinline__ int moved(const KvCompact &a, int page, const int32_t *before) {
+    return before[page >> 5] + __popc(used_bits(a, page >> 5) & ((1u << (page & 31)) - 1u));
 }
 
+// A workgroup of 256 counts for itself: pages in use before each word (all != nullptr) or before word `upto`; returns all.
+__device__ __forceinline__ int count_256(const KvCompact &a, int upto, int32_t *all, int *before, int *tmp) {
+    const int words = (a.from_pages + 31) / 32, each = (words + 255) / 256;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int w0 = (int)threadIdx.x * each, w1 = w0 + each < words ? w0 + each : words;
+    int own = 0, low = 0;
+    for (int w = w0; w < w1; ++w) {
+        const int n = __popc(used_bits(a, w));
+        own += n;
+        low += w < upto ? n : 0;
+    }
+    int run = own;
+    if (all) {
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int o = __shfl_up(run, off);
+            if (lane >= off) run += o;
+        }
+    } else {
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) run += __shfl_xor(run, off), low += __shfl_xor(low, off);
+    }
+    if (lane == 63) tmp[wave] = run, tmp[4 + wave] = low;
+    __syncthreads();
+    if (all) {
+        int at = run - own;
+        for (int w = 0; w < wave; ++w) at += tmp[w];
+        for (int w = w0; w < w1; ++w) {
+            all[w] = at;
+            at += __popc(used_bits(a, w));
+        }
+        __syncthreads();
+    } else {
+        *before = tmp[4] + tmp[5] + tmp[6] + tmp[7];
+    }
+    return tmp[0] + tmp[1] + tmp[2] + tmp[3];
+}
+
+// Pools of up to this many pages are counted by every workgroup anew (2 KB of bits from the caches), a launch less.
+constexpr int kCountPages = 16384;
+
+template <bool COUNT>
 __global__ __launch_bounds__(256) void kv_move(KvCompact a, int parts, int copy_parts, unsigned row_groups, unsigned page_groups) {
-    const int n_used = *a.n_used;
-    if (n_used > a.to_pages) return;
+    __shared__ int32_t mine[COUNT ? kCountPages / 32 : 1];
+    __shared__ int tmp[8];
     unsigned b = blockIdx.x;
+    if (b >= row_groups + page_groups) {
+        b -= row_groups + page_groups;
+        const int page = (int)(b / (unsigned)copy_parts), part = (int)(b % (unsigned)copy_parts);
+        if (!in_use(a, page)) return;
+        int to, n_used;
+        if (COUNT) {
+            int before;
+            n_used = count_256(a, page >> 5, nullptr, &before, tmp);
+            to = before + __popc(used_bits(a, page >> 5) & ((1u << (page & 31)) - 1u));
+        } else {
+            n_used = *a.n_used;
+            to = moved(a, page, a.before);
+        }
+        if (n_used > a.to_pages) return;
+        if (part == 0 && threadIdx.x == 0) a.to_ref[to] = a.ref[page];
+        copy_part(a.to, a.from, a.shape, to, page, part, (int)a.shape.page.d);
+        return;
+    }
+    int before;
+    const int n_used = COUNT ? count_256(a, 0, mine, &before, tmp) : *a.n_used;
+    if (COUNT && b == row_groups + page_groups - 1 && threadIdx.x == 0) *a.n_used = n_used;
+    if (n_used > a.to_pages) return;
     if (b < row_groups) {                                        // a row of the table
         const int s = (int)(b / (unsigned)parts), part = (int)(b % (unsigned)parts);
         const int len = a.t.lens[s];
         const int n = bad_len(len, (int64_t)a.t.cols * a.shape.page.d) ? 0 : pages_of(a.shape.page, len);
         const int c1 = a.t.cols < (part + 1) * kCols ? a.t.cols : (part + 1) * kCols;
-        for (int c = part * kCols + (int)threadIdx.x; c < c1; c += 256)
-            a.to_table[s * a.ld_to + c] = c < n ? moved(a, a.t.table[s * a.t.ld + c]) : -1;
-        return;
-    }
-    b -= row_groups;
-    if (b < page_groups) {                                       // bits, and the counts of pages that none moves to
-        const int page = (int)(b * 256 + threadIdx.x);
-        if (page < (a.to_pages + 31) / 32) {
-            const int left = n_used - page * 32, last = a.to_pages - page * 32;
-            const uint32_t used = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1u : 0u;
-            a.to_free[page] = ~used & (last >= 32 ? ~0u : (1u << last) - 1u);
+        for (int c = part * kCols + (int)threadIdx.x; c < c1; c += 256) {
+            const int page = c < n ? a.t.table[s * a.t.ld + c] : -1;
+            a.to_table[s * a.ld_to + c] = in_use(a, page) ? moved(a, page, COUNT ? mine : a.before) : -1;
         }
-        if (page >= n_used && page < a.to_pages) a.to_ref[page] = 0;
         return;
     }
-    b -= page_groups;
-    const int page = (int)(b / (unsigned)copy_parts), part = (int)(b % (unsigned)copy_parts);
-    const int to = moved(a, page);
-    if (to < 0) return;
-    if (part == 0 && threadIdx.x == 0) a.to_ref[to] = a.ref[page];
-    copy_part(a.to, a.from, a.shape, to, page, part, (int)a.shape.page.d);
+    b -= row_groups;                                             // bits, and the counts of pages that none moves to
+    const int page = (int)(b * 256 + threadIdx.x);
+    if (page < (a.to_pages + 31) / 32) {
+        const int left = n_used - page * 32, last = a.to_pages - page * 32;
+        const uint32_t used = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1u : 0u;
+        a.to_free[page] = ~used & (last >= 32 ? ~0u : (1u << last) - 1u);
+    }
+    if (page >= n_used && page < a.to_pages) a.to_ref[page] = 0;
 }
 
 hipError_t launch_kv_compact(const KvCompact &a, hipStream_t s) {
-    kv_count<<<1, 1024, 0, s>>>(a);
     const int parts = col_parts(a.t.cols), copy_parts = parts_of(a.shape);
-    const unsigned rows = (unsigned)kv_table_groups(a.t.n_seqs, a.t.cols), pages = ((unsigned)a.to_pages + 255u) / 256u;
+    const unsigned rows = (unsigned)kv_table_groups(a.t.n_seqs, a.t.cols);
+    const unsigned pages = a.to_pages ? ((unsigned)a.to_pages + 255u) / 256u : 1u;    // (one writes n_used)
     const unsigned groups = rows + pages + (unsigned)a.from_pages * (unsigned)copy_parts;
-    if (groups) kv_move<<<groups, 256, 0, s>>>(a, parts, copy_parts, rows, pages);
+    if (a.from_pages <= kCountPages) {
+        kv_move<true><<<groups, 256, 0, s>>>(a, parts, copy_parts, rows, pages);
+        return hipGetLastError();
+    }
+    kv_count<<<1, 1024, 0, s>>>(a);
+    kv_move<false><<<groups, 256, 0, s>>>(a, parts, copy_parts, rows, pages);
     return hipGetLastError();
 }
 

@@ -9,8 +9,9 @@
 // wave's largest key as moe_choose does, upper halves first and lower halves only where these are
 // equal, and the lowest lane and place among equals is the lowest index.
 //
-// Groups: the keys go through LDS, lane g looks through group g for its one or two best; a group's
-// rank is the number of groups before it, counted with a lane read of each.
+// Groups: where one is the keys of 1, 2, 4 .. lanes, those exchange their two best (8 groups of 32 experts: 3 steps);
+// else the keys go through LDS and lane g looks through group g.  A group's rank is the number of groups before it, counted
+// with a lane read of each.
 #include <type_traits>
 
 #include "serve_common.h"
@@ -38,6 +39,23 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
     return v;
+}
+
+__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int off) {
+    const uint32_t lo = (uint32_t)__shfl_xor((int)(uint32_t)v, off), hi = (uint32_t)__shfl_xor((int)(uint32_t)(v >> 32), off);
+    return (uint64_t)hi << 32 | lo;
+}
+
+// the two largest of (b1 >= b2) and (o1 >= o2)
+__device__ __forceinline__ void two_largest(uint64_t &b1, uint64_t &b2, uint64_t o1, uint64_t o2) {
+    const bool more = o1 > b1;
+    const uint64_t low = more ? b1 : o1, next = more ? o2 : b2;  // the lower of the largest, and what the larger one's side has next
+    b1 = more ? o1 : b1;
+    b2 = low > next ? low : next;
+}
+
+__device__ __forceinline__ uint64_t group_key(const ChooseGroups &a, uint64_t b1, uint64_t b2) {
+    return order_key64(a.group_top == 2 ? key_value64(b1) + key_value64(b2) : key_value64(b1));
 }
 
 template <int PL, typename XT, bool SIGMOID>
@@ -85,7 +103,27 @@ __global__ __launch_bounds__(256) void moe_choose_groups(ChooseGroups a) {
         const int e = lane * PL + i;
         key[i] = e < a.n_expert ? order_key64(s[i] + (a.bias ? (double)a.bias[e] : 0.0)) : 0u;
     }
-    if (a.n_group > 1) {
+    if (a.group_lanes > 0) {
+        // a group is the keys of a power of two of lanes: its two largest by exchanges, and its value is known to all of them
+        uint64_t b1 = key[0], b2 = 0u;
+#pragma unroll
+        for (int i = 1; i < PL; ++i) two_largest(b1, b2, key[i], 0u);
+        for (int off = 1; off < a.group_lanes; off <<= 1) {
+            const uint64_t o1 = shfl_xor64(b1, off);
+            two_largest(b1, b2, o1, shfl_xor64(b2, off));
+        }
+        const uint64_t g = group_key(a, b1, b2);
+        const int mine = lane / a.group_lanes;
+        int rank = 0;
+        for (int h = 0; h < a.n_group; ++h) {
+            const uint64_t k = read_lane64(g, h * a.group_lanes);
+            rank += k > g || (k == g && h < mine);
+        }
+        if (rank >= a.n_group_used)
+#pragma unroll
+            for (int i = 0; i < PL; ++i) key[i] = 0u;
+    } else if (a.n_group > 1) {
+        // groups of any size: through LDS, lane g looks through group g
         uint64_t *mine = key_lds + wave * 64 * PL;
 #pragma unroll
         for (int i = 0; i < PL; ++i) mine[lane * PL + i] = key[i];
@@ -95,12 +133,9 @@ __global__ __launch_bounds__(256) void moe_choose_groups(ChooseGroups a) {
         if (lane < a.n_group) {
             const int n = (int)a.size.d;
             uint64_t b1 = 0u, b2 = 0u;
-            for (int i = 0; i < n; ++i) {
-                const uint64_t k = mine[lane * n + i];
-                b2 = k > b1 ? b1 : (k > b2 ? k : b2);
-                b1 = k > b1 ? k : b1;
-            }
-            g = order_key64(a.group_top == 2 ? key_value64(b1) + key_value64(b2) : key_value64(b1));
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) two_largest(b1, b2, mine[lane * n + i], 0u);
+            g = group_key(a, b1, b2);
         }
         int rank = 0;
         for (int h = 0; h < a.n_group; ++h) {
@@ -155,13 +190,15 @@ __global__ __launch_bounds__(256) void moe_choose_groups(ChooseGroups a) {
     }
 }
 
-hipError_t launch_moe_choose_groups(const ChooseGroups &a, Act xt, bool sigmoid, hipStream_t s) {
+hipError_t launch_moe_choose_groups(ChooseGroups a, Act xt, bool sigmoid, hipStream_t s) {
     return with_act(xt, [&](auto tag) -> hipError_t {
         using XT = decltype(tag);
         const dim3 grid((unsigned)((a.n_tokens + 3) / 4));
         auto go = [&](auto pl) {
             constexpr int PL = decltype(pl)::value;
-            const size_t lds = a.n_group > 1 ? 4 * 64 * PL * sizeof(uint64_t) : 0;
+            const int lanes = (int)a.size.d / PL;
+            a.group_lanes = a.n_group > 1 && a.size.d % PL == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+            const size_t lds = a.n_group > 1 && !a.group_lanes ? 4 * 64 * PL * sizeof(uint64_t) : 0;
             if (sigmoid) moe_choose_groups<PL, XT, true><<<grid, 256, lds, s>>>(a);
             else moe_choose_groups<PL, XT, false><<<grid, 256, lds, s>>>(a);
         };

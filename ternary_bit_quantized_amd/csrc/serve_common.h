@@ -13,12 +13,13 @@ struct ChooseGroups {
     const float *bias;
     FastDiv size;          // experts of a group
     int n_expert, n_used, n_group, n_group_used, group_top;
+    int group_lanes;       // lanes whose keys are a group, a power of two (0: no groups, or of another size)
     int normalise;
     float scale;
     int32_t *ids;
     float *weights;
 };
-hipError_t launch_moe_choose_groups(const ChooseGroups &a, Act xt, bool sigmoid, hipStream_t s);
+hipError_t launch_moe_choose_groups(ChooseGroups a, Act xt, bool sigmoid, hipStream_t s);
 
 // ---- verification of drafted tokens
 struct DraftPlan {
@@ -94,6 +95,7 @@ struct KvResize {
     int32_t *missing;
     int32_t *plan;         // 8 numbers a sequence
     int32_t *fresh;        // the pages that the call takes
+    int32_t *before;       // free pages before each word of `free` (large tables), how many are taken, and of how many words
 };
 hipError_t launch_kv_resize(const KvResize &a, hipStream_t s);
 
