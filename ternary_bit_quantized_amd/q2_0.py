@@ -801,6 +801,14 @@ def _ints(t, name, dev):
     return t.data_ptr(), t.shape[0]
 
 
+def _result(t, like, shape, dtype, name, stream, dev):
+    """A result given, or a new one -> (tensor, address)."""
+    if t is None:
+        t = _empty(like, shape, dtype, stream)
+        return t, t.data_ptr()
+    return t, _dense(t, dtype, shape, name, dev)
+
+
 def _pages(ref, free, n_pages, dev):
     """Counts and free bits (int32, 32 pages a word) of n_pages pages -> KvPages."""
     import torch
@@ -831,14 +839,10 @@ def q2_0_moe_route_groups(logits, n_used: int, score: int = Q2_0_SCORE_SIGMOID, 
         raise ValueError("logits must be float32, float16 or bfloat16")
     ld = _rows(logits, n, n_expert, "logits", dev)
     bp = 0 if bias is None else _dense(bias, torch.float32, (n_expert,), "bias", dev)
-    if ids is None:
-        ids = _empty(logits, (n, n_used), torch.int32, stream)
-    if weights is None:
-        weights = _empty(logits, (n, n_used), torch.float32, stream)
+    ids, ip = _result(ids, logits, (n, n_used), torch.int32, "ids", stream, dev)
+    weights, wp = _result(weights, logits, (n, n_used), torch.float32, "weights", stream, dev)
     _check(moe_route_groups_raw(logits.data_ptr(), xt, ld, n, n_expert, n_used, score, bp, n_group, n_group_used, group_top,
-                                int(bool(normalise)), scale, _dense(ids, torch.int32, (n, n_used), "ids", dev),
-                                _dense(weights, torch.float32, (n, n_used), "weights", dev), _stream(stream, dev)),
-           "q2_0_moe_route_groups")
+                                int(bool(normalise)), scale, ip, wp, _stream(stream, dev)), "q2_0_moe_route_groups")
     return ids, weights
 
 
@@ -864,18 +868,14 @@ def q2_0_draft_verify(target, draft, tokens, n_draft, u, form: int = Q2_0_DRAFT_
             raise ValueError("draft must have as many columns as target")
         dp, ldd = draft.data_ptr(), _rows(draft, n * most, vocab, "draft", dev)
     tp = 0 if temperature is None else _dense(temperature, torch.float32, (n,), "temperature", dev)
-    if out is None:
-        out = _empty(target, (n, most + 1), torch.int32, stream)
-    if n_accepted is None:
-        n_accepted = _empty(target, (n,), torch.int32, stream)
+    out, op = _result(out, target, (n, most + 1), torch.int32, "out", stream, dev)
+    n_accepted, ap = _result(n_accepted, target, (n,), torch.int32, "n_accepted", stream, dev)
     need = draft_verify_workspace_bytes(n, most, vocab, xt, form, int(draft is not None))
     workspace, wsp, wsb = _work(workspace, need, target, stream, dev)
     _check(draft_verify_raw(target.data_ptr(), ldt, dp, ldd, xt, form, vocab, tp,
                             _dense(tokens, torch.int32, (n, most), "tokens", dev),
                             _dense(n_draft, torch.int32, (n,), "n_draft", dev),
-                            _dense(u, torch.float32, (n, most + 1), "u", dev), n, most,
-                            _dense(out, torch.int32, (n, most + 1), "out", dev),
-                            _dense(n_accepted, torch.int32, (n,), "n_accepted", dev), wsp, wsb, _stream(stream, dev)),
+                            _dense(u, torch.float32, (n, most + 1), "u", dev), n, most, op, ap, wsp, wsb, _stream(stream, dev)),
            "q2_0_draft_verify")
     return out, n_accepted
 
@@ -915,15 +915,14 @@ def q2_0_kv_resize(k_cache, v_cache, ref, free, table, lens, new_lens, missing=N
     dev = torch.cuda.current_device()
     c = _cache(k_cache, v_cache, dev)
     tp, n_seqs, cols, ldt = _table(table, dev)
-    if missing is None:
-        missing = _empty(lens, (1,), torch.int32, stream)
+    missing, mp = _result(missing, lens, (1,), torch.int32, "missing", stream, dev)
     if n_seqs == 0:
         return missing.zero_()
     workspace, wsp, wsb = _work(workspace, kv_resize_workspace_bytes(n_seqs, c.n_pages), lens, stream, dev)
     _check(kv_resize_raw(c, _pages(ref, free, c.n_pages, dev), tp, n_seqs, cols, ldt,
                          _dense(lens, torch.int32, (n_seqs,), "lens", dev),
-                         _dense(new_lens, torch.int32, (n_seqs,), "new_lens", dev),
-                         _dense(missing, torch.int32, (1,), "missing", dev), wsp, wsb, _stream(stream, dev)), "q2_0_kv_resize")
+                         _dense(new_lens, torch.int32, (n_seqs,), "new_lens", dev), mp, wsp, wsb, _stream(stream, dev)),
+           "q2_0_kv_resize")
     return missing
 
 
@@ -939,10 +938,9 @@ def q2_0_kv_compact(k_to, v_to, ref_to, free_to, table_to, k_from, v_from, ref, 
     np_, n_to, cols_to, ldn = _table(table_to, dev)
     if n_to != n_seqs or cols_to != cols:
         raise ValueError("table_to must have the shape of table")
-    if n_used is None:
-        n_used = _empty(lens, (1,), torch.int32, stream)
+    n_used, up = _result(n_used, lens, (1,), torch.int32, "n_used", stream, dev)
     workspace, wsp, wsb = _work(workspace, kv_compact_workspace_bytes(frm.n_pages), lens, stream, dev)
     _check(kv_compact_raw(to, _pages(ref_to, free_to, to.n_pages, dev), frm, _pages(ref, free, frm.n_pages, dev), tp, n_seqs,
-                          cols, ldt, _dense(lens, torch.int32, (n_seqs,), "lens", dev), np_, ldn,
-                          _dense(n_used, torch.int32, (1,), "n_used", dev), wsp, wsb, _stream(stream, dev)), "q2_0_kv_compact")
+                          cols, ldt, _dense(lens, torch.int32, (n_seqs,), "lens", dev), np_, ldn, up, wsp, wsb,
+                          _stream(stream, dev)), "q2_0_kv_compact")
     return n_used
