@@ -20,7 +20,7 @@ namespace q2_0 {
 
 constexpr int kMaxRows = 2 * Q2_0_DRAFT_MAX + 1;
 constexpr int kTile = 512;
-constexpr int kPassVecs = 1024;       // 16-byte vectors of a workgroup's pass: 4 a thread
+constexpr int kPass = 4096;           // values of a workgroup's pass: 16 a thread
 
 // 2^r for r in [-1/2, 1/2]: the polynomial of degree 8 that meets it at the Chebyshev points (relative error 1.1e-12).
 __device__ __forceinline__ double exp2_frac(double r) {
@@ -99,6 +99,7 @@ __device__ __forceinline__ bool greedy_of(const DraftVerify &a, int s) { return 
 template <typename XT>
 struct Vec {                          // 16 bytes of a row
     static constexpr int n = 16 / sizeof(XT);
+    static constexpr int each = kPass / 256 / n, pass = kPass / n;   // vectors of a thread and of a pass
     float x[n];
 };
 
@@ -125,20 +126,20 @@ __device__ __forceinline__ void unpack(u32x4_t v, Vec<bf16_t> &o) {
     }
 }
 
-// A thread's four vectors of the pass that begins at vector v of a row whose first element is `shift` elements past a 16-byte
+// A thread's vectors of the pass that begins at vector v of a row whose first element is `shift` elements past a 16-byte
 // boundary; what is outside the row (or at `end` and after it) is -inf and not read.
 template <typename XT>
-__device__ __forceinline__ void load_pass(const XT *row, int shift, int n_vocab, int v, int end, Vec<XT> (&x)[4]) {
+__device__ __forceinline__ void load_pass(const XT *row, int shift, int n_vocab, int v, int end, Vec<XT> (&x)[Vec<XT>::each]) {
     constexpr int VE = Vec<XT>::n;
     const int first = v * VE - shift;
-    if (first >= 0 && v + kPassVecs <= end && first + kPassVecs * VE <= n_vocab) {
+    if (first >= 0 && v + Vec<XT>::pass <= end && first + kPass <= n_vocab) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < Vec<XT>::each; ++i)
             unpack(__builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(row + first + (i * 256 + (int)threadIdx.x) * VE)), x[i]);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < Vec<XT>::each; ++i) {
         const int w = v + i * 256 + (int)threadIdx.x, e = w * VE - shift;
         if (w < end && e >= 0 && e + VE <= n_vocab) {
             unpack(*reinterpret_cast<const u32x4_t *>(row + e), x[i]);
@@ -174,12 +175,12 @@ __global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
     bool bad = false;
     Exps ex;
     ex.scale(scale_of(a, s));
-    for (int v = v0; v < v1; v += kPassVecs) {
-        Vec<XT> x[4];
+    for (int v = v0; v < v1; v += Vec<XT>::pass) {
+        Vec<XT> x[Vec<XT>::each];
         load_pass(row, shift, a.n_vocab, v, v1, x);
         float top = m;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < Vec<XT>::each; ++i)
 #pragma unroll
             for (int e = 0; e < VE; e += 2) {
                 top = fmaxf(fmaxf(x[i].x[e], x[i].x[e + 1]), top);
@@ -189,7 +190,7 @@ __global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
             if (top > m) {
                 m = top;
 #pragma unroll
-                for (int i = 3; i >= 0; --i)
+                for (int i = Vec<XT>::each - 1; i >= 0; --i)
 #pragma unroll
                     for (int e = VE - 1; e >= 0; --e)
                         if (x[i].x[e] == top) arg = (v + i * 256 + (int)threadIdx.x) * VE - shift + e;
@@ -204,7 +205,7 @@ __global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
         }
         if (m == -__builtin_inff()) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < Vec<XT>::each; ++i)
 #pragma unroll
             for (int e = 0; e < VE; ++e) z += ex.of(x[i].x[e], ex.k);
     }
@@ -639,9 +640,10 @@ DraftPlan draft_plan(int64_t n_seqs, int64_t max_draft, int64_t n_vocab, bool ha
     const int64_t rows = probs ? 0 : n_seqs * (max_draft + 1 + (has_draft ? max_draft : 0));
     const int64_t ve = 16 / elem_bytes, vecs = (n_vocab + 2 * ve - 2) / ve;      // of the worst alignment
     // one pass a workgroup until there are some 16 workgroups for each of the 256 CUs, then longer chunks
-    int64_t passes = (vecs + kPassVecs - 1) / kPassVecs, per = 1;
+    const int64_t pass = kPass / ve;
+    int64_t passes = (vecs + pass - 1) / pass, per = 1;
     while (per < 8 && rows * ((passes + per - 1) / per) > 6000) per *= 2;
-    p.chunk_vecs = (int)(per * kPassVecs);
+    p.chunk_vecs = (int)(per * pass);
     p.chunks = (int)((passes + per - 1) / per);
     p.tiles = (int)((n_vocab + kTile - 1) / kTile);
     p.stat_groups = rows * p.chunks;
