@@ -108,7 +108,9 @@ __device__ __forceinline__ T scan_1024(T v, T *tmp, T &total) {
 }
 
 // One workgroup of 1024 goes through `count` things of each of up to 1024 * PT owners, thread t's being PT in a row from t * PT, as
-// one list: f(owner, i) for every i < count.  `ends` holds 1024 * PT numbers in shared memory.
+// one list, eight at a time a thread: f(owner, i, in) for things i < count of their owners where in.  (One at a time the
+// loads and counts of each wait for the one before.)  `ends` holds 1024 * PT numbers in shared memory.
+constexpr int kAtOnce = 8;
 template <int PT, typename F>
 __device__ __forceinline__ void each_of(const int (&count)[PT], int *ends, int64_t *tmp, F &&f) {
     int64_t sum = 0, total;
@@ -122,17 +124,31 @@ __device__ __forceinline__ void each_of(const int (&count)[PT], int *ends, int64
         ends[threadIdx.x * PT + i] = (int)at;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < (int)total; e += 1024) {
-        int lo = 0;                                              // owners that end at or before e
+    for (int from = 0; from < (int)total; from += 1024 * kAtOnce) {
+        int owner[kAtOnce], thing[kAtOnce];
+        bool in[kAtOnce];
 #pragma unroll
-        for (int step = 512 * PT; step >= 1; step >>= 1)
-            if (ends[lo + step - 1] <= e) lo += step;
-        f(lo, e - (lo ? ends[lo - 1] : 0));
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int e = from + 1024 * k + (int)threadIdx.x;
+            in[k] = e < (int)total;
+            owner[k] = thing[k] = 0;
+            if (from + 1024 * k >= (int)total) continue;         // (uniform)
+            int lo = 0;                                          // owners that end at or before e
+#pragma unroll
+            for (int step = 512 * PT; step >= 1; step >>= 1)
+                if (ends[lo + step - 1] <= e) lo += step;
+            owner[k] = in[k] ? lo : 0;
+            thing[k] = in[k] ? e - (lo ? ends[lo - 1] : 0) : 0;
+        }
+        f(owner, thing, in);
     }
 }
 
-// Tables of up to this many entries are left to the one workgroup that plans, a launch less; a call that changes all
-// of them takes it some 30 us.  Measured: 7000 entries of which a few change 9.4 us as one, 12.5 as two.
+// Tables of up to this many entries are left to the one workgroup that plans, two launches less of a resize and one of a fork.
+// Measured in a graph: two calls for 64 sequences of 48000 entries in all that change 40 of them take 19.2 us so, 23.0 with
+// kv_drop and kv_list, and eager calls 6 us less of the host.  One that changes much is slower: 8000 pages given back and
+// taken 73 us against 31, 32000 of them 236 against 40 (a CU does an atomic in some 7 cycles).  Steps that change a few
+// pages are the rule, and a sequence that ends is one of many.
 constexpr int64_t kOneGroup = 65536;
 
 // ---------------------------------------------------------------------------- fork
@@ -165,10 +181,17 @@ __global__ __launch_bounds__(1024) void kv_fork_plan(KvFork a) {
     // (a thread has written what it reads here: n <= 1024)
     const int len = (int)threadIdx.x < a.n ? a.plan[threadIdx.x] : 0;
     const int count[1] = {len > 0 ? pages_of(a.page, len) : 0};
-    each_of<1>(count, ends, tmp, [&](int i, int c) {
-        const int page = a.t.table[a.src[i] * a.t.ld + c];
-        a.t.table[a.dst[i] * a.t.ld + c] = page;
-        if (page >= 0 && page < a.n_pages) atomicAdd(a.ref + page, 1);
+    each_of<1>(count, ends, tmp, [&](const int (&i)[kAtOnce], const int (&c)[kAtOnce], const bool (&in)[kAtOnce]) {
+        int page[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+            if (in[k]) page[k] = a.t.table[a.src[i[k]] * a.t.ld + c[k]];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+            if (in[k]) {
+                a.t.table[a.dst[i[k]] * a.t.ld + c[k]] = page[k];
+                if (page[k] >= 0 && page[k] < a.n_pages) atomicAdd(a.ref + page[k], 1);
+            }
     });
 }
 
@@ -192,6 +215,8 @@ hipError_t launch_kv_fork(const KvFork &a, hipStream_t s) {
         return hipGetLastError();
     }
     kv_fork_plan<false><<<1, 1024, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();                      // (nothing runs on a plan that was not made)
+    if (e != hipSuccess) return e;
     if (a.t.cols > 0)
         kv_fork_rows<<<(unsigned)kv_table_groups(a.n, a.t.cols), 256, 0, s>>>(a, col_parts(a.t.cols));
     return hipGetLastError();
@@ -282,7 +307,26 @@ __global__ __launch_bounds__(1024) void kv_plan(KvResize a) {
 #pragma unroll
         for (int i = 0; i < PT; ++i)
             count[i] = now[i] < len[i] ? pages_of(a.shape.page, len[i]) - pages_of(a.shape.page, now[i]) : 0;
-        each_of<PT>(count, ends, tmp, [&](int s, int i) { drop_page(a, a.t.table + s * a.t.ld + pages_of(a.shape.page, a.new_lens[s]) + i); });
+        each_of<PT>(count, ends, tmp, [&](const int (&s)[kAtOnce], const int (&i)[kAtOnce], const bool (&in)[kAtOnce]) {
+            int32_t *entry[kAtOnce];
+            int page[kAtOnce], held[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                if (!in[k]) continue;
+                entry[k] = a.t.table + s[k] * a.t.ld + pages_of(a.shape.page, a.new_lens[s[k]]) + i[k];
+                page[k] = *entry[k];
+            }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                held[k] = 0;
+                if (!in[k]) continue;
+                *entry[k] = -1;
+                if (page[k] >= 0 && page[k] < a.n_pages) held[k] = atomicSub(a.ref + page[k], 1);
+            }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+                if (held[k] == 1) atomicOr(a.free + (page[k] >> 5), 1u << (page[k] & 31));
+        });
         all_done();
     }
     // free pages; their bits stay in shared memory for the list, as far as that reaches
@@ -411,13 +455,21 @@ hipError_t launch_kv_resize(const KvResize &a, hipStream_t s) {
     const int parts = col_parts(a.t.cols), copy_parts = parts_of(a.shape);
     const unsigned rows = (unsigned)kv_table_groups(a.t.n_seqs, a.t.cols);
     const bool one = (int64_t)a.t.n_seqs * a.t.cols <= kOneGroup;
-    if (rows && !one) kv_drop<<<rows, 256, 0, s>>>(a, parts);
     constexpr int kMany = kResizeMaxSeqs / 1024;
+    hipError_t e = hipSuccess;                                   // nothing runs after a launch that failed
+    if (!one) {
+        kv_drop<<<rows, 256, 0, s>>>(a, parts);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
     if (a.t.n_seqs <= 1024 && one) kv_plan<1, true><<<1, 1024, 0, s>>>(a);
     else if (a.t.n_seqs <= 1024) kv_plan<1, false><<<1, 1024, 0, s>>>(a);
     else if (one) kv_plan<kMany, true><<<1, 1024, 0, s>>>(a);
     else kv_plan<kMany, false><<<1, 1024, 0, s>>>(a);
-    if (!one) kv_list<<<((unsigned)a.n_pages / 32u + 256u) / 256u, 256, 0, s>>>(a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (!one) {
+        kv_list<<<((unsigned)a.n_pages / 32u + 256u) / 256u, 256, 0, s>>>(a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
     if (rows) kv_take<<<rows + (unsigned)(a.t.n_seqs * copy_parts), 256, 0, s>>>(a, parts, copy_parts, rows);
     return hipGetLastError();
 }
@@ -489,8 +541,9 @@ __device__ __forceinline__ int count_256(const KvCompact &a, int upto, int32_t *
     return tmp[0] + tmp[1] + tmp[2] + tmp[3];
 }
 
-// Pools of up to this many pages are counted by every workgroup anew (2 KB of bits from the caches), a launch less.
-constexpr int kCountPages = 16384;
+// Pools of up to this many pages (a word of bits a thread) are counted by every workgroup anew, a launch less: of 6000 pages
+// 2100 of 64 KB move in 47.1 us so, in 49.8 after kv_count; of 16000 pages 5600 of 16 KB in 34.7 and 33.2.
+constexpr int kCountPages = 8192;
 
 template <bool COUNT>
 __global__ __launch_bounds__(256) void kv_move(KvCompact a, int parts, int copy_parts, unsigned row_groups, unsigned page_groups) {
@@ -550,6 +603,8 @@ hipError_t launch_kv_compact(const KvCompact &a, hipStream_t s) {
         return hipGetLastError();
     }
     kv_count<<<1, 1024, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     kv_move<false><<<groups, 256, 0, s>>>(a, parts, copy_parts, rows, pages);
     return hipGetLastError();
 }
