@@ -278,58 +278,64 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
     __shared__ RowExps most[kMaxRows];
     __shared__ double inv[kMaxRows];
     __shared__ int arg[kMaxRows];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int nd = a.n_draft[s], per = a.max_draft + 1;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, per = a.max_draft + 1;
+    const double *all_z = reinterpret_cast<const double *>(a.ws + p.off_z);
+    const float *all_m = reinterpret_cast<const float *>(a.ws + p.off_max);
+    const int *all_at = reinterpret_cast<const int *>(a.ws + p.off_arg);
+    // Rows of the target, then of the draft, whether they are needed or not: what their first four have is asked for together
+    // with the number of drafts and the drafted tokens (what was not needed was not written, and is not used below).
+    const int rows = PROBS ? 0 : per + (a.draft ? a.max_draft : 0);
+    auto row_of = [&](int r) { return (r < per ? (int64_t)s * per + r : (int64_t)a.n_seqs * per + (int64_t)s * a.max_draft + (r - per)) * p.chunks; };
+    float m[4];
+    double z[4];
+    int at[4];
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t c = row_of(r0 + 4 * i < rows ? r0 + 4 * i : r0) + (lane < p.chunks ? lane : 0);
+            m[i] = all_m[c];
+            z[i] = all_z[c];
+            at[i] = a.temperature ? all_at[c] : 0x7fffffff;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (lane >= p.chunks) m[i] = -__builtin_inff(), z[i] = 0.0, at[i] = 0x7fffffff;
+    };
+    const int nd = a.n_draft[s];
+    int tok = -1;
+    float u = 0.f;
+    const int64_t row_p = (int64_t)s * per + lane, row_q = (int64_t)s * a.max_draft + lane;
+    if (wave == 0 && lane < a.max_draft) tok = a.tokens[row_q], u = a.u[row_p];
+    if (wave < rows) load(wave);
     if (nd < 0 || nd > a.max_draft) {
         if (threadIdx.x == 0) pick.taken = -1, pick.kind = kFixed, pick.token = -1;
         return;
     }
     const bool greedy = !PROBS && greedy_of(a, s);
     const double k = PROBS ? 0.0 : scale_of(a, s);
-    const double *all_z = reinterpret_cast<const double *>(a.ws + p.off_z);
-    const float *all_m = reinterpret_cast<const float *>(a.ws + p.off_max);
-    const int *all_at = reinterpret_cast<const int *>(a.ws + p.off_arg);
-    // the drafted tokens' values are asked for first: they arrive while the rows are joined
-    int tok = -1;
-    bool known = false;
-    float xt = 0.f, xd = 0.f, u = 0.f;
-    const int64_t row_p = (int64_t)s * per + lane, row_q = (int64_t)s * a.max_draft + lane;
-    if (wave == 0 && lane < nd) {
-        tok = a.tokens[row_q];
-        u = a.u[row_p];
-        known = tok >= 0 && tok < a.n_vocab;
-        if (known && !greedy) {
-            xt = act_to_f32(static_cast<const XT *>(a.target)[row_p * a.ld_target + tok]);
-            if (a.draft) xd = act_to_f32(static_cast<const XT *>(a.draft)[row_q * a.ld_draft + tok]);
-        }
+    // the drafted tokens' values arrive while the rows are joined
+    float xt = 0.f, xd = 0.f;
+    const bool known = lane < nd && tok >= 0 && tok < a.n_vocab;
+    if (known && !greedy) {
+        xt = act_to_f32(static_cast<const XT *>(a.target)[row_p * a.ld_target + tok]);
+        if (a.draft) xd = act_to_f32(static_cast<const XT *>(a.draft)[row_q * a.ld_draft + tok]);
     }
     if (!PROBS) {
         // four rows of a wave side by side: loads, maxima and sums of one wait for memory and for each other
-        const int rows = nd + 1 + (a.draft && !greedy ? nd : 0);
         for (int r0 = wave; r0 < rows; r0 += 16) {
-            int64_t b[4];
-            float m[4], top[4];
-            double z[4];
-            int at[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = r0 + 4 * i < rows ? r0 + 4 * i : r0;
-                b[i] = (r <= nd ? (int64_t)s * per + r : (int64_t)a.n_seqs * per + (int64_t)s * a.max_draft + (r - nd - 1)) * p.chunks;
-                const int64_t c = b[i] + (lane < p.chunks ? lane : 0);
-                m[i] = lane < p.chunks ? all_m[c] : -__builtin_inff();
-                z[i] = lane < p.chunks ? all_z[c] : 0.0;
-                at[i] = greedy && lane < p.chunks ? all_at[c] : 0x7fffffff;
-            }
+            if (r0 != wave) load(r0);
+            float top[4];
             Exps part, all;
             part.scale(k), all.scale(k);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                const int64_t from = row_of(r0 + 4 * i < rows ? r0 + 4 * i : r0);
                 for (int c = lane + 64; c < p.chunks; c += 64) {         // (rows of over 64 chunks)
-                    const float om = all_m[b[i] + c];
-                    const double oz = all_z[b[i] + c];
+                    const float om = all_m[from + c];
+                    const double oz = all_z[from + c];
                     if (greedy) {
                         z[i] += oz;
-                        if (om > m[i]) at[i] = all_at[b[i] + c];         // (chunks of a lane go up: the first of equals stays)
+                        if (om > m[i]) at[i] = all_at[from + c];         // (chunks of a lane go up: the first of equals stays)
                         m[i] = fmaxf(m[i], om);
                     } else {
                         const float most = fmaxf(m[i], om);
@@ -385,7 +391,7 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
             yes = arg[lane] == tok;
         } else {
             const double pt = prob<PROBS>(xt, most[lane], k, inv[lane]);
-            const double qt = !a.draft ? 1.0 : prob<PROBS>(xd, most[nd + 1 + lane], k, inv[nd + 1 + lane]);
+            const double qt = !a.draft ? 1.0 : prob<PROBS>(xd, most[per + lane], k, inv[per + lane]);
             yes = (double)u * qt < pt;
         }
     }
@@ -399,7 +405,7 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
         pick.row_q = (int64_t)s * a.max_draft + j;
         if (!PROBS) {
             pick.p = most[j], pick.inv_p = inv[j];
-            if (j < nd && a.draft && !greedy) pick.q = most[nd + 1 + j], pick.inv_q = inv[nd + 1 + j];
+            if (j < nd && a.draft && !greedy) pick.q = most[per + j], pick.inv_q = inv[per + j];
         }
         if (greedy) pick.kind = kFixed, pick.token = arg[j];
         else if (j == nd) pick.kind = kPlain, pick.token = -1;
@@ -531,13 +537,21 @@ __device__ __forceinline__ void pick_token(const DraftVerify &a, const DraftPlan
     __shared__ int hits[8], found;
     double *tiles = reinterpret_cast<double *>(a.ws + p.off_tiles) + (int64_t)s * p.tiles;
     const float u = a.u[(int64_t)s * (a.max_draft + 1) + a.max_draft];
+    const int64_t place = (int64_t)s * (a.max_draft + 1) + tid;
+    const int drafted = tid < pick.taken ? a.tokens[(int64_t)s * a.max_draft + tid] : -1;
     int kind = pick.kind, result = pick.token;
+    // a thread's tiles, next to each other; their sums stay in registers (8 of them: over a million tokens)
+    constexpr int kHeld = 8;
     const int each = (p.tiles + 255) / 256, t0 = tid * each, t1 = t0 + each < p.tiles ? t0 + each : p.tiles;
     if (kind != kFixed) {
-        double own, run, total;
+        double own, run, total, held[kHeld];
         auto sums = [&]() {
             own = 0.0;
-            for (int t = t0; t < t1; ++t) own += sum_of(tiles + t);
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) held[i] = i < each && t0 + i < t1 ? sum_of(tiles + t0 + i) : 0.0;
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) own += held[i];
+            for (int t = t0 + kHeld; t < t1; ++t) own += sum_of(tiles + t);
             run = run_256(own, wave_sums, total);
         };
         sums();
@@ -557,12 +571,19 @@ __device__ __forceinline__ void pick_token(const DraftVerify &a, const DraftPlan
             const double r = (u > 0.f ? (double)u : 0.0) * total;
             if (tid == thread_at(run, own, r, hits)) {
                 double at = run - own, from = at;
-                for (int t = t0; t < t1; ++t) {
-                    const double v = sum_of(tiles + t);
-                    if (v > 0.0) found = t, before = from = at;
-                    at += v;
-                    if (v > 0.0 && at > r) break;
+                int tile = t0;
+                bool passed = false;
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i) {
+                    if (!passed && held[i] > 0.0) tile = t0 + i, from = at, passed = at + held[i] > r;
+                    at += held[i];
                 }
+                for (int t = t0 + kHeld; t < t1 && !passed; ++t) {
+                    const double v = sum_of(tiles + t);
+                    if (v > 0.0) tile = t, from = at, passed = at + v > r;
+                    at += v;
+                }
+                found = tile, before = from;
             }
             __syncthreads();
             constexpr int kEach = kTile / 256;
@@ -594,9 +615,8 @@ __device__ __forceinline__ void pick_token(const DraftVerify &a, const DraftPlan
         }
     }
     if (tid <= a.max_draft) {
-        const int64_t at = (int64_t)s * (a.max_draft + 1) + tid;
         const int taken = pick.taken;
-        a.out[at] = tid < taken ? a.tokens[(int64_t)s * a.max_draft + tid] : tid == taken ? result : -1;
+        a.out[place] = tid < taken ? drafted : tid == taken ? result : -1;
         if (tid == 0) a.n_accepted[s] = taken < 0 ? 0 : taken;
     }
 }
