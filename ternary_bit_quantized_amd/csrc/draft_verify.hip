@@ -78,13 +78,57 @@ struct Exps : RowExps {
         big = kBig - (whole ? rint(mk) : 0.0);
         low = (whole ? top : 0.f) - d;
     }
-    // 2^(this one's ref - that one's), of a part with values to the whole: at most 1
-    __device__ __forceinline__ double share_of(const Exps &all) const {
-        return exp2_64(off == 0.f && all.off == 0.f ? all.big - big : ((double)m - (double)all.m) * k);
+    // a sum about this part's ref as one about the whole's
+    __device__ __forceinline__ double share_of(double z, const Exps &all) const {
+        if (off == 0.f && all.off == 0.f) return __builtin_amdgcn_ldexp(z, (int)fmax(all.big - big, -4000.0));
+        return z * exp2_64(((double)m - (double)all.m) * k);
     }
 };
 
 __device__ __forceinline__ double nan64() { return __builtin_nan(""); }
+
+// A lane's value (`none` where there is no such lane or the row of 16 is not of ROWS) by the lane moves that need no LDS: CTRL 0x111 ..
+// 0x118 from 1 .. 8 lanes below in the row, 0x142 and 0x143 the last of the row, and of the rows, before.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float lane_move(float v, float none) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v), CTRL, ROWS,
+                                                                 0xf, false));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double lane_move(double v) {
+    const u32x2_t b = __builtin_bit_cast(u32x2_t, v);
+    const uint32_t lo = b.x, hi = b.y;
+    const u32x2_t o = {(uint32_t)__builtin_amdgcn_update_dpp(0, (int)lo, CTRL, ROWS, 0xf, false),
+                       (uint32_t)__builtin_amdgcn_update_dpp(0, (int)hi, CTRL, ROWS, 0xf, false)};
+    return __builtin_bit_cast(double, o);
+}
+// Sums over the lanes up to each, in a fixed order; all 64 lanes.
+__device__ __forceinline__ double lanes_run(double v) {
+    v += lane_move<0x111, 0xf>(v);
+    v += lane_move<0x112, 0xf>(v);
+    v += lane_move<0x114, 0xf>(v);
+    v += lane_move<0x118, 0xf>(v);
+    v += lane_move<0x142, 0xa>(v);
+    v += lane_move<0x143, 0xc>(v);
+    return v;
+}
+__device__ __forceinline__ double last_lane(double v) {
+    const u32x2_t b = __builtin_bit_cast(u32x2_t, v);
+    const uint32_t lo = b.x, hi = b.y;
+    const u32x2_t o = {(uint32_t)__builtin_amdgcn_readlane((int)lo, 63), (uint32_t)__builtin_amdgcn_readlane((int)hi, 63)};
+    return __builtin_bit_cast(double, o);
+}
+__device__ __forceinline__ double wave_sum(double v) { return last_lane(lanes_run(v)); }
+__device__ __forceinline__ float wave_max(float v) {
+    const float none = -__builtin_inff();
+    v = fmaxf(v, lane_move<0x111, 0xf>(v, none));
+    v = fmaxf(v, lane_move<0x112, 0xf>(v, none));
+    v = fmaxf(v, lane_move<0x114, 0xf>(v, none));
+    v = fmaxf(v, lane_move<0x118, 0xf>(v, none));
+    v = fmaxf(v, lane_move<0x142, 0xa>(v, none));
+    v = fmaxf(v, lane_move<0x143, 0xc>(v, none));
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
 
 // log2(e) / temperature, which counts as at most 2^100 and at least 2^-100 (logits would be out of all proportion to it); NaN
 // for one that is not positive.
@@ -200,7 +244,7 @@ __global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
         if (top > m) {
             const Exps before = ex;
             ex.about(top);
-            z = m == -__builtin_inff() ? 0.0 : z * before.share_of(ex);
+            z = m == -__builtin_inff() ? 0.0 : before.share_of(z, ex);
             m = top;
         }
         if (m == -__builtin_inff()) continue;
@@ -213,9 +257,7 @@ __global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
     __shared__ double wz[4];
     __shared__ int warg[4], wbad[4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    float top = m;
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    float top = wave_max(m);
     if (lane == 0) wm[wave] = top;
     __syncthreads();
     top = fmaxf(fmaxf(wm[0], wm[1]), fmaxf(wm[2], wm[3]));
@@ -230,9 +272,8 @@ __global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
     } else {
         const Exps mine = ex;
         ex.about(top);
-        z = m == -__builtin_inff() ? 0.0 : z * mine.share_of(ex);
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) z += __shfl_xor(z, off);
+        z = m == -__builtin_inff() ? 0.0 : mine.share_of(z, ex);
+        z = wave_sum(z);
     }
     const bool any = __ballot(bad) != 0;
     if (lane == 0) wz[wave] = z, wbad[wave] = any;
@@ -266,17 +307,11 @@ __device__ __forceinline__ double prob(float x, const RowExps &e, double k, doub
     return PROBS ? (double)x : e.exact(x, k) * inv;
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
-    return v;
-}
-
 // All threads of the workgroup; the result is in `pick` after a barrier.
 template <typename XT, bool PROBS>
 __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pick) {
     __shared__ RowExps most[kMaxRows];
-    __shared__ double inv[kMaxRows];
+    __shared__ double whole[kMaxRows];           // sums of exponentials
     __shared__ int arg[kMaxRows];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, per = a.max_draft + 1;
     const double *all_z = reinterpret_cast<const double *>(a.ws + p.off_z);
@@ -341,30 +376,25 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
                         const float most = fmaxf(m[i], om);
                         all.about(most);
                         part.about(m[i]);
-                        if (m[i] > -__builtin_inff()) z[i] *= part.share_of(all);
+                        if (m[i] > -__builtin_inff()) z[i] = part.share_of(z[i], all);
                         part.about(om);
-                        z[i] += om > -__builtin_inff() ? oz * part.share_of(all) : oz;
+                        z[i] += om > -__builtin_inff() ? part.share_of(oz, all) : oz;
                         m[i] = most;
                     }
                 }
-                top[i] = m[i];
             }
 #pragma unroll
-            for (int off = 32; off >= 1; off >>= 1)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], __shfl_xor(top[i], off));
+            for (int i = 0; i < 4; ++i) top[i] = wave_max(m[i]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 all.about(top[i]);
                 part.about(m[i]);
                 // (a chunk of NaN: its sum is NaN and stays so)
-                if (!greedy && m[i] > -__builtin_inff()) z[i] *= part.share_of(all);
+                if (!greedy && m[i] > -__builtin_inff()) z[i] = part.share_of(z[i], all);
                 at[i] = m[i] == top[i] ? at[i] : 0x7fffffff;
             }
 #pragma unroll
-            for (int off = 32; off >= 1; off >>= 1)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) z[i] += __shfl_xor(z[i], off);
+            for (int i = 0; i < 4; ++i) z[i] = wave_sum(z[i]);
             if (greedy)
 #pragma unroll
                 for (int off = 32; off >= 1; off >>= 1)
@@ -378,7 +408,7 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
                 if (lane == 0 && r0 + 4 * i < rows) {
                     all.about(top[i]);
                     most[r0 + 4 * i] = all;
-                    inv[r0 + 4 * i] = z[i] > 0.0 && z[i] < __builtin_inf() ? 1.0 / z[i] : nan64();
+                    whole[r0 + 4 * i] = z[i] > 0.0 && z[i] < __builtin_inf() ? z[i] : nan64();
                     arg[r0 + 4 * i] = z[i] == z[i] && top[i] > -__builtin_inff() ? at[i] : -1;
                 }
         }
@@ -390,9 +420,11 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
         if (greedy) {
             yes = arg[lane] == tok;
         } else {
-            const double pt = prob<PROBS>(xt, most[lane], k, inv[lane]);
-            const double qt = !a.draft ? 1.0 : prob<PROBS>(xd, most[per + lane], k, inv[per + lane]);
-            yes = (double)u * qt < pt;
+            // u q < p, by the sums in place of their quotients
+            const double pt = prob<PROBS>(xt, most[lane], k, 1.0), sp = PROBS ? 1.0 : whole[lane];
+            const double qt = !a.draft ? 1.0 : prob<PROBS>(xd, most[per + lane], k, 1.0);
+            const double sq = !a.draft || PROBS ? 1.0 : whole[per + lane];
+            yes = (double)u * qt * sp < pt * sq;
         }
     }
     const uint64_t no = __ballot(!yes);                  // (lanes from nd on: not taken)
@@ -404,8 +436,8 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
         pick.row_p = (int64_t)s * per + j;
         pick.row_q = (int64_t)s * a.max_draft + j;
         if (!PROBS) {
-            pick.p = most[j], pick.inv_p = inv[j];
-            if (j < nd && a.draft && !greedy) pick.q = most[per + j], pick.inv_q = inv[per + j];
+            pick.p = most[j], pick.inv_p = 1.0 / whole[j];
+            if (j < nd && a.draft && !greedy) pick.q = most[per + j], pick.inv_q = 1.0 / whole[per + j];
         }
         if (greedy) pick.kind = kFixed, pick.token = arg[j];
         else if (j == nd) pick.kind = kPlain, pick.token = -1;
@@ -498,11 +530,7 @@ __device__ __forceinline__ void sums_done() {
 // Running sums over the 256 threads in their order: the sum up to the thread itself; `total`: all.
 __device__ __forceinline__ double run_256(double v, double *wave_sums, double &total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const double o = __shfl_up(v, off);
-        if (lane >= off) v += o;
-    }
+    v = lanes_run(v);
     __syncthreads();                                     // (wave_sums may be read still)
     if (lane == 63) wave_sums[wave] = v;
     __syncthreads();
