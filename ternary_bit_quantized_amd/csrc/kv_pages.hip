@@ -84,23 +84,20 @@ static int col_parts(int64_t cols) { return (int)((cols + kCols - 1) / kCols); }
 
 int64_t kv_table_groups(int64_t n_rows, int64_t cols) { return n_rows * col_parts(cols); }
 
-// Sum over the workgroup of 1024 of the values of lower threads; `total`: of all.
+// Sum over the workgroup of 1024 of the values of lower threads; `total`: of all.  Counts that may pass 2^31 are doubles (exact
+// up to 2^53).
 template <typename T>
-__device__ __forceinline__ T scan_1024(T v, T *tmp, T &total) {
+__device__ __forceinline__ T scan_1024(T v, double *tmp, T &total) {
+    T *sums = reinterpret_cast<T *>(tmp);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    T run = v;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const T o = __shfl_up(run, off);
-        if (lane >= off) run += o;
-    }
-    if (lane == 63) tmp[wave] = run;
+    const T run = lanes_run(v);
+    if (lane == 63) sums[wave] = run;
     __syncthreads();
     T base = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < 16; ++w) {
         if (w == wave) base = all;
-        all += tmp[w];
+        all += sums[w];
     }
     __syncthreads();
     total = all;
@@ -112,27 +109,27 @@ __device__ __forceinline__ T scan_1024(T v, T *tmp, T &total) {
 // loads and counts of each wait for the one before.)  `ends` holds 1024 * PT numbers in shared memory.
 constexpr int kAtOnce = 8;
 template <int PT, typename F>
-__device__ __forceinline__ void each_of(const int (&count)[PT], int *ends, int64_t *tmp, F &&f) {
-    int64_t sum = 0, total;
+__device__ __forceinline__ void each_of(const int (&count)[PT], int *ends, double *tmp, F &&f) {
+    int sum = 0, total;              // (of a small table)
 #pragma unroll
     for (int i = 0; i < PT; ++i) sum += count[i];
-    int64_t at = scan_1024(sum, tmp, total);
+    int at = scan_1024(sum, tmp, total);
     if (total == 0) return;                                      // (uniform)
 #pragma unroll
     for (int i = 0; i < PT; ++i) {
         at += count[i];
-        ends[threadIdx.x * PT + i] = (int)at;
+        ends[threadIdx.x * PT + i] = at;
     }
     __syncthreads();
-    for (int from = 0; from < (int)total; from += 1024 * kAtOnce) {
+    for (int from = 0; from < total; from += 1024 * kAtOnce) {
         int owner[kAtOnce], thing[kAtOnce];
         bool in[kAtOnce];
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
             const int e = from + 1024 * k + (int)threadIdx.x;
-            in[k] = e < (int)total;
+            in[k] = e < total;
             owner[k] = thing[k] = 0;
-            if (from + 1024 * k >= (int)total) continue;         // (uniform)
+            if (from + 1024 * k >= total) continue;         // (uniform)
             int lo = 0;                                          // owners that end at or before e
 #pragma unroll
             for (int step = 512 * PT; step >= 1; step >>= 1)
@@ -155,7 +152,7 @@ constexpr int64_t kOneGroup = 65536;
 
 template <bool ROWS>
 __global__ __launch_bounds__(1024) void kv_fork_plan(KvFork a) {
-    __shared__ int64_t tmp[16];
+    __shared__ double tmp[16];
     __shared__ int ends[1024];
     const int64_t most = (int64_t)a.t.cols * a.page.d;
     for (int i = threadIdx.x; i < a.n; i += 1024) {
@@ -286,7 +283,7 @@ static_assert(sizeof(Planned) == 32, "8 numbers a sequence");
 // claim on the count is the one that stays.
 template <int PT, bool DROP>
 __global__ __launch_bounds__(1024) void kv_plan(KvResize a) {
-    __shared__ int64_t tmp[16];
+    __shared__ double tmp[16];
     __shared__ int ends[DROP ? 1024 * PT : 1];
     __shared__ uint32_t held[kHeldWords];
     const int64_t most = (int64_t)a.t.cols * a.shape.page.d;
@@ -329,17 +326,8 @@ __global__ __launch_bounds__(1024) void kv_plan(KvResize a) {
         });
         all_done();
     }
-    // free pages; their bits stay in shared memory for the list, as far as that reaches
-    const int words = (a.n_pages + 31) / 32;
-    int64_t some = 0;
-#pragma unroll
-    for (int j = 0; j < kHeldWords / 1024; ++j) {
-        const int w = j * 1024 + tid;
-        const uint32_t bits = w < words ? free_bits(a, w) : 0u;
-        held[w] = bits;
-        some += __popc(bits);
-    }
-    for (int w = kHeldWords + tid; w < words; w += 1024) some += __popc(free_bits(a, w));
+    // the pages that growing sequences are inside of, and the free ones: asked for together
+    int tail[PT];
 #pragma unroll
     for (int i = 0; i < PT; ++i) {
         const int s = tid * PT + i;
@@ -349,13 +337,25 @@ __global__ __launch_bounds__(1024) void kv_plan(KvResize a) {
         pl[i].want = grows[i] ? pages_of(a.shape.page, now[i]) : pl[i].have;
         pl[i].rows = ok && pl[i].have > 0 ? len[i] - (pl[i].have - 1) * (int)a.shape.page.d : 0;
         pl[i].old = -1;
+        tail[i] = grows[i] && pl[i].rows > 0 && pl[i].rows < (int)a.shape.page.d ? a.t.table[s * a.t.ld + pl[i].have - 1] : -1;
+    }
+    const int words = (a.n_pages + 31) / 32;
+    uint32_t bits[kHeldWords / 1024];
+#pragma unroll
+    for (int j = 0; j < kHeldWords / 1024; ++j) bits[j] = j * 1024 + tid < words ? free_bits(a, j * 1024 + tid) : 0u;
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
         count[i] = 0;
-        if (grows[i] && pl[i].rows > 0 && pl[i].rows < (int)a.shape.page.d) {
-            const int page = a.t.table[s * a.t.ld + pl[i].have - 1];
-            if (page >= 0 && page < a.n_pages) pl[i].old = page, count[i] = peek(a.ref + page);
-        }
+        if (tail[i] >= 0 && tail[i] < a.n_pages) pl[i].old = tail[i], count[i] = peek(a.ref + tail[i]);
         shared[i] = count[i] > 1;
     }
+    int some = 0;                                                // (the bits stay in shared memory for the list, as far as that reaches)
+#pragma unroll
+    for (int j = 0; j < kHeldWords / 1024; ++j) {
+        held[j * 1024 + tid] = bits[j];
+        some += __popc(bits[j]);
+    }
+    for (int w = kHeldWords + tid; w < words; w += 1024) some += __popc(free_bits(a, w));
     bool any = false;
 #pragma unroll
     for (int i = 0; i < PT; ++i) left[i] = 1, keeps[i] = false, any |= shared[i];
@@ -376,15 +376,15 @@ __global__ __launch_bounds__(1024) void kv_plan(KvResize a) {
 #pragma unroll
         for (int i = 0; i < PT; ++i) keeps[i] = left[i] == 0 && peek(a.ref + pl[i].old) == tid * PT + i - a.t.n_seqs;
     }
-    int64_t need = 0;
+    double need = 0.0, total;
 #pragma unroll
-    for (int i = 0; i < PT; ++i) need += pl[i].want - pl[i].have + (shared[i] && !keeps[i]);
-    int64_t total;
-    int64_t slot = scan_1024(need, tmp, total);
-    int64_t avail;
+    for (int i = 0; i < PT; ++i) need += (double)(pl[i].want - pl[i].have + (shared[i] && !keeps[i]));
+    const double before = scan_1024(need, tmp, total);
+    int avail;
     scan_1024(some, tmp, avail);
-    const bool enough = total <= avail;
-    if (tid == 0) *a.missing = enough ? 0 : (int)(total - avail < 0x7fffffff ? total - avail : 0x7fffffff);
+    const bool enough = total <= (double)avail;
+    if (tid == 0) *a.missing = enough ? 0 : total - avail < 2147483647.0 ? (int)(total - avail) : 2147483647;
+    int slot = enough ? (int)before : 0;                         // (at most n_pages)
 #pragma unroll
     for (int i = 0; i < PT; ++i) {
         const int s = tid * PT + i;
@@ -393,8 +393,8 @@ __global__ __launch_bounds__(1024) void kv_plan(KvResize a) {
         if (copies && left[i] > 0 && !enough) atomicAdd(a.ref + pl[i].old, 1);
         if (s >= a.t.n_seqs) continue;
         if (now[i] != len[i] && (enough || !grows[i])) a.t.lens[s] = now[i];
-        pl[i].slot = enough ? (int)slot : 0;
-        slot += pl[i].want - pl[i].have + copies;
+        pl[i].slot = slot;
+        if (enough) slot += pl[i].want - pl[i].have + copies;
         if (!copies || !enough) pl[i].old = -1;
         if (!enough) pl[i].want = pl[i].have;
         reinterpret_cast<Planned *>(a.plan)[s] = pl[i];
@@ -407,7 +407,7 @@ __global__ __launch_bounds__(1024) void kv_plan(KvResize a) {
         const int w = w0 + tid;
         const uint32_t bits = w0 < kHeldWords ? held[w] : w < words ? free_bits(a, w) : 0u;
         int all;
-        const int at = base + scan_1024((int)__popc(bits), reinterpret_cast<int *>(tmp), all);
+        const int at = base + scan_1024((int)__popc(bits), tmp, all);
         if (DROP) list_word(a, w, bits, at, take);
         else if (w < words) a.before[w] = at;
         base += all;
@@ -482,17 +482,17 @@ __device__ __forceinline__ uint32_t used_bits(const KvCompact &a, int w) {
 }
 
 __global__ __launch_bounds__(1024) void kv_count(KvCompact a) {
-    __shared__ int64_t tmp[16];
+    __shared__ double tmp[16];
     const int words = (a.from_pages + 31) / 32;
-    int64_t base = 0;
+    int base = 0;
     for (int w0 = 0; w0 < words; w0 += 1024) {
         const int w = w0 + (int)threadIdx.x;
-        int64_t all;
-        const int64_t at = scan_1024((int64_t)(w < words ? __popc(used_bits(a, w)) : 0), tmp, all);
-        if (w < words) a.before[w] = (int)(base + at);
+        int all;
+        const int at = scan_1024(w < words ? (int)__popc(used_bits(a, w)) : 0, tmp, all);
+        if (w < words) a.before[w] = base + at;
         base += all;
     }
-    if (threadIdx.x == 0) *a.n_used = (int)base;
+    if (threadIdx.x == 0) *a.n_used = base;
 }
 
 // The new number of a page in use: pages in use before it.
@@ -516,14 +516,9 @@ __device__ __forceinline__ int count_256(const KvCompact &a, int upto, int32_t *
     }
     int run = own;
     if (all) {
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const int o = __shfl_up(run, off);
-            if (lane >= off) run += o;
-        }
+        run = lanes_run(run);
     } else {
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) run += __shfl_xor(run, off), low += __shfl_xor(low, off);
+        run = lanes_run(run), low = lanes_run(low);              // (the last lane's are the wave's)
     }
     if (lane == 63) tmp[wave] = run, tmp[4 + wave] = low;
     __syncthreads();

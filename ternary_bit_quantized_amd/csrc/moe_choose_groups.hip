@@ -35,12 +35,6 @@ __device__ __forceinline__ uint64_t read_lane64(uint64_t v, int lane) {
     return (uint64_t)hi << 32 | lo;
 }
 
-__device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
-    return v;
-}
-
 // e^x to some 10^-15 of itself: 2^n 2^r with n = rint(x log2 e) from the low bits of x log2 e + 1.5 2^52, r in [-1/2, 1/2]
 // and the polynomial of degree 10 that meets 2^r at the Chebyshev points.  NaN stays NaN; 17 instructions, where the
 // library's function takes 45.
@@ -119,7 +113,7 @@ __global__ __launch_bounds__(256) void moe_choose_groups(ChooseGroups a) {
             s[i] = exp64((double)v[i] - m);
             sum += s[i];
         }
-        sum = wave_sum_f64(sum);
+        sum = wave_sum(sum);
         inv = sum == 0.0 ? 0.0 : 1.0 / sum;
 #pragma unroll
         for (int i = 0; i < PL; ++i) s[i] *= inv;

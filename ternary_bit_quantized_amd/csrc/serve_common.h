@@ -6,6 +6,53 @@
 
 namespace q2_0 {
 
+// ---- lanes
+// A lane's value (`none` where there is no such lane or the row of 16 is not of ROWS) by the lane moves that need no LDS: CTRL 0x111 ..
+// 0x118 from 1 .. 8 lanes below in the row, 0x142 and 0x143 the last of the row, and of the rows, before.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float lane_move(float v, float none) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v), CTRL, ROWS,
+                                                                 0xf, false));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double lane_move(double v) {
+    const u32x2_t b = __builtin_bit_cast(u32x2_t, v);
+    const uint32_t lo = b.x, hi = b.y;
+    const u32x2_t o = {(uint32_t)__builtin_amdgcn_update_dpp(0, (int)lo, CTRL, ROWS, 0xf, false),
+                       (uint32_t)__builtin_amdgcn_update_dpp(0, (int)hi, CTRL, ROWS, 0xf, false)};
+    return __builtin_bit_cast(double, o);
+}
+// Sums over the lanes up to each, in a fixed order; all 64 lanes.
+__device__ __forceinline__ double lanes_run(double v) {
+    v += lane_move<0x111, 0xf>(v);
+    v += lane_move<0x112, 0xf>(v);
+    v += lane_move<0x114, 0xf>(v);
+    v += lane_move<0x118, 0xf>(v);
+    v += lane_move<0x142, 0xa>(v);
+    v += lane_move<0x143, 0xc>(v);
+    return v;
+}
+__device__ __forceinline__ double last_lane(double v) {
+    const u32x2_t b = __builtin_bit_cast(u32x2_t, v);
+    const uint32_t lo = b.x, hi = b.y;
+    const u32x2_t o = {(uint32_t)__builtin_amdgcn_readlane((int)lo, 63), (uint32_t)__builtin_amdgcn_readlane((int)hi, 63)};
+    return __builtin_bit_cast(double, o);
+}
+__device__ __forceinline__ double wave_sum(double v) { return last_lane(lanes_run(v)); }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int lane_move(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ int lanes_run(int v) {
+    v += lane_move<0x111, 0xf>(v);
+    v += lane_move<0x112, 0xf>(v);
+    v += lane_move<0x114, 0xf>(v);
+    v += lane_move<0x118, 0xf>(v);
+    v += lane_move<0x142, 0xa>(v);
+    v += lane_move<0x143, 0xc>(v);
+    return v;
+}
+
 // ---- expert choice in groups
 struct ChooseGroups {
     const void *logits;
