@@ -478,14 +478,16 @@ __device__ __forceinline__ double tile_sum(const DraftVerify &a, const Pick &pic
     return wave_sum(sum);
 }
 
-// Tile sums go from the workgroups that make them to the one that reads them by atomics of the whole device alone, which meet
-// in one memory whatever the dies' caches hold.  A fence for the device instead would write back and drop a cache for
-// every workgroup: 1280 of them took 155 us in place of 25.
+// Tile sums go from the workgroups that make them to the one that reads them by exchanges with memory alone, as their count
+// does: written and read where all of the device's atomics meet, whatever the dies' caches hold.  A fence for the device
+// instead would write back and drop a cache for every workgroup: 1280 of them took 155 us in place of 25.
 __device__ __forceinline__ void put_sum(double *p, double v) {
     __hip_atomic_exchange(reinterpret_cast<uint64_t *>(p), __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ double sum_of(const double *p) {
-    return __builtin_bit_cast(double, __hip_atomic_load(reinterpret_cast<const uint64_t *>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+__device__ __forceinline__ double sum_of(double *p) {
+    uint64_t none = 0;
+    asm volatile("" : "+v"(none));       // (the compiler makes a load of an exchange that it sees to change nothing)
+    return __builtin_bit_cast(double, __hip_atomic_fetch_or(reinterpret_cast<uint64_t *>(p), none, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
 }
 // All threads: the workgroup's atomics have been performed.
 __device__ __forceinline__ void sums_done() {
