@@ -12,6 +12,10 @@
 // Groups: where one is the keys of 1, 2, 4 .. lanes, those exchange their two best (8 groups of 32 experts: 3 steps);
 // else the keys go through LDS and lane g looks through group g.  A group's rank is the number of groups before it, counted
 // with a lane read of each.
+//
+// What bounds it: a launch and the rounds' dependent steps for few tokens (8 of 128 experts: 5.0 us for one token in a
+// graph); instruction issue for many: 4096 tokens of 256 experts take 11.3 us, some 950 instructions a token of which 440 are
+// the 8 rounds, where their 4.5 MB would take 0.9.
 #include <type_traits>
 
 #include "serve_common.h"
