@@ -27,6 +27,7 @@ namespace q2_0 {
 
 constexpr int kMaxRows = 2 * Q2_0_DRAFT_MAX + 1;
 constexpr int kTile = 512;            // tokens of a tile sum (of 1024: one chat 1.6 us more, 64 sequences 1.3 less)
+constexpr int kCountEvery = 32;       // counters of sequences in lines of their own: side by side 400 workgroups wait 2 us for 16
 constexpr int kPass = 4096;           // values of a workgroup's pass: 16 a thread
 
 // 2^r for r in [-1/2, 1/2]: the polynomial of degree 8 that meets it at the Chebyshev points (relative error 1.1e-12).
@@ -60,16 +61,16 @@ __device__ __forceinline__ double exp2_64(double y) {
 struct RowExps {
     double big;            // kBig - ref
     float off, low;        // values below `low`, 2^-1000 of the largest, count nothing
-    // for sums: 2^-1000 and less count as that
+    // for sums: 2^-1000 and less count as that; x less `off` already
     __device__ __forceinline__ double of(float x, double k) const {
-        const double v = (double)fmaxf(x - off, low);
+        const double v = (double)__builtin_elementwise_maximum(x, low);      // (NaN stays; fmaxf would take two instructions)
         const double t = fma(v, k, big);
         u32x2_t e = __builtin_bit_cast(u32x2_t, exp2_frac(fma(v, k, -(t - big))));
         e.y += (uint32_t)__builtin_bit_cast(uint64_t, t) << 20;
         return __builtin_bit_cast(double, e);
     }
     __device__ __forceinline__ double exact(float x, double k) const {
-        const double v = of(x, k);
+        const double v = of(x - off, k);
         return x - off < low ? 0.0 : v;
     }
 };
@@ -114,6 +115,11 @@ __device__ __forceinline__ double scale_of(const DraftVerify &a, int s) {
 }
 
 __device__ __forceinline__ bool greedy_of(const DraftVerify &a, int s) { return a.temperature && a.temperature[s] == 0.f; }
+
+// The largest of three, NaN if one is: one instruction that finds both.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
+}
 
 template <typename XT>
 struct Vec {                          // 16 bytes of a row
@@ -177,7 +183,7 @@ __global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
     const bool is_draft = b >= n_target;
     const int s = is_draft ? (b - n_target) / a.max_draft : b / per;
     const int j = is_draft ? (b - n_target) % a.max_draft : b % per;
-    if (!is_draft && j == 0 && c == 0 && threadIdx.x == 0) reinterpret_cast<int *>(a.ws + p.off_done)[s] = 0;
+    if (!is_draft && j == 0 && c == 0 && threadIdx.x == 0) reinterpret_cast<int *>(a.ws + p.off_done)[s * kCountEvery] = 0;
     const int nd = a.n_draft[s];
     if (nd < 0 || nd > a.max_draft || j >= nd + (is_draft ? 0 : 1)) return;
     const bool greedy = greedy_of(a, s);
@@ -201,10 +207,8 @@ __global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
 #pragma unroll
         for (int i = 0; i < Vec<XT>::each; ++i)
 #pragma unroll
-            for (int e = 0; e < VE; e += 2) {
-                top = fmaxf(fmaxf(x[i].x[e], x[i].x[e + 1]), top);
-                bad |= __builtin_isunordered(x[i].x[e], x[i].x[e + 1]);
-            }
+            for (int e = 0; e < VE; e += 2) top = max3(top, x[i].x[e], x[i].x[e + 1]);
+        bad |= top != top;
         if (greedy) {
             if (top > m) {
                 m = top;
@@ -223,10 +227,17 @@ __global__ __launch_bounds__(256) void draft_stats(DraftVerify a, DraftPlan p) {
             m = top;
         }
         if (m == -__builtin_inff()) continue;
+        if (ex.off == 0.f) {
 #pragma unroll
-        for (int i = 0; i < Vec<XT>::each; ++i)
+            for (int i = 0; i < Vec<XT>::each; ++i)
 #pragma unroll
-            for (int e = 0; e < VE; ++e) z += ex.of(x[i].x[e], ex.k);
+                for (int e = 0; e < VE; ++e) z += ex.of(x[i].x[e], ex.k);
+        } else {
+#pragma unroll
+            for (int i = 0; i < Vec<XT>::each; ++i)
+#pragma unroll
+                for (int e = 0; e < VE; ++e) z += ex.of(x[i].x[e] - ex.off, ex.k);
+        }
     }
     __shared__ float wm[4];
     __shared__ double wz[4];
@@ -648,7 +659,7 @@ __global__ __launch_bounds__(256, 5) void draft_sums(DraftVerify a, DraftPlan p)
     if (PROBS) return;
     sums_done();
     if (threadIdx.x == 0)
-        last = __hip_atomic_fetch_add(reinterpret_cast<int *>(a.ws + p.off_done) + s, 1, __ATOMIC_RELAXED,
+        last = __hip_atomic_fetch_add(reinterpret_cast<int *>(a.ws + p.off_done) + s * kCountEvery, 1, __ATOMIC_RELAXED,
                                       __HIP_MEMORY_SCOPE_AGENT) == p.sum_parts - 1;
     sums_done();
     if (!last) return;
@@ -688,7 +699,7 @@ DraftPlan draft_plan(int64_t n_seqs, int64_t max_draft, int64_t n_vocab, bool ha
     p.off_max = take((size_t)p.stat_groups * 4);
     p.off_arg = take((size_t)p.stat_groups * 4);
     p.off_tiles = take((size_t)n_seqs * p.tiles * 8);
-    p.off_done = take((size_t)n_seqs * 4);
+    p.off_done = take((size_t)n_seqs * kCountEvery * 4);
     p.off_pick = take((size_t)n_seqs * sizeof(Pick));
     p.ws_bytes = at;
     return p;
