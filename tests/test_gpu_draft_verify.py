@@ -131,6 +131,19 @@ def test_shapes(n, most, v):
     check(*case(n, most, v, "bf16", has_draft=False, seed=n + 1))
 
 
+@pytest.mark.parametrize("v", [300000, 1300001])
+def test_large_vocabularies(v):
+    """More parts of a row than lanes, and more tiles than threads hold, greedy and not."""
+    import torch
+    target, draft, tokens, n_draft, u = case(3, 1, v, seed=v)
+    n_draft.fill_(1)
+    temp = torch.tensor([0.0, 0.8, 0.0], device="cuda")
+    tokens[0] = target.view(3, 2, v)[0, 0].argmax().int()
+    check(target, draft, tokens, n_draft, u, temp=temp)
+    check(target, None, tokens, n_draft, u, temp=temp)
+    check(torch.softmax(target, 1), torch.softmax(draft, 1), tokens, n_draft, u, form="probs")
+
+
 def test_many_passes_a_chunk():
     """Enough rows that a workgroup takes several passes over its part of a row."""
     target, draft, tokens, n_draft, u = case(48, 7, 40000, "f32", seed=5)

@@ -251,7 +251,7 @@ def test_a_pool_at_random():
         assert counts == t.m.ref and t.m.free == {p for p in range(n_pages) if counts[p] == 0}
 
 
-@pytest.mark.parametrize("n_seqs,cols", [(1, 3000), (1024, 3), (1025, 2), (8192, 2), (300, 1100)])
+@pytest.mark.parametrize("n_seqs,cols", [(1, 3000), (1024, 3), (1025, 2), (8192, 2), (300, 1100), (2000, 50)])
 def test_many_sequences_and_long_rows(n_seqs, cols):
     import torch
     page, n_pages = 4, min(400000, n_seqs * cols + 77)
@@ -270,6 +270,19 @@ def test_many_sequences_and_long_rows(n_seqs, cols):
     t.fork([a for a, _ in pairs], [b for _, b in pairs])
     t.resize(new)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("n_seqs,cols", [(3, 8), (80, 1000)])
+def test_free_pages_far_up_in_a_large_pool(n_seqs, cols):
+    """The first 208000 pages are the caller's own (no holder, not free)."""
+    t = Both(n_pages=250000, n_seqs=n_seqs, cols=cols, page=1, n_kv=1)
+    t.free[:6500] = 0
+    t.m.free = set(range(6500 * 32, 250000))
+    t.resize([5] + [0] * (n_seqs - 2) + [cols])
+    t.resize([3] + [2] * (n_seqs - 2) + [cols // 2])
+    t.fork([0], [0])
+    t.resize([cols] * n_seqs)
+    assert t.resize([0] * n_seqs) == 0 and len(t.m.free) == 250000 - 6500 * 32
 
 
 def test_workspaces_of_any_content():
@@ -341,7 +354,7 @@ def test_pages_past_32_bit_offsets():
 # ---------------------------------------------------------------------------- compact
 
 @pytest.mark.parametrize("n_pages,to_pages,layout", [(70, 40, "heads"), (64, 200, "tokens"), (31, 31, "beside"), (1, 1, "heads"),
-                                                     (5000, 3001, "heads")])
+                                                     (5000, 3001, "heads"), (8192, 700, "tokens"), (8193, 9000, "heads")])
 def test_compact(n_pages, to_pages, layout):
     import torch
     r = random.Random(n_pages)
