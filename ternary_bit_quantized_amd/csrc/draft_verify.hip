@@ -16,11 +16,12 @@
 // Given probabilities need no statistics, and find the token in a launch of its own (draft_pick).  All sums are in a fixed
 // order: results are the same in every run.
 //
-// What bounds it, in a graph.  64 sequences of 4 drafts over 151936 f32 logits, 350 MB: 88 us, of them 60 the
+// What bounds it, in a graph.  64 sequences of 4 drafts over 151936 f32 logits, 350 MB: 90 us, of them 60 the
 // statistics, whose 64-bit instructions (13 an exponential) alone take 58 and whose loads alone 43 (6.5 TB/s for the 283 MB that
 // are needed), and 29 the tile sums (deciding 7.6, two rows' exponentials 11, the token 3).  One sequence of them: 15.2 us,
 // two launches of dependent steps: deciding 4, a tile 1.8, the token 3.  16 sequences of 5 found drafts over 50001 bfloat16
-// logits 21 us; 32 of 3 given probabilities over 32003, 7.7 us.
+// logits 18 us; 32 of 3 given probabilities over 32003, 7.8 us.  (The statistics' loads are non-temporal: 64 sequences 76.7 us
+// a pass with other work between, 80.5 with plain ones.)
 #include "serve_common.h"
 
 namespace q2_0 {
