@@ -710,17 +710,10 @@ hipError_t launch_draft_verify(const DraftVerify &a, const DraftPlan &p, Act xt,
     return with_act(xt, [&](auto tag) -> hipError_t {
         using XT = decltype(tag);
         const unsigned sums = (unsigned)p.sum_groups, seqs = (unsigned)a.n_seqs;
-        hipError_t e = hipSuccess;                               // nothing runs after a launch that failed
-        if (probs) {
-            draft_sums<XT, true><<<sums, 256, 0, s>>>(a, p);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-            draft_pick<XT><<<seqs, 256, 0, s>>>(a, p);
-        } else {
-            draft_stats<XT><<<(unsigned)p.stat_groups, 256, 0, s>>>(a, p);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-            draft_sums<XT, false><<<sums, 256, 0, s>>>(a, p);
-        }
-        return hipGetLastError();
+        const hipError_t e = probs ? launch(draft_sums<XT, true>, sums, 256, 0, s, a, p)
+                                   : launch(draft_stats<XT>, (unsigned)p.stat_groups, 256, 0, s, a, p);
+        if (e != hipSuccess) return e;                           // nothing runs after a launch that failed
+        return probs ? launch(draft_pick<XT>, seqs, 256, 0, s, a, p) : launch(draft_sums<XT, false>, sums, 256, 0, s, a, p);
     });
 }
 

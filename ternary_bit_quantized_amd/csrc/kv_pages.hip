@@ -77,8 +77,7 @@ __global__ __launch_bounds__(256) void kv_copy_pages(KvCopy a, int parts) {
 int64_t kv_copy_groups(const PageShape &p, int64_t n) { return n * parts_of(p); }
 
 hipError_t launch_kv_copy(const KvCopy &a, hipStream_t s) {
-    kv_copy_pages<<<(unsigned)kv_copy_groups(a.shape, a.n), 256, 0, s>>>(a, parts_of(a.shape));
-    return hipGetLastError();
+    return launch(kv_copy_pages, (unsigned)kv_copy_groups(a.shape, a.n), 256, 0, s, a, parts_of(a.shape));
 }
 
 // ---------------------------------------------------------------------------- shared by rows of tables
@@ -212,16 +211,10 @@ __global__ __launch_bounds__(256) void kv_fork_rows(KvFork a, int parts) {
 }
 
 hipError_t launch_kv_fork(const KvFork &a, hipStream_t s) {
-    if (a.n <= 1024 && (int64_t)a.n * a.t.cols <= kOneGroup) {
-        kv_fork_plan<true><<<1, 1024, 0, s>>>(a);
-        return hipGetLastError();
-    }
-    kv_fork_plan<false><<<1, 1024, 0, s>>>(a);
-    const hipError_t e = hipGetLastError();                      // (nothing runs on a plan that was not made)
-    if (e != hipSuccess) return e;
-    if (a.t.cols > 0)
-        kv_fork_rows<<<(unsigned)kv_table_groups(a.n, a.t.cols), 256, 0, s>>>(a, col_parts(a.t.cols));
-    return hipGetLastError();
+    if (a.n <= 1024 && (int64_t)a.n * a.t.cols <= kOneGroup) return launch(kv_fork_plan<true>, 1, 1024, 0, s, a);
+    const hipError_t e = launch(kv_fork_plan<false>, 1, 1024, 0, s, a);
+    if (e != hipSuccess || a.t.cols == 0) return e;              // (nothing runs on a plan that was not made)
+    return launch(kv_fork_rows, (unsigned)kv_table_groups(a.n, a.t.cols), 256, 0, s, a, col_parts(a.t.cols));
 }
 
 // ---------------------------------------------------------------------------- resize
@@ -462,21 +455,13 @@ hipError_t launch_kv_resize(const KvResize &a, hipStream_t s) {
     const bool one = (int64_t)a.t.n_seqs * a.t.cols <= kOneGroup;
     constexpr int kMany = kResizeMaxSeqs / 1024;
     hipError_t e = hipSuccess;                                   // nothing runs after a launch that failed
-    if (!one) {
-        kv_drop<<<rows, 256, 0, s>>>(a, parts);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    if (a.t.n_seqs <= 1024 && one) kv_plan<1, true><<<1, 1024, 0, s>>>(a);
-    else if (a.t.n_seqs <= 1024) kv_plan<1, false><<<1, 1024, 0, s>>>(a);
-    else if (one) kv_plan<kMany, true><<<1, 1024, 0, s>>>(a);
-    else kv_plan<kMany, false><<<1, 1024, 0, s>>>(a);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (!one) {
-        kv_list<<<((unsigned)a.n_pages / 32u + 256u) / 256u, 256, 0, s>>>(a);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    if (rows) kv_take<<<rows + (unsigned)(a.t.n_seqs * copy_parts), 256, 0, s>>>(a, parts, copy_parts, rows);
-    return hipGetLastError();
+    if (!one && (e = launch(kv_drop, rows, 256, 0, s, a, parts)) != hipSuccess) return e;
+    if (a.t.n_seqs <= 1024) e = launch(one ? kv_plan<1, true> : kv_plan<1, false>, 1, 1024, 0, s, a);
+    else e = launch(one ? kv_plan<kMany, true> : kv_plan<kMany, false>, 1, 1024, 0, s, a);
+    if (e != hipSuccess) return e;
+    if (!one && (e = launch(kv_list, ((unsigned)a.n_pages / 32u + 256u) / 256u, 256, 0, s, a)) != hipSuccess) return e;
+    if (rows == 0) return hipSuccess;
+    return launch(kv_take, rows + (unsigned)(a.t.n_seqs * copy_parts), 256, 0, s, a, parts, copy_parts, rows);
 }
 
 // ---------------------------------------------------------------------------- compact
@@ -598,15 +583,10 @@ hipError_t launch_kv_compact(const KvCompact &a, hipStream_t s) {
     const unsigned rows = (unsigned)kv_table_groups(a.t.n_seqs, a.t.cols);
     const unsigned pages = a.to_pages ? ((unsigned)a.to_pages + 255u) / 256u : 1u;    // (one writes n_used)
     const unsigned groups = rows + pages + (unsigned)a.from_pages * (unsigned)copy_parts;
-    if (a.from_pages <= kCountPages) {
-        kv_move<true><<<groups, 256, 0, s>>>(a, parts, copy_parts, rows, pages);
-        return hipGetLastError();
-    }
-    kv_count<<<1, 1024, 0, s>>>(a);
-    const hipError_t e = hipGetLastError();
+    if (a.from_pages <= kCountPages) return launch(kv_move<true>, groups, 256, 0, s, a, parts, copy_parts, rows, pages);
+    const hipError_t e = launch(kv_count, 1, 1024, 0, s, a);
     if (e != hipSuccess) return e;
-    kv_move<false><<<groups, 256, 0, s>>>(a, parts, copy_parts, rows, pages);
-    return hipGetLastError();
+    return launch(kv_move<false>, groups, 256, 0, s, a, parts, copy_parts, rows, pages);
 }
 
 }  // namespace q2_0

@@ -220,22 +220,20 @@ __global__ __launch_bounds__(256) void moe_choose_groups(ChooseGroups a) {
 hipError_t launch_moe_choose_groups(ChooseGroups a, Act xt, bool sigmoid, hipStream_t s) {
     return with_act(xt, [&](auto tag) -> hipError_t {
         using XT = decltype(tag);
-        const dim3 grid((unsigned)((a.n_tokens + 3) / 4));
+        const unsigned groups = (unsigned)((a.n_tokens + 3) / 4);
         auto go = [&](auto pl) {
             constexpr int PL = decltype(pl)::value;
             const int lanes = (int)a.size.d / PL;
             a.group_lanes = a.n_group > 1 && a.size.d % PL == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
             const size_t lds = a.n_group > 1 && !a.group_lanes ? 4 * 64 * PL * sizeof(uint64_t) : 0;
-            if (sigmoid) moe_choose_groups<PL, XT, true><<<grid, 256, lds, s>>>(a);
-            else moe_choose_groups<PL, XT, false><<<grid, 256, lds, s>>>(a);
+            return launch(sigmoid ? moe_choose_groups<PL, XT, true> : moe_choose_groups<PL, XT, false>, groups, 256, lds, s, a);
         };
         // the smallest register tile that holds a row
-        if (a.n_expert <= 64) go(std::integral_constant<int, 1>{});
-        else if (a.n_expert <= 128) go(std::integral_constant<int, 2>{});
-        else if (a.n_expert <= 256) go(std::integral_constant<int, 4>{});
-        else if (a.n_expert <= 512) go(std::integral_constant<int, 8>{});
-        else go(std::integral_constant<int, 16>{});
-        return hipGetLastError();
+        if (a.n_expert <= 64) return go(std::integral_constant<int, 1>{});
+        if (a.n_expert <= 128) return go(std::integral_constant<int, 2>{});
+        if (a.n_expert <= 256) return go(std::integral_constant<int, 4>{});
+        if (a.n_expert <= 512) return go(std::integral_constant<int, 8>{});
+        return go(std::integral_constant<int, 16>{});
     });
 }
 

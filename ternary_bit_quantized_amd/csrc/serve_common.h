@@ -6,6 +6,17 @@
 
 namespace q2_0 {
 
+// ---- launches
+// One launch and its own status: what another call left as the last error is neither taken for this one's (the rest of a
+// call would not run) nor cleared.
+template <typename... A, typename... B>
+inline hipError_t launch(void (*kernel)(A...), unsigned groups, unsigned threads, size_t lds, hipStream_t s, B... args) {
+    return [&](A... exact) {
+        void *at[] = {&exact...};
+        return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(groups), dim3(threads), at, lds, s);
+    }(args...);
+}
+
 // ---- lanes
 // A lane's value (`none` where there is no such lane or the row of 16 is not of ROWS) by the lane moves that need no LDS: CTRL 0x111 ..
 // 0x118 from 1 .. 8 lanes below in the row, 0x142 and 0x143 the last of the row, and of the rows, before.
