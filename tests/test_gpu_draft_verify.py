@@ -345,3 +345,20 @@ def test_same_every_time_and_workspace_of_any_content():
         got = check(target, draft, tokens, n_draft, u, workspace=ws)
         first = first or got
         assert torch.equal(first[0], got[0]) and torch.equal(first[1], got[1])
+
+
+@pytest.mark.parametrize("x", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("t", [1.0, 0.25])
+def test_where_probabilities_end(x, t):
+    """Next to nothing is still taken where the draft gave it less; below 2^-1000 of the largest it is nothing."""
+    import torch
+    ends = {"f32": 690.0, "f16": 690.0, "bf16": 688.0}[x], {"f32": 697.0, "f16": 697.0, "bf16": 700.0}[x]
+    target = torch.zeros(4, 70, device="cuda", dtype=types()[x])    # (two sequences' rows; 1000 ln 2 = 693.1)
+    target[0, 9], target[2, 9] = -ends[0] * t, -ends[1] * t
+    draft = torch.zeros(2, 70, device="cuda", dtype=types()[x])
+    draft[:, 9] = -float("inf")
+    tokens = torch.full((2, 1), 9, dtype=torch.int32, device="cuda")
+    u = torch.full((2, 2), 0.5, device="cuda")
+    _, acc = B.q2_0_draft_verify(target, draft, tokens, torch.ones(2, dtype=torch.int32, device="cuda"), u,
+                                 form=FORM["logits"], temperature=torch.full((2,), t, device="cuda"))
+    assert acc.tolist() == [1, 0]

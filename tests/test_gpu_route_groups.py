@@ -178,3 +178,13 @@ def test_the_chosen_feed_the_expert_layer():
     assert torch.equal(a[0], b[0])
     # exp, sum and quotient in float32 there: a few roundings
     assert torch.all((a[1] - b[1]).abs() <= 8 * 2.0 ** -24 * b[1])
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_one_expert(score):
+    import torch
+    x = torch.tensor([[0.3], [-2.0], [40.0]], device="cuda")
+    ids, w = B.q2_0_moe_route_groups(x, 1, SCORE[score], bias=torch.tensor([0.25], device="cuda"), normalise=False)
+    want = 1 / (1 + np.exp(-x.double().cpu().numpy())) if score == "sigmoid" else np.ones((3, 1))
+    assert ids.tolist() == [[0]] * 3
+    assert np.all(np.abs(w.double().cpu().numpy() - want) <= (2.0 ** -24 + 2.0 ** -45) * want)
