@@ -87,10 +87,15 @@ struct Exps : RowExps {
         big = kBig - (whole ? rint(mk) : 0.0);
         low = (whole ? top : 0.f) - d;
     }
-    // a sum about this part's ref as one about the whole's
+    // A sum about this part's reference as one about the whole's (all.m >= m): the whole number where `off` is 0, else k m
+    // itself.  Where they are of two kinds, the product and the whole number are subtracted in one rounding (of a product of
+    // 2^28 alone it would be 2^-25).
     __device__ __forceinline__ double share_of(double z, const Exps &all) const {
         if (off == 0.f && all.off == 0.f) return __builtin_amdgcn_ldexp(z, (int)fmax(all.big - big, -4000.0));
-        return z * exp2_64(((double)m - (double)all.m) * k);
+        const double lower = off == 0.f         ? -fma((double)all.m, k, big - kBig)
+                             : all.off == 0.f ? fma((double)m, k, all.big - kBig)
+                                              : ((double)m - (double)all.m) * k;
+        return z * exp2_64(lower);
     }
 };
 

@@ -362,3 +362,50 @@ def test_where_probabilities_end(x, t):
     _, acc = B.q2_0_draft_verify(target, draft, tokens, torch.ones(2, dtype=torch.int32, device="cuda"), u,
                                  form=FORM["logits"], temperature=torch.full((2,), t, device="cuda"))
     assert acc.tolist() == [1, 0]
+
+
+def border(sign):
+    """(temperature, x, y): neighbouring float32 values with x > y on either side of |value log2(e) / temperature| = 2^28, where
+    sums change their reference, and the value inside it some 0.45 from a whole number there.  y counts about 2^-16 of x."""
+    for i in range(100000):
+        t = np.float32(1e-8) * (np.float32(1) + np.float32(i) * np.float32(2.0 ** -20))
+        k = 1.4426950408889634 / float(t)
+        inside = np.float32(2.0 ** 28 / k)
+        while abs(float(inside)) * k >= 2.0 ** 28:
+            inside = np.nextafter(inside, np.float32(0))
+        while abs(float(np.nextafter(inside, np.float32(9)))) * k < 2.0 ** 28:
+            inside = np.nextafter(inside, np.float32(9))
+        outside = np.nextafter(inside, np.float32(9))
+        off = float(inside) * k - np.rint(float(inside) * k)
+        if 0.4 < abs(off) < 0.5 and (float(outside) - float(inside)) * k < 20:
+            return (float(t), float(outside), float(inside), off) if sign > 0 else (float(t), -float(inside), -float(outside), -off)
+    raise AssertionError("no such values")
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("where", ["threads", "chunks", "passes", "many chunks"])
+def test_values_on_either_side_of_a_references_border(sign, where):
+    """The largest logit and its lower neighbours in one pass, in other chunks of the row, in two passes of a thread, and in two
+    chunks that one lane joins; the number that decides lies halfway between the probability and what it would be with one
+    side's reference for both."""
+    import torch
+    t, high, low, off = border(sign)
+    v, n, most, at = {"threads": (4096, 3, 1, 7), "chunks": (100000, 3, 1, 7), "passes": (40000, 76, 7, 4096),
+                      "many chunks": (300000, 3, 1, 4100)}[where]
+    row = torch.full((v,), low, dtype=torch.float32)
+    if where == "passes":                     # of 4096 values: 16 of a thread in the first, its next in the second
+        row[:] = -float("inf")
+        row[(torch.arange(4)[:, None] * 1024 + torch.arange(4)).flatten()] = low
+    if where == "many chunks":
+        row[: 65 * 4096] = -float("inf")
+    row[at] = high
+    others = int((row == low).sum()) * 2.0 ** (-(high - low) / t * 1.4426950408889634)
+    p = 1 / (1 + others)
+    # the sum of the part whose reference is a whole number, taken as if it were about its largest value
+    wrong = 1 / (1 + others * 2.0 ** off) if sign > 0 else 1 / (1 + others * 2.0 ** -off)
+    u = np.float32((p + wrong) / 2)
+    assert min(p, wrong) < float(u) < max(p, wrong)
+    target = row.cuda().expand(n * (most + 1), v).contiguous()
+    tokens = torch.full((n, most), at, dtype=torch.int32, device="cuda")
+    uu = torch.full((n, most + 1), float(u), device="cuda")
+    check(target, None, tokens, torch.full((n,), most, dtype=torch.int32, device="cuda"), uu, temp=torch.full((n,), t, device="cuda"))
