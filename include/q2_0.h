@@ -575,8 +575,8 @@ typedef enum {
  * the running sum passes u times the whole.  With max_draft = 0 the call draws a token from each row.
  * A row that is needed and holds NaN or +inf, or nothing but -inf (probabilities: nothing above 0), or has a
  * temperature that is negative or NaN, takes no token and gives -1.
- * Exponentials and sums are in 64 bits, in a fixed order; a token whose exponential is below 2^-1000 of its row's
- * largest has probability 0.  Deterministic run to run.
+ * Exponentials (within 2^-45 of themselves) and sums are in 64 bits, in a fixed order; a token whose exponential is below
+ * 2^-1000 of its row's largest has probability 0.  Deterministic run to run.
  *   workspace / ws_bytes: at least q2_0_draft_verify_workspace_bytes() bytes, 16-byte aligned.  Overwritten.
  * n_vocab <= 2^24, n_seqs <= 2^20, max_draft <= Q2_0_DRAFT_MAX.  Errors: SHAPE (also launches past 2^24
  * workgroups), the n_seqs == 0 no-op, NULL, LAYOUT (ld below n_vocab), UNSUPPORTED (x_type, form), ALIGN, WORKSPACE.

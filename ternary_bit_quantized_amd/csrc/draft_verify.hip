@@ -17,7 +17,7 @@
 // order: results are the same in every run.
 //
 // What bounds it, in a graph.  64 sequences of 4 drafts over 151936 f32 logits, 350 MB: 90 us, of them 60 the
-// statistics, whose 64-bit instructions (13 an exponential) alone take 58 and whose loads alone 43 (6.5 TB/s for the 283 MB that
+// statistics, whose 64-bit instructions (14 an exponential) alone take 58 and whose loads alone 43 (6.5 TB/s for the 283 MB that
 // are needed), and 29 the tile sums (deciding 7.6, two rows' exponentials 11, the token 3).  One sequence of them: 15.2 us,
 // two launches of dependent steps: deciding 4, a tile 1.8, the token 3.  16 sequences of 5 found drafts over 50001 bfloat16
 // logits 18 us; 32 of 3 given probabilities over 32003, 7.8 us.  (The statistics' loads are non-temporal: 64 sequences 76.7 us
@@ -31,17 +31,20 @@ constexpr int kTile = 512;            // tokens of a tile sum (of 1024: one chat
 constexpr int kCountEvery = 32;       // counters of sequences in lines of their own: side by side 400 workgroups wait 2 us for 16
 constexpr int kPass = 4096;           // values of a workgroup's pass: 16 a thread
 
-// 2^r for r in [-1/2, 1/2]: the polynomial of degree 8 that meets it at the Chebyshev points (relative error 1.1e-12).
+// 2^r for r in [-1/2, 1/2]: the polynomial of degree 9 that meets it at the Chebyshev points (relative error 1.9e-14, below
+// 2^-45).  Of degree 8 the error is 1.1e-12 and 64 sequences of 4 drafts take 80.3 us a pass in place of 83.2, but 21 of
+// 6 million two-token rows, whose number is the float32 next to their probability, are decided otherwise than they are defined.
 __device__ __forceinline__ double exp2_frac(double r) {
-    double e = 1.3255224884799127e-06;
-    e = fma(e, r, 1.5310079402383103e-05);
-    e = fma(e, r, 0.00015403455852419016);
-    e = fma(e, r, 0.0013333450568000008);
-    e = fma(e, r, 0.00961812915940262);
-    e = fma(e, r, 0.05550410941205934);
-    e = fma(e, r, 0.2402265069581299);
-    e = fma(e, r, 0.6931471805459335);
-    return fma(e, r, 1.0);
+    double e = 1.020590550210069e-07;
+    e = fma(e, r, 1.3259645241948732e-06);
+    e = fma(e, r, 1.5252672924257465e-05);
+    e = fma(e, r, 0.0001540343375126647);
+    e = fma(e, r, 0.0013333558200796013);
+    e = fma(e, r, 0.00961812919393429);
+    e = fma(e, r, 0.05550410866465166);
+    e = fma(e, r, 0.2402265069564034);
+    e = fma(e, r, 0.6931471805599462);
+    return fma(e, r, 1.0000000000000135);
 }
 
 constexpr double kBig = 6755399441055744.0;      // 1.5 2^52: x + kBig is x rounded to a whole number, in the low bits
@@ -55,7 +58,7 @@ __device__ __forceinline__ double exp2_64(double y) {
 
 // The exponentials of a row (or a part of one) of largest value m: 2^(k x - ref) with ref the whole number next to k m.  ref goes
 // into the exponent: with t = k x + (kBig - ref), one rounding to a whole number, q = t - (kBig - ref) and r = k x - q, a value
-// takes 13 64-bit instructions, and k x is not rounded before its whole part is gone.
+// takes 14 64-bit instructions, and k x is not rounded before its whole part is gone.
 // Where k m is 2^28 and more, float32 has no value 1000 below m in the exponent to stop at (`low` is off by 16 there): x - m takes
 // the place of x (`off`; else 0) with ref 0.  The difference is exact in float32 for x within a factor of 2 of m, and the
 // others are 2^-2^27 and less.

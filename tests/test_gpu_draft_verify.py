@@ -409,3 +409,23 @@ def test_values_on_either_side_of_a_references_border(sign, where):
     tokens = torch.full((n, most), at, dtype=torch.int32, device="cuda")
     uu = torch.full((n, most + 1), float(u), device="cuda")
     check(target, None, tokens, torch.full((n,), most, dtype=torch.int32, device="cuda"), uu, temp=torch.full((n,), t, device="cuda"))
+
+
+def test_choices_that_float32_does_not_decide():
+    """Two-token rows whose probability lies next to the number that decides, closer than a float32 step by some 10^5.  An
+    exponential is within 2^-45 of itself and a probability, a quotient of two by their sum, within 2^-44 and a few roundings
+    of 2^-53: what is further off than 2^-43 has to be decided as the definition says."""
+    import torch
+    x = np.random.default_rng(31).uniform(-8, 8, 6000000).astype(np.float32)
+    p = 1 / (1 + np.exp(-x.astype(np.longdouble)))
+    u = p.astype(np.float32)
+    off = np.abs(p / u.astype(np.longdouble) - 1)
+    some = np.nonzero((off > 2.0 ** -43) & (off < 2.0 ** -40))[0]
+    n = len(some)
+    assert n > 50
+    target = torch.zeros(n, 2, 2, device="cuda")
+    target[:, 0, 1] = torch.from_numpy(x[some]).cuda()
+    tokens, n_draft = torch.ones(n, 1, dtype=torch.int32, device="cuda"), torch.ones(n, dtype=torch.int32, device="cuda")
+    uu = torch.from_numpy(u[some]).cuda()[:, None].repeat(1, 2)
+    _, acc = B.q2_0_draft_verify(target.view(2 * n, 2), None, tokens, n_draft, uu)
+    assert np.array_equal(acc.cpu().numpy() == 1, u[some] < p[some])
