@@ -573,8 +573,10 @@ typedef enum {
  * Place j's token t is taken where u*q(t) < p(t), up to the first that is not.  There the token that follows is drawn
  * from max(p - q, 0) (from p where that leaves less than 2^-32), after the last place from p: the lowest token at which
  * the running sum passes u times the whole.  With max_draft = 0 the call draws a token from each row.
- * A row that is needed and holds NaN or +inf, or nothing but -inf (probabilities: nothing above 0), or has a
- * temperature that is negative or NaN, takes no token and gives -1.
+ * Logits: a row that is needed and holds NaN or +inf, or nothing but -inf, or has a temperature that is negative or
+ * NaN, takes no token and gives -1.  Probabilities are read whole only at the place where the next token is drawn: a
+ * row there that holds NaN or +inf, or nothing above 0, gives -1.  At the places before it the drafted token's two values
+ * alone are read: it is not taken where one of them is NaN or +inf.
  * Exponentials (within 2^-45 of themselves) and sums are in 64 bits, in a fixed order; a token whose exponential is below
  * 2^-1000 of its row's largest has probability 0.  Deterministic run to run.
  *   workspace / ws_bytes: at least q2_0_draft_verify_workspace_bytes() bytes, 16-byte aligned.  Overwritten.

@@ -419,7 +419,7 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
             const double pt = prob<PROBS>(xt, most[lane], k, 1.0), sp = PROBS ? 1.0 : whole[lane];
             const double qt = !a.draft ? 1.0 : prob<PROBS>(xd, most[per + lane], k, 1.0);
             const double sq = !a.draft || PROBS ? 1.0 : whole[per + lane];
-            yes = (double)u * qt * sp < pt * sq;
+            yes = (double)u * qt * sp < pt * sq && (!PROBS || pt < __builtin_inf());   // (given: of NaN neither comparison holds)
         }
     }
     const uint64_t no = __ballot(!yes);                  // (lanes from nd on: not taken)
@@ -480,7 +480,8 @@ struct Tokens {
     __device__ __forceinline__ double left(const DraftVerify &a, const Pick &pick, int kind, int i, int at) const {
         double v = prob<PROBS>(x[i], pick.p, pick.k, pick.inv_p);
         if (kind == kMinus) v -= prob<PROBS>(y[i], pick.q, pick.k, pick.inv_q);
-        const bool out = at >= a.n_vocab || (kind == kOneHot && at == pick.token);
+        // (a given probability that is none stays one, of the token to leave out too)
+        const bool out = at >= a.n_vocab || (kind == kOneHot && at == pick.token && !(PROBS && !(v < __builtin_inf())));
         return out || v <= 0.0 ? 0.0 : v;
     }
 };

@@ -429,3 +429,27 @@ def test_choices_that_float32_does_not_decide():
     uu = torch.from_numpy(u[some]).cuda()[:, None].repeat(1, 2)
     _, acc = B.q2_0_draft_verify(target.view(2 * n, 2), None, tokens, n_draft, uu)
     assert np.array_equal(acc.cpu().numpy() == 1, u[some] < p[some])
+
+
+@pytest.mark.parametrize("x", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("value", ["nan", "inf"])
+@pytest.mark.parametrize("side", ["target", "draft"])
+def test_given_probabilities_of_a_drafted_token(x, value, side):
+    """A drafted token with a value that is none is not taken, whatever its number; of a target like that nothing follows."""
+    import torch
+    target, draft, tokens, n_draft, u = case(6, 3, 700, x, "probs", seed=41)
+    n_draft.fill_(3)
+    draft.copy_(target.reshape(6, 4, 700)[:, :3].reshape(18, 700))       # (each draft is taken where u < 1)
+    tokens.copy_(draft.argmax(1).int().view(6, 3))
+    for s in range(6):
+        rows, per = (target, 4) if side == "target" else (draft, 3)
+        rows[s * per + s % 3, int(tokens[s, s % 3])] = float(value)
+    u[3:] = 0.0
+    out, acc = B.q2_0_draft_verify(target, draft, tokens, n_draft, u, form=FORM["probs"])
+    assert acc.tolist() == [0, 1, 2, 0, 1, 2]
+    for s in range(6):
+        assert out[s, : s % 3].tolist() == tokens[s, : s % 3].tolist()
+        assert side == "draft" or torch.all(out[s, s % 3:] == -1)
+    if side == "target":
+        out, acc = B.q2_0_draft_verify(target, None, tokens, n_draft, torch.zeros_like(u), form=FORM["probs"])
+        assert acc.tolist() == [0, 1, 2, 0, 1, 2] and all(out[s, s % 3] == -1 for s in range(6))
