@@ -547,7 +547,7 @@ int q2_0_moe_route_groups(const void *logits, int x_type, int64_t ld, int64_t n_
 /* What the rows given to q2_0_draft_verify hold. */
 typedef enum {
     Q2_0_DRAFT_LOGITS = 0,   /* logits: probabilities are their softmax over the temperature; -inf masks a token */
-    Q2_0_DRAFT_PROBS = 1     /* probabilities, taken as they are (values below 0 count as 0 where a token is drawn) */
+    Q2_0_DRAFT_PROBS = 1     /* probabilities, taken as they are (values below 0 count as 0) */
 } q2_0_draft_form;
 
 /* Largest number of drafted tokens of a sequence in one call. */

@@ -297,9 +297,10 @@ struct Pick {
 };
 enum { kFixed = 0, kPlain = 1, kOneHot = 2, kMinus = 3 };
 
+// (given probabilities below 0 count as 0; NaN stays)
 template <bool PROBS>
 __device__ __forceinline__ double prob(float x, const RowExps &e, double k, double inv) {
-    return PROBS ? (double)x : e.exact(x, k) * inv;
+    return PROBS ? (double)(x < 0.f ? 0.f : x) : e.exact(x, k) * inv;
 }
 
 // All threads of the workgroup; the result is in `pick` after a barrier.

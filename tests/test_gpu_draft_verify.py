@@ -453,3 +453,31 @@ def test_given_probabilities_of_a_drafted_token(x, value, side):
     if side == "target":
         out, acc = B.q2_0_draft_verify(target, None, tokens, n_draft, torch.zeros_like(u), form=FORM["probs"])
         assert acc.tolist() == [0, 1, 2, 0, 1, 2] and all(out[s, s % 3] == -1 for s in range(6))
+
+
+@pytest.mark.parametrize("x", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("v", [3, 1000, 20011])
+def test_given_probabilities_below_zero(x, v):
+    """They count as 0, the draft's too: such rows give what the same rows with zeros in those places do."""
+    import torch
+    n = 40
+    target, draft, tokens, n_draft, u = case(n, 3, v, x, "probs", seed=v)
+    g = torch.Generator(device="cuda").manual_seed(v)
+    for rows in (target, draft):
+        rows[torch.rand(rows.shape, generator=g, device="cuda") < 0.4] = 0.0
+    draft[:, v - 1] = 0.25                                      # (no draft of nothing)
+    keep = [r.clone() for r in (target, draft)]
+    tokens[::4] = torch.randint(0, v, tokens[::4].shape, generator=g, device="cuda", dtype=torch.int32)
+    want = check(target, draft, tokens, n_draft, u, form="probs")
+    for rows in (target, draft):
+        rows[rows == 0] = -0.75
+        rows[1::3][rows[1::3] < 0] = -float("inf")
+    out, acc = B.q2_0_draft_verify(target, draft, tokens, n_draft, u, form=FORM["probs"])
+    assert torch.equal(acc, want[1]) and torch.equal(out, want[0])
+    # a token of no probability is not taken because the draft's is below 0
+    target, draft = keep
+    target[:, 0], draft[:, 0] = 0.0, -0.5
+    tokens.zero_()
+    n_draft.fill_(3)
+    _, acc = B.q2_0_draft_verify(target, draft, tokens, n_draft, u, form=FORM["probs"])
+    assert torch.all(acc == 0)
