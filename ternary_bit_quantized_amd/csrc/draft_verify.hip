@@ -293,9 +293,11 @@ struct Pick {
     int64_t row_p, row_q;                 // rows of target and draft
     int taken;                            // drafts taken; < 0: the sequence is left out
     int kind;                             // kFixed: `token`; else what is taken from p
-    int token;                            // the next token (kFixed), the token to leave out (kOneHot)
+    int token;                            // the next token (kFixed), the token to leave out (kOneHot); kUnseen: of a given draft
+                                          // row nothing above 0 has been read
 };
 enum { kFixed = 0, kPlain = 1, kOneHot = 2, kMinus = 3 };
+constexpr int kUnseen = -2;
 
 // (given probabilities below 0 count as 0; NaN stays)
 template <bool PROBS>
@@ -426,6 +428,7 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
     const uint64_t no = __ballot(!yes);                  // (lanes from nd on: not taken)
     const int j = (int)__ffsll((unsigned long long)no) - 1;
     const int t = __builtin_amdgcn_readlane(tok, j);
+    const bool seen = !PROBS || (__ballot(xd > 0.f) >> j & 1);
     if (lane == 0) {
         pick.taken = j;
         pick.k = k;
@@ -438,7 +441,7 @@ __device__ void decide(const DraftVerify &a, const DraftPlan &p, int s, Pick &pi
         if (greedy) pick.kind = kFixed, pick.token = arg[j];
         else if (j == nd) pick.kind = kPlain, pick.token = -1;
         else if (!a.draft) pick.kind = kOneHot, pick.token = t;
-        else pick.kind = kMinus, pick.token = -1;
+        else pick.kind = kMinus, pick.token = seen ? -1 : kUnseen;
     }
 }
 
@@ -481,6 +484,7 @@ struct Tokens {
     __device__ __forceinline__ double left(const DraftVerify &a, const Pick &pick, int kind, int i, int at) const {
         double v = prob<PROBS>(x[i], pick.p, pick.k, pick.inv_p);
         if (kind == kMinus) v -= prob<PROBS>(y[i], pick.q, pick.k, pick.inv_q);
+        if (PROBS && kind == kMinus && y[i] == __builtin_inff()) v = nan64();        // (p - inf would be nothing left)
         // (a given probability that is none stays one, of the token to leave out too)
         const bool out = at >= a.n_vocab || (kind == kOneHot && at == pick.token && !(PROBS && !(v < __builtin_inf())));
         return out || v <= 0.0 ? 0.0 : v;
@@ -556,6 +560,22 @@ __device__ __forceinline__ int thread_at(double run, double own, double r, int *
     return who;
 }
 
+// Whether a given draft row holds anything above 0; all threads.  A token that was drawn from the row does, so that this is
+// met only where the drafted token is none, or was not drawn from it.
+template <typename XT>
+__device__ bool any_drawn(const DraftVerify &a, int64_t row_q) {
+    const XT *d = static_cast<const XT *>(a.draft) + row_q * a.ld_draft;
+    bool some = false;
+    for (int e = threadIdx.x; e < a.n_vocab; e += 8 * 256) {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = act_to_f32(d[e + i * 256 < a.n_vocab ? e + i * 256 : a.n_vocab - 1]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) some |= y[i] > 0.f;
+    }
+    return __syncthreads_or(some) != 0;
+}
+
 // The token that follows, and all of a sequence's results: one workgroup, after all tile sums.
 template <typename XT, bool PROBS>
 __device__ __forceinline__ void pick_token(const DraftVerify &a, const DraftPlan &p, int s, const Pick &pick) {
@@ -567,6 +587,7 @@ __device__ __forceinline__ void pick_token(const DraftVerify &a, const DraftPlan
     const int64_t place = (int64_t)s * (a.max_draft + 1) + tid;
     const int drafted = tid < pick.taken ? a.tokens[(int64_t)s * a.max_draft + tid] : -1;
     int kind = pick.kind, result = pick.token;
+    if (PROBS && kind == kMinus && pick.token == kUnseen && !any_drawn<XT>(a, pick.row_q)) kind = kFixed, result = -1;
     // a thread's tiles, next to each other; their sums stay in registers (8 of them: over a million tokens)
     constexpr int kHeld = 8;
     const int each = (p.tiles + 255) / 256, t0 = tid * each, t1 = t0 + each < p.tiles ? t0 + each : p.tiles;

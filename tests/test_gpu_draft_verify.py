@@ -481,3 +481,42 @@ def test_given_probabilities_below_zero(x, v):
     n_draft.fill_(3)
     _, acc = B.q2_0_draft_verify(target, draft, tokens, n_draft, u, form=FORM["probs"])
     assert torch.all(acc == 0)
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("v", [5, 513, 9001])
+def test_given_probabilities_of_the_deciding_rows(x, v):
+    """NaN or +inf anywhere in the rows of the place that decides, and rows with nothing above 0: no token follows."""
+    import torch
+    nan, inf = float("nan"), float("inf")
+    n = 12
+    target, draft, tokens, n_draft, u = case(n, 2, v, x, "probs", seed=v)
+    t, d = target.view(n, 3, v), draft.view(n, 2, v)
+    n_draft.fill_(2)
+    tokens.fill_(v - 1)
+    t[:, :, v - 1], d[:, :, v - 1] = 0.0, 0.5                   # refused at once
+    t[0, 0, 1], t[1, 0, v - 2], t[2, 0, 2] = nan, inf, -inf    # (-inf: below 0, nothing)
+    d[3, 0, 1], d[4, 0, v - 2] = nan, inf
+    t[6, 0] = 0.0
+    d[7, 0] = 0.0
+    d[8, 0], tokens[8, 0] = 0.0, v                              # a token that is none, and a draft of nothing
+    d[9, 0] = -0.25
+    t[10, 0, v - 1] = nan
+    t[11, 0, v - 2], d[11, 0, v - 2] = inf, inf
+    out, acc = B.q2_0_draft_verify(target, draft, tokens, n_draft, u, form=FORM["probs"])
+    assert torch.all(acc == 0) and torch.all(out[:, 1:] == -1)
+    assert [int(o) >= 0 for o in out[:, 0]] == [s in (2, 5) for s in range(n)], out[:, 0]
+    # found drafts: the token itself has what is none
+    t[:, :, v - 1] = 0.0
+    t[0, 0, v - 1], t[1, 0, v - 1], t[2, 0, v - 1], tokens[2, 0] = nan, inf, nan, -1
+    t[3:] = torch.softmax(torch.randn(n - 3, 3, v, device="cuda"), 2).to(t.dtype)
+    out, acc = B.q2_0_draft_verify(target, None, tokens, n_draft, torch.full_like(u, 0.9999), form=FORM["probs"])
+    assert out[:3, 0].tolist() == [-1, -1, -1] and torch.all(acc[:3] == 0) and torch.all(out[3:, 0] >= 0)
+    # rows of places that were passed are not looked through, but for the drafted token's values
+    target, draft, tokens, n_draft, u = case(2, 1, v, x, "probs", seed=v)
+    n_draft.fill_(1)
+    draft.copy_(target.view(2, 2, v)[:, 0])
+    tokens.copy_(draft.argmax(1).int()[:, None])
+    target[0, (int(tokens[0]) + 1) % v], draft[1, (int(tokens[1]) + 1) % v] = nan, inf
+    _, acc = B.q2_0_draft_verify(target, draft, tokens, n_draft, u, form=FORM["probs"])
+    assert acc.tolist() == [1, 1]
