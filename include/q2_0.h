@@ -650,7 +650,8 @@ size_t q2_0_kv_fork_workspace_bytes(int64_t n);
  *   lens   : DEVICE int32 [n_seqs], the lengths so far; set to new_lens.  A sequence with either length outside
  *            [0, table_len*page_size] stays as it is (new_lens -1: leave it).
  *   missing: DEVICE int32 [1]: 0, or how many pages more the growing sequences need than there are: then none of
- *            them grows (their rows, lengths and pages stay), while the others have become shorter.
+ *            them grows (their rows, lengths and pages stay), while the others have become shorter.  Not written
+ *            with n_seqs == 0.
  *   workspace / ws_bytes: at least q2_0_kv_resize_workspace_bytes() bytes, 16-byte aligned.  Overwritten.
  * Table entries outside [0, n_pages) are no pages: nothing is counted or copied for them.  pages->n_pages is the cache's;
  * n_seqs <= 8192.  Errors: NULL (cache, pages), SHAPE, the n_seqs == 0 no-op, NULL, LAYOUT, UNSUPPORTED, ALIGN, WORKSPACE.

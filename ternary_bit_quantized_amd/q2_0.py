@@ -8,6 +8,7 @@ is raised.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -403,22 +404,29 @@ def _stream(stream, dev=None):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _other(stream):
+    """A call's stream as torch has it; None where that is the current one."""
+    import torch
+    handle = _stream(stream)
+    if handle == torch.cuda.current_stream().cuda_stream:
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()      # (0 is the default stream)
+
+
 def _empty(like, shape, dtype, stream, result=True):
     """A new tensor on like's device for a call whose kernels run on `stream`.  Its memory is that stream's: what the
     allocator gives and takes back is in order with the kernels, though another stream is current.  The caller may
     read a result on the current stream and free it then, so the allocator is told of that one too."""
-    if stream is None:
+    other = None if stream is None else _other(stream)
+    if other is None:
         return like.new_empty(shape, dtype=dtype)
     import torch
-    handle, current = _stream(stream), torch.cuda.current_stream()
-    if handle == current.cuda_stream:
-        return like.new_empty(shape, dtype=dtype)
-    if not isinstance(stream, torch.cuda.Stream):       # (a handle of 0 is the default stream)
-        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(other):
         t = like.new_empty(shape, dtype=dtype)
     if result:
-        t.record_stream(current)
+        t.record_stream(torch.cuda.current_stream())
     return t
 
 
@@ -916,8 +924,11 @@ def q2_0_kv_resize(k_cache, v_cache, ref, free, table, lens, new_lens, missing=N
     c = _cache(k_cache, v_cache, dev)
     tp, n_seqs, cols, ldt = _table(table, dev)
     missing, mp = _result(missing, lens, (1,), torch.int32, "missing", stream, dev)
-    if n_seqs == 0:
-        return missing.zero_()
+    if n_seqs == 0:                       # (the library writes nothing then)
+        _stream(stream, dev)
+        other = None if stream is None else _other(stream)
+        with torch.cuda.stream(other) if other is not None else contextlib.nullcontext():
+            return missing.zero_()
     workspace, wsp, wsb = _work(workspace, kv_resize_workspace_bytes(n_seqs, c.n_pages), lens, stream, dev)
     _check(kv_resize_raw(c, _pages(ref, free, c.n_pages, dev), tp, n_seqs, cols, ldt,
                          _dense(lens, torch.int32, (n_seqs,), "lens", dev),

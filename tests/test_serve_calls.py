@@ -101,3 +101,26 @@ def test_no_sequences(fakes):  # noqa: F811
 def test_a_new_pool():
     ref, free = B.q2_0_kv_pages(70, device="cpu")
     assert ref.dtype == free.dtype == torch.int32 and ref.tolist() == [0] * 70 and free.tolist() == [-1] * 3
+
+
+@pytest.mark.parametrize("stream", [None, FakeStream(CURRENT), FakeStream(OTHER), OTHER])
+@pytest.mark.parametrize("given", [False, True])
+def test_no_sequences_on_a_stream(stream, given, fakes, monkeypatch):  # noqa: F811
+    """What is missing is written on the call's stream, where its reader waits for it."""
+    written = []
+    zero = torch.Tensor.zero_
+
+    def noted(t):
+        written.append(torch.cuda.current_stream().cuda_stream)
+        return zero(t)
+
+    monkeypatch.setattr(OnGpu, "zero_", noted, raising=False)
+    call, t, _ = arguments("resize")
+    missing = torch.ones_like(t["missing"]).as_subclass(OnGpu) if given else None
+    got = call(**dict(t, table=int32(0, 6), lens=int32(0), new_lens=int32(0), missing=missing), stream=stream)
+    assert got.item() == 0 and (got is missing or not given) and not fakes
+    assert written == [OTHER if stream == OTHER or getattr(stream, "cuda_stream", None) == OTHER else CURRENT]
+    with pytest.raises(ValueError):
+        other = FakeStream(5)
+        other.device_index = 1
+        call(**dict(t, table=int32(0, 6), lens=int32(0), new_lens=int32(0), missing=missing), stream=other)
