@@ -598,8 +598,8 @@ size_t q2_0_draft_verify_workspace_bytes(int64_t n_seqs, int64_t max_draft, int6
  *   free   : one bit a page, bit i % 32 of word i / 32: the page may be taken.  Bits past n_pages are ignored.
  * A new pool has ref 0 and every bit set.  A page with ref 0 and its bit clear is the caller's.
  * These calls change tables, lengths, counts and bits in place: those of one pool belong on one stream.  Results
- * do not depend on timing.  n_pages and table_len <= 2^30, page_size and n_kv so that a page's 16-byte
- * vectors stay below 2^31, launches below 2^24 workgroups: SHAPE otherwise.
+ * do not depend on timing.  n_pages and table_len <= 2^30, page_size and n_kv so that a page has at most 2^31 - 2048
+ * vectors of 16 bytes, launches below 2^24 workgroups: SHAPE otherwise.
  */
 typedef struct {
     int32_t *ref;

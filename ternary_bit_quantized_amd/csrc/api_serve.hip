@@ -20,10 +20,13 @@ bool in(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
 
 bool known_act(int t) { return t == Q2_0_ACT_F32 || t == Q2_0_ACT_F16 || t == Q2_0_ACT_BF16; }
 
-// 16-byte vectors of a page's keys and values: 2 * n_kv * page_size * head_dim / 8
+// 16-byte vectors of a page's keys and values: 2 * n_kv * page_size * head_dim / 8.  A copy's threads count up to the next
+// multiple of 2048 of them in 32 bits.
+constexpr int64_t kMaxVecs = kMaxInt - 2047;
+
 bool cache_shape_ok(const q2_0_kv_cache &c) {
     return in(c.n_pages, 0, kMaxPages) && in(c.page_size, 1, kMaxInt) && in(c.n_kv, 1, 4096) && in(c.head_dim, 1, 4096) &&
-           c.page_size <= kMaxInt / (c.n_kv * ((c.head_dim + 7) / 8) * 2);
+           c.page_size <= kMaxVecs / (c.n_kv * ((c.head_dim + 7) / 8) * 2);
 }
 
 int check_cache(const q2_0_kv_cache &c) {

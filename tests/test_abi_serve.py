@@ -193,6 +193,17 @@ def test_compact():
     assert compact(ws_bytes=need - 1) == compact(workspace=0) == compact(workspace=P + 8) == B.Q2_0_ERR_WORKSPACE
     assert B.kv_compact_workspace_bytes(0) == B.kv_compact_workspace_bytes(-1) == 0
 
+@pytest.mark.parametrize("call", [lambda c: copy(to=c, frm=c, n=1, src=0), lambda c: resize(c, pages(n_pages=1), table=0),
+                                  lambda c: compact(to=c, tp=pages(Q, Q, 1), frm=c, fp=pages(n_pages=1), table=0)])
+def test_pages_of_nearly_2_31_vectors(call):
+    """A thread's last vectors lie up to 2047 past a page's: all of them have to be 32-bit numbers."""
+    for kw, vectors in ((dict(n_kv=1, head_dim=64), 16), (dict(n_kv=8, head_dim=128), 256), (dict(n_kv=3, head_dim=256), 192)):
+        most = (2 ** 31 - 2048) // vectors
+        assert call(cache(n_pages=1, page_size=most + 1, token_stride=256, **kw)) == B.Q2_0_ERR_SHAPE, kw
+        assert call(cache(n_pages=1, page_size=(2 ** 31 - 1) // vectors, token_stride=256, **kw)) == B.Q2_0_ERR_SHAPE, kw
+    assert copy(to=cache(n_pages=1, page_size=most, token_stride=256, **kw), frm=cache(n_pages=1, page_size=most, token_stride=256, **kw),
+                n=1, src=0) == B.Q2_0_ERR_NULL
+
 
 def test_under_asan_and_ubsan():
     """These tests once more on a build whose host code carries the sanitizers."""
