@@ -62,7 +62,9 @@ class Server:
         B.q2_0_kv_append(self.k, self.v, self.table, torch.zeros_like(pos), pos, k, v, rope=self.rope)
         B.q2_0_kv_fork(self.ref, self.table, self.page, self.lens, torch.zeros_like(self.seq[1:]), self.seq[1:])
         self.cur.copy_(ids[n:])
-        self.follow[:, ids[:n].long()] = ids[1:]
+        # a token may stand in it many times: the last place counts
+        last = torch.full((self.vocab,), -1, device="cuda").scatter_reduce_(0, ids[:n].long(), pos.long(), "amax")
+        self.follow.copy_(torch.where(last >= 0, ids[last + 1], self.follow))
 
     def draft(self):
         """(tokens (n, drafts), how many of them): the answer's own text, as far as it goes on."""

@@ -138,6 +138,20 @@ def test_captured_step():
         assert all(torch.equal(a, b) for a, b in zip((out, taken, s.lens, s.table, s.free), want[i])), i
     pages_add_up(s)
 
+def test_a_prompt_that_goes_on_differently():
+    """Drafts come from what followed a token last in the prompt, however often it stands there."""
+    import torch
+    E = example()
+    for seed in range(4):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        ids = torch.randint(0, [2, 7, 40, 300][seed], (190,), generator=g, device="cuda", dtype=torch.int32)
+        s = E.Server(3, 200, 2, [0.0] * 3, seed=seed, **SIZES)
+        s.prompt(ids)
+        text, want = ids.tolist(), [-1] * s.vocab
+        for a, b in zip(text, text[1:]):
+            want[a] = b
+        assert s.follow.tolist() == [want] * 3
+
 
 def test_example_runs(monkeypatch, capsys):
     E = example()
