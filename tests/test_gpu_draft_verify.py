@@ -520,3 +520,21 @@ def test_given_probabilities_of_the_deciding_rows(x, v):
     target[0, (int(tokens[0]) + 1) % v], draft[1, (int(tokens[1]) + 1) % v] = nan, inf
     _, acc = B.q2_0_draft_verify(target, draft, tokens, n_draft, u, form=FORM["probs"])
     assert acc.tolist() == [1, 1]
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+def test_infinite_temperatures(x):
+    """Every token that is not masked alike, up to the documented end of temperatures."""
+    import torch
+    target, draft, tokens, n_draft, u = case(12, 2, 3001, x, seed=43)
+    target.view(12, 3, 3001)[:, :, 100:] = -float("inf")
+    draft.view(12, 2, 3001)[::2, :, 50:] = -float("inf")
+    tokens.remainder_(120)
+    temp = torch.full((12,), float("inf"), device="cuda")
+    temp[::3] = 1e30
+    for d in (draft, None):
+        out, _ = check(target, d, tokens, n_draft, u, temp=temp)
+        assert int(out.max()) < 100
+    u[:, 2] = (torch.arange(12, device="cuda") * 8 + 0.5) / 100
+    out, _ = check(target, None, tokens, torch.zeros_like(n_draft), u, temp=temp)
+    assert out[:, 0].tolist() == [8 * s for s in range(12)]
