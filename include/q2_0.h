@@ -577,8 +577,8 @@ typedef enum {
  * NaN, takes no token and gives -1.  Probabilities are read whole only at the place where the next token is drawn: a
  * row there that holds NaN or +inf, or nothing above 0, gives -1.  At the places before it the drafted token's two values
  * alone are read: it is not taken where one of them is NaN or +inf.
- * Exponentials (within 2^-45 of themselves) and sums are in 64 bits, in a fixed order; a token whose exponential is below
- * 2^-1000 of its row's largest has probability 0.  Deterministic run to run.
+ * Exponentials and sums are in 64 bits, in a fixed order: e^-y is within 2^-45 + y 2^-52 of itself, and a token for which it is
+ * below 2^-1000 (of its row's largest) has probability 0.  Deterministic run to run.
  *   workspace / ws_bytes: at least q2_0_draft_verify_workspace_bytes() bytes, 16-byte aligned.  Overwritten.
  * n_vocab <= 2^24, n_seqs <= 2^20, max_draft <= Q2_0_DRAFT_MAX.  Errors: SHAPE (also launches past 2^24
  * workgroups), the n_seqs == 0 no-op, NULL, LAYOUT (ld below n_vocab), UNSUPPORTED (x_type, form), ALIGN, WORKSPACE.

@@ -16,12 +16,15 @@
 // Given probabilities need no statistics, and find the token in a launch of its own (draft_pick).  All sums are in a fixed
 // order: results are the same in every run.
 //
-// What bounds it, in a graph.  64 sequences of 4 drafts over 151936 f32 logits, 350 MB: 90 us, of them 60 the
-// statistics, whose 64-bit instructions (14 an exponential) alone take 58 and whose loads alone 43 (6.5 TB/s for the 283 MB that
-// are needed), and 29 the tile sums (deciding 7.6, two rows' exponentials 11, the token 3).  One sequence of them: 15.2 us,
-// two launches of dependent steps: deciding 4, a tile 1.8, the token 3.  16 sequences of 5 found drafts over 50001 bfloat16
-// logits 18 us; 32 of 3 given probabilities over 32003, 7.8 us.  (The statistics' loads are non-temporal: 64 sequences 76.7 us
-// a pass with other work between, 80.5 with plain ones.)
+// What bounds it, in a graph.  64 sequences of 4 drafts over 151936 f32 logits, 350 MB: 84 to 91 us.  57 to 62 of them are the
+// statistics, by counters: the vector units are busy for 37 of 57 us (14 64-bit instructions an exponential, 22.6 million of
+// all kinds on 1024 SIMDs), with 4.2 waves a SIMD on average, which spend 44 % of their time waiting to issue and 35 %
+// at waits (their loads alone take 43 us: 6.5 TB/s for the 283 MB that are needed).  29 to 31 are the tile sums (deciding 7.6,
+// two rows' exponentials 11, the token 3).  The same logits in bfloat16: 88 us, since the instructions are the same (the
+// statistics 53) and the tile sums' waves (39) are at waits 2.4 times as long.  One sequence of f32: 15.4 us, two launches of
+// dependent steps: deciding 4, a tile 1.8, the token 3.  16 sequences of 5 found drafts over 50001 bfloat16 logits 18.5 us; 32
+// of 3 given probabilities over 32003, 8.0 us.  (The statistics' loads are non-temporal: 64 sequences took 76.7 us a pass with
+// other work between, 80.5 with plain ones.)
 #include "serve_common.h"
 
 namespace q2_0 {
